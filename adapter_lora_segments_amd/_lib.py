@@ -14,6 +14,7 @@ DTYPES = {"fp32": 0, "bf16": 1}
 W0_LAYOUTS = {"kn": 0, "nk": 1, "both": 2}
 W0_FORMATS = {"bf16": 0, "mxfp8": 1, "mxfp4": 2}
 ACT_FORMATS = {"bf16": 0, "mxfp8": 1}
+EXPERT_ACT_FORMATS = {"bf16": 0, "mxfp4": 2}
 WG_OVERLAP = {"auto": 0, "side": 1, "after": 2}
 
 TABLES = ["rpad", "zoff", "roff", "group_first_adapter", "nb", "nb_start", "chunks", "chunk_start",
@@ -30,7 +31,9 @@ KERNELS = ["shrink", "gemm_fwd", "dz", "token_reduce", "reduce", "gemm_dx", "pre
 EXPORTS = ["mlora_plan", "mlora_plan_from_ids", "mlora_plan_multi", "mlora_plan_multi_from_ids", "mlora_plan_destroy", "mlora_plan_get_info", "mlora_plan_export",
            "mlora_plan_upload", "mlora_forward", "mlora_backward", "mlora_adamw_step", "mlora_profile_enable",
            "mlora_profile_read", "mlora_device_check", "mlora_status_string", "mlora_last_error",
-           "mlora_version", "mlora_base_transpose", "mlora_forward_noalloc"]
+           "mlora_version", "mlora_base_transpose", "mlora_forward_noalloc", "mlora_group_rows_workspace",
+           "mlora_group_rows", "mlora_expert_workspace", "mlora_expert_forward", "mlora_expert_backward",
+           "mlora_microscale_quantize"]
 
 
 class PlanOpts(ctypes.Structure):
@@ -59,6 +62,14 @@ class AdamwHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
                 ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("step", ctypes.c_int32),
                 ("max_grad_norm", ctypes.c_float)]
+
+
+class ExpertShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
+                ("n_experts", ctypes.c_int32), ("dtype", ctypes.c_int32), ("w_layout", ctypes.c_int32),
+                ("w_format", ctypes.c_int32), ("act_format", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("x_by_order", ctypes.c_int32), ("y_by_order", ctypes.c_int32),
+                ("grad_accumulate", ctypes.c_int32)]
 
 
 class MloraError(RuntimeError):
@@ -116,6 +127,18 @@ def lib() -> ctypes.CDLL:
     L.mlora_backward.restype = i32
     L.mlora_adamw_step.argtypes = [vp] + [vp] * 11 + [i32, vp, sz, vp]
     L.mlora_adamw_step.restype = i32
+    L.mlora_group_rows_workspace.argtypes = [i64, i32, ctypes.POINTER(i64)]
+    L.mlora_group_rows_workspace.restype = i32
+    L.mlora_group_rows.argtypes = [vp, i64, i32, vp, vp, vp, sz, vp]
+    L.mlora_group_rows.restype = i32
+    L.mlora_expert_workspace.argtypes = [ctypes.POINTER(ExpertShape), ctypes.POINTER(i64)]
+    L.mlora_expert_workspace.restype = i32
+    L.mlora_expert_forward.argtypes = [ctypes.POINTER(ExpertShape), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mlora_expert_forward.restype = i32
+    L.mlora_expert_backward.argtypes = [ctypes.POINTER(ExpertShape), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mlora_expert_backward.restype = i32
+    L.mlora_microscale_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
+    L.mlora_microscale_quantize.restype = i32
     L.mlora_profile_enable.argtypes = [vp, i32]
     L.mlora_profile_enable.restype = i32
     L.mlora_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]

@@ -474,3 +474,247 @@ class AdamW:
                          self.vA_ptrs, self.mB_ptrs, self.vB_ptrs, self.copies[0], self.copies[1],
                          L.ws, stream, clip_grads)
         return hp
+
+
+# ---- grouped expert products, row grouping, MXFP4 quantization ----
+
+def _launch(tensors, stream, call):
+    """Run ``call(stream handle)`` on the device that holds ``tensors`` (None
+    entries skipped): on ``stream``, which must be of that device, or on that
+    device's current stream."""
+    torch = _torch()
+    index = None
+    for t in tensors:
+        if t is None:
+            continue
+        i = t.device.index
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError(f"tensors are on different devices: cuda:{index} and cuda:{i}")
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    s = stream if stream is not None else torch.cuda.current_stream(index)
+    if index == torch.cuda.current_device():
+        check(call(ctypes.c_void_p(s.cuda_stream)))
+    else:
+        with torch.cuda.device(index):
+            check(call(ctypes.c_void_p(s.cuda_stream)))
+
+
+def group_rows_workspace(rows: int, n_groups: int) -> int:
+    """Workspace bytes of mlora_group_rows for up to ``rows`` rows."""
+    n = ctypes.c_int64()
+    check(lib().mlora_group_rows_workspace(rows, n_groups, ctypes.byref(n)))
+    return n.value
+
+
+def mlora_group_rows(ids, n_groups: int, offsets, order, ws=None, stream=None):
+    """Stable grouping of rows by int32 ``ids`` (any value outside
+    [0, n_groups): no group): offsets [n_groups + 1] and order [rows] int32;
+    positions behind the last group hold -1."""
+    torch = _torch()
+    _check_t(ids, "ids", (ids.numel(),), torch.int32)
+    _check_t(offsets, "offsets", (n_groups + 1,), torch.int32)
+    _check_t(order, "order", (ids.numel(),), torch.int32)
+    if ws is not None:
+        _check_t(ws, "ws", None, torch.uint8)
+    _launch((ids, offsets, order, ws), stream,
+            lambda s: lib().mlora_group_rows(_p(ids), ids.numel(), n_groups, _p(offsets), _p(order), _p(ws),
+                                             0 if ws is None else ws.numel(), s))
+    return offsets, order
+
+
+class RowGroups:
+    """Buffers of mlora_group_rows for up to ``max_rows`` rows: ``group(ids)``
+    returns (offsets, order), which the next call overwrites."""
+
+    def __init__(self, max_rows: int, n_groups: int, device="cuda"):
+        torch = _torch()
+        need = group_rows_workspace(max_rows, n_groups)
+        self.max_rows, self.n_groups = max_rows, n_groups
+        self.offsets = torch.empty(n_groups + 1, dtype=torch.int32, device=device)
+        self.order = torch.empty(max_rows, dtype=torch.int32, device=device)
+        self.ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+    def group(self, ids, stream=None):
+        if ids.numel() > self.max_rows:
+            raise ValueError(f"{ids.numel()} ids for buffers of {self.max_rows} rows")
+        return mlora_group_rows(ids, self.n_groups, self.offsets, self.order[:ids.numel()], self.ws, stream)
+
+
+class ExpertShape:
+    """Sizes, types and layouts of a grouped expert product
+    (``mlora_expert_shape``).  ``rows`` is the most rows of a call; ``src_rows``
+    is the number of rows X then has."""
+
+    def __init__(self, rows: int, n_experts: int, d_in: int, d_out: int, dtype: str = "bf16", w_layout: str = "kn",
+                 w_format: str = "bf16", act_format: str = "bf16", top_k: int = 1, x_order: bool = False,
+                 y_order: bool = False, grad_accumulate: bool = False):
+        if w_layout not in ("kn", "nk"):
+            raise ValueError(f"w_layout must be 'kn' or 'nk', got {w_layout!r}")
+        if w_format not in ("bf16", "mxfp4"):
+            raise ValueError(f"w_format must be 'bf16' (the dtype's own values) or 'mxfp4', got {w_format!r}")
+        if act_format not in _lib.EXPERT_ACT_FORMATS:
+            raise ValueError(f"act_format must be 'bf16' or 'mxfp4', got {act_format!r}")
+        self.rows, self.n_experts, self.d_in, self.d_out = int(rows), int(n_experts), int(d_in), int(d_out)
+        self.dtype, self.w_layout, self.w_format, self.act_format = dtype, w_layout, w_format, act_format
+        self.top_k, self.x_order, self.y_order = int(top_k), bool(x_order), bool(y_order)
+        self.grad_accumulate = bool(grad_accumulate)
+        self.workspace_bytes = 0
+        n = ctypes.c_int64()
+        check(lib().mlora_expert_workspace(ctypes.byref(self.struct(self.rows)), ctypes.byref(n)))
+        self.workspace_bytes = n.value
+
+    def struct(self, rows: int):
+        return _lib.ExpertShape(rows, self.d_in, self.d_out, self.n_experts, _lib.DTYPES[self.dtype],
+                                _lib.W0_LAYOUTS[self.w_layout], _lib.W0_FORMATS[self.w_format],
+                                _lib.EXPERT_ACT_FORMATS[self.act_format], self.top_k, int(self.x_order),
+                                int(self.y_order), int(self.grad_accumulate))
+
+    def src_rows(self, rows: int) -> int:
+        return rows // self.top_k if self.x_order else rows
+
+    @property
+    def w_shape(self):
+        """Shape of all experts' weights (MXFP4: of the packed buffer)."""
+        if self.w_format == "mxfp4":
+            return (microscale_bytes(self.n_experts * self.d_out, self.d_in),)
+        return (self.n_experts,) + ((self.d_in, self.d_out) if self.w_layout == "kn" else (self.d_out, self.d_in))
+
+    def alloc_workspace(self, device="cuda"):
+        torch = _torch()
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device) if self.workspace_bytes else None
+
+
+def _check_expert(shape: ExpertShape, rows: int, W, offsets, order, ws):
+    torch = _torch()
+    if rows > shape.rows:
+        raise ValueError(f"{rows} rows for a shape of at most {shape.rows}")
+    if W is not None:
+        _check_t(W, "W", shape.w_shape, torch.uint8 if shape.w_format == "mxfp4" else _dt(shape))
+    if offsets is not None:
+        _check_t(offsets, "offsets", (shape.n_experts + 1,), torch.int32)
+    if order is not None:
+        _check_t(order, "order", (rows,), torch.int32)
+    if ws is not None:
+        _check_t(ws, "ws", None, torch.uint8)
+
+
+def mlora_expert_forward(shape: ExpertShape, X, W, offsets, order, Y, ws=None, stream=None):
+    """Y[y(s)] = X[x(s)] W_e for every expert e and its grouped rows s (rows
+    of Y that belong to no group are left as they were)."""
+    rows = Y.shape[0]
+    dt = _dt(shape)
+    _check_t(X, "X", (shape.src_rows(rows), shape.d_in), dt)
+    _check_t(Y, "Y", (rows, shape.d_out), dt)
+    if W is None:
+        raise ValueError("W is required")
+    _check_expert(shape, rows, W, offsets, order, ws)
+    c = shape.struct(rows)
+    _launch((X, W, offsets, order, Y, ws), stream,
+            lambda s: lib().mlora_expert_forward(ctypes.byref(c), _p(X), _p(W), _p(offsets), _p(order), _p(Y),
+                                                 _p(ws), 0 if ws is None else ws.numel(), s))
+    return Y
+
+
+def mlora_expert_backward(shape: ExpertShape, dY, X, W, offsets, order, dX, dW, ws=None, stream=None):
+    """dX[p(s)] = dY[y(s)] W_e^T and dW_e = sum_s X[x(s)]^T dY[y(s)] (fp32);
+    dX or dW may be None to skip it."""
+    torch = _torch()
+    rows = dY.shape[0]
+    dt = _dt(shape)
+    _check_t(dY, "dY", (rows, shape.d_out), dt)
+    if X is not None:
+        _check_t(X, "X", (shape.src_rows(rows), shape.d_in), dt)
+    if dX is not None:
+        _check_t(dX, "dX", (rows, shape.d_in), dt)
+    if dW is not None:
+        _check_t(dW, "dW", shape.w_shape, torch.float32)
+    _check_expert(shape, rows, W, offsets, order, ws)
+    c = shape.struct(rows)
+    _launch((dY, X, W, offsets, order, dX, dW, ws), stream,
+            lambda s: lib().mlora_expert_backward(ctypes.byref(c), _p(dY), _p(X), _p(W), _p(offsets), _p(order),
+                                                  _p(dX), _p(dW), _p(ws), 0 if ws is None else ws.numel(), s))
+    return dX
+
+
+class ExpertLinear:
+    """A base weight per expert with its buffers: ``W`` holds all experts'
+    weights in the layout and format given ([n_experts][d_in][d_out] for "kn",
+    [n_experts][d_out][d_in] for "nk", the packed buffer of
+    ``mlora_microscale_quantize`` for "mxfp4").  ``forward`` and ``backward``
+    take up to ``max_rows`` grouped rows; ``dW`` holds the fp32 gradients of
+    the last backward (with grad_accumulate, their sum since it was zeroed)."""
+
+    def __init__(self, W, n_experts: int, d_in: int, d_out: int, max_rows: int, **options):
+        torch = _torch()
+        self.shape = ExpertShape(max_rows, n_experts, d_in, d_out, **options)
+        _check_expert(self.shape, 0, W, None, None, None)
+        self.W = W
+        self.ws = self.shape.alloc_workspace(W.device)
+        self.dW = None
+        if self.shape.grad_accumulate and self.shape.w_format == "bf16":
+            self.dW = torch.zeros(self.shape.w_shape, dtype=torch.float32, device=W.device)
+
+    def forward(self, X, offsets=None, order=None, Y=None, stream=None):
+        """Y [rows][d_out]; a Y made here is zero in rows of no group when an
+        order names the rows."""
+        torch = _torch()
+        sh = self.shape
+        if Y is None:
+            rows = X.shape[0] * sh.top_k if sh.x_order else X.shape[0]
+            make = torch.zeros if sh.y_order else torch.empty
+            Y = make((rows, sh.d_out), dtype=X.dtype, device=X.device)
+        return mlora_expert_forward(sh, X, self.W, offsets, order, Y, self.ws, stream)
+
+    def backward(self, dY, X, offsets=None, order=None, dX=None, want_dx=True, want_dw=True, stream=None):
+        """dX [rows][d_in]; ``self.dW`` unless the weight is frozen (MXFP4) or
+        want_dw is False.  A dX made here is zero in rows of no group when an
+        order names the rows."""
+        torch = _torch()
+        sh = self.shape
+        if want_dx and dX is None:
+            make = torch.zeros if sh.x_order else torch.empty
+            dX = make((dY.shape[0], sh.d_in), dtype=dY.dtype, device=dY.device)
+        want_dw = want_dw and sh.w_format == "bf16"
+        if want_dw and self.dW is None:
+            self.dW = torch.empty(sh.w_shape, dtype=torch.float32, device=self.W.device)
+        mlora_expert_backward(sh, dY, X, self.W, offsets, order, dX if want_dx else None,
+                              self.dW if want_dw else None, self.ws, stream)
+        return dX if want_dx else None
+
+
+def microscale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the packed MXFP4 buffer of a [rows][cols] matrix."""
+    return rows * cols // 2 + rows * cols // 32
+
+
+def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", stream=None):
+    """X [rows][cols] (bf16 or fp32, rows contiguous) to MXFP4: q, the packed
+    buffer of codes and scales, made if None.  along: "cols", blocks of 32
+    along a row (a [d_out][d_in] weight or activations), or "rows", blocks down
+    a column (a [d_in][d_out] weight).  values: None or a dense tensor like X
+    for the decoded elements."""
+    torch = _torch()
+    if along not in ("cols", "rows"):
+        raise ValueError(f"along must be 'cols' or 'rows', got {along!r}")
+    if X.dim() != 2 or X.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("X must be a 2-d bf16 or fp32 tensor")
+    if not X.is_cuda:
+        raise ValueError("X must be a device tensor")
+    rows, cols = X.shape
+    if X.stride(1) != 1 and cols > 1:
+        raise ValueError("X's rows must be contiguous")
+    n = microscale_bytes(rows, cols)
+    if q is None:
+        q = torch.empty(n, dtype=torch.uint8, device=X.device)
+    _check_t(q, "q", (n,), torch.uint8)
+    if values is not None:
+        _check_t(values, "values", (rows, cols), X.dtype)
+    dt = _lib.DTYPES["bf16" if X.dtype == torch.bfloat16 else "fp32"]
+    ld = X.stride(0) if rows > 1 else cols
+    _launch((X, q, values), stream,
+            lambda s: lib().mlora_microscale_quantize(_p(X), dt, rows, cols, ld, 1 if along == "rows" else 0, _p(q),
+                                                      _p(values), s))
+    return q

@@ -227,6 +227,11 @@ mlora_status decode_base(mlora_plan_s* p, const void* W0, uint16_t* w0deq, bool 
   });
 }
 
+// The message of the calls in other files.
+namespace mlora {
+void set_last_error(const std::string& msg) { g_err = msg; }
+}  // namespace mlora
+
 extern "C" {
 
 const char* mlora_version(void) { return "mlora 0.1 gfx950"; }

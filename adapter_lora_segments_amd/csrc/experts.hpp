@@ -1,0 +1,94 @@
+// Launch interface of the grouped expert products, the row grouping and the
+// MXFP4 quantizer (host side).  As in kernels.hpp, launchers check nothing:
+// the C interface validates shapes and sizes before calling.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <string>
+
+#include "../../include/mlora.h"
+
+namespace mlora {
+
+// The message mlora_last_error() returns on this thread (api.cpp).
+void set_last_error(const std::string& msg);
+
+// ---------------- row grouping ----------------
+
+// Rows per workgroup of the two-kernel form and its number of workgroups:
+// at most kGroupMaxParts parts, so every workgroup can sum the parts' counts
+// before its own by itself.
+constexpr int64_t kGroupMinPart = 4096;
+constexpr int64_t kGroupMaxParts = 256;
+// Rows up to which one workgroup does everything in one launch.
+constexpr int64_t kGroupOneLaunch = 8192;
+inline int64_t group_part_rows(int64_t rows) {
+  const int64_t even = (rows + kGroupMaxParts - 1) / kGroupMaxParts;
+  return even > kGroupMinPart ? (even + 1023) / 1024 * 1024 : kGroupMinPart;
+}
+// counts: [parts][n_groups] ints of workspace (unused by the one-launch form).
+void launch_group_rows(const int32_t* ids, int64_t rows, int32_t n_groups, int32_t* offsets, int32_t* order,
+                       int32_t* counts, hipStream_t s);
+
+// ---------------- MXFP4 quantizer ----------------
+
+// codes [rows][cols / 2]; scales [rows][cols / 32], or [cols][rows / 32] with
+// down; values NULL or [rows][cols] of X's type.
+void launch_quant_mx4(bool f32, bool down, const void* X, int64_t rows, int64_t cols, int64_t ld, uint8_t* codes,
+                      uint8_t* scales, void* values, hipStream_t s);
+
+// ---------------- grouped products ----------------
+
+// Unsigned division of values below 2^31 by a fixed divisor: n / d =
+// umulhi(n, mul) >> shift (d > 1), n for d = 1 (mul = 0).
+struct DivBy {
+  uint32_t mul;
+  int32_t shift;
+};
+inline DivBy div_by(int32_t d) {
+  if (d <= 1) return {0u, 0};
+  int l = 0;
+  while ((1 << l) < d) ++l;                                  // ceil(log2 d)
+  const uint64_t m = ((uint64_t)1 << (31 + l)) / (uint64_t)d + 1;
+  return {(uint32_t)m, l - 1};
+}
+
+// How the rows of an operand or output lie: grouped row s at row s, or at
+// order[s] / top_k.
+struct RowMap {
+  int32_t by_order;
+  DivBy div;
+};
+
+// One product over all experts.
+//   rows form (forward, dX): C[rc(s)][n] = sum_k A[ra(s)][k] B_e(k, n)
+//   dW form: C_e[m][n] = sum_s A[ra(s)][m] B[rb(s)][n] (fp32 C)
+struct ExpertArgs {
+  const uint8_t* A;
+  const uint8_t* B;
+  int64_t lda, ldb, ldc;        // row strides in elements of the operand's format
+  int64_t b_expert;             // bytes from one expert's B to the next (rows form)
+  int64_t c_expert;             // elements from one expert's C to the next (dW form)
+  void* C;
+  RowMap ma, mb, mc;
+  const int32_t* offsets;       // NULL: one expert over all rows
+  const int32_t* order;
+  int32_t rows, n_experts;
+  int32_t M, N, K;              // dW form: M x N outputs per expert; rows form: N, K
+  const uint8_t* a_scale;       // MXFP4 scale codes of A [..][K / 32], B [N][K / 32] per expert
+  const uint8_t* b_scale;
+  int32_t accumulate;           // dW form: add to C
+};
+
+enum class ExpertForm { kBf16, kF32, kW4A16, kW4A4 };
+
+// rows form; b_kc: B_e(k, n) at B[n * ldb + k], else at B[k * ldb + n]
+// (MXFP4 weights are always k-contiguous).
+void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStream_t s);
+// The same for few rows per group: 16 row_blocks (1 or 2) rows per tile.
+void launch_expert_few(ExpertForm form, bool b_kc, int row_blocks, const ExpertArgs& a, hipStream_t s);
+// dW form, bf16 or fp32 operands, both n-contiguous.
+void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s);
+
+}  // namespace mlora

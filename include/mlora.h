@@ -95,7 +95,11 @@ typedef enum {
 typedef enum { MLORA_FP32 = 0, MLORA_BF16 = 1 } mlora_dtype;
 typedef enum { MLORA_W0_KN = 0, MLORA_W0_NK = 1, MLORA_W0_BOTH = 2 } mlora_w0_layout;
 typedef enum { MLORA_W0_BF16 = 0, MLORA_W0_MXFP8 = 1, MLORA_W0_MXFP4 = 2 } mlora_w0_format;
-typedef enum { MLORA_ACT_BF16 = 0, MLORA_ACT_MXFP8 = 1 } mlora_act_format;
+typedef enum {
+  MLORA_ACT_BF16 = 0,
+  MLORA_ACT_MXFP8 = 1, /* plans only */
+  MLORA_ACT_MXFP4 = 2  /* grouped expert products only */
+} mlora_act_format;
 
 /* The backward's weight gradients (dA, dB) run on the side stream beside the
  * dX GEMM(s) (SIDE), or after them on the caller's stream (AFTER).  AUTO:
@@ -485,6 +489,129 @@ mlora_status mlora_adamw_step(mlora_plan_t plan, const mlora_adamw_hparams *hpar
  */
 mlora_status mlora_base_transpose(const void *in, void *out, int64_t rows, int64_t cols,
                                   mlora_dtype dtype, void *stream);
+
+/*
+ * Grouped expert products: a base weight per group of rows.
+ *
+ * The layer above shares one W0 among all rows.  In a mixture-of-experts
+ * block every row belongs to one of n_experts weights instead, and a router
+ * on the device decides to which, so group sizes are known on the device
+ * only: offsets and order below are device arrays that no call copies to
+ * the host or waits for.
+ *
+ * mlora_group_rows -- the stable grouping of rows by id, on the device (what
+ * mlora_plan_from_ids does with host ids).  ids: rows int32 values; row i
+ * belongs to group ids[i] in [0, n_groups), any other value (-1, say) puts
+ * it in no group.  offsets [n_groups + 1] int32: group g owns grouped rows
+ * [offsets[g], offsets[g + 1]).  order [rows] int32: order[s] is the row at
+ * grouped position s, rows of one group in ascending order; positions from
+ * offsets[n_groups] on hold -1.  The result depends on ids alone (no order
+ * of atomics enters it).  0 <= rows < 2^31, 1 <= n_groups <=
+ * MLORA_MAX_EXPERTS.  workspace: mlora_group_rows_workspace bytes, 16-byte
+ * aligned; nothing in it has to be kept between calls.  One or two kernels.
+ */
+#define MLORA_MAX_EXPERTS 4096
+#define MLORA_MAX_EXPERT_DIM 1048576
+mlora_status mlora_group_rows_workspace(int64_t rows, int32_t n_groups, int64_t *bytes);
+mlora_status mlora_group_rows(const int32_t *ids, int64_t rows, int32_t n_groups, int32_t *offsets,
+                              int32_t *order, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Sizes, types and layouts of a grouped expert product.
+ *
+ * Expert e owns grouped rows o_e <= s < o_{e+1} (o = offsets):
+ *   forward :  Y[y(s)]  = X[x(s)] W_e
+ *   backward:  dX[p(s)] = dY[y(s)] W_e^T
+ *              dW_e     = sum_s X[x(s)]^T dY[y(s)]     (fp32; 0 without rows)
+ * Where the rows lie: x_by_order = 0 reads X at grouped row s; 1 reads the
+ * caller's row order[s] / top_k of X [rows / top_k][d_in], so each of the
+ * top_k ids of a token reads that token's row, and dX is [rows][d_in] with
+ * p(s) = order[s]: one gradient per (token, id), the token's being their sum
+ * over its top_k rows.  With x_by_order = 0, p(s) = s and top_k is 1.
+ * y_by_order = 0 takes Y and dY at grouped row s, 1 at row order[s].  Rows of
+ * Y and dX that no grouped row names are left as they were.
+ *
+ * MLORA_BF16: X, W, dY, Y, dX bf16, fp32 accumulation, one rounding at the
+ * end.  MLORA_FP32: every tensor fp32, products and sums in fp32.  W: all
+ * experts in one buffer, [n_experts][d_in][d_out] (MLORA_W0_KN) or
+ * [n_experts][d_out][d_in] (MLORA_W0_NK); dW has W's layout.  Rows are dense.
+ * d_in and d_out: multiples of 8 (bf16) or 4 (fp32), at most
+ * MLORA_MAX_EXPERT_DIM.
+ *
+ * w_format MLORA_W0_MXFP4 (bf16, MLORA_W0_NK, d_in a multiple of 128): W is
+ * the packed buffer that mlora_microscale_quantize makes of the
+ * [n_experts * d_out][d_in] weights, and is read as codes: no decoded copy
+ * is made in the forward.  Such a weight is frozen (dW must be NULL); dX
+ * decodes it into the workspace first.  act_format MLORA_ACT_BF16: X as it
+ * is, the weights' bf16 values (exact: two significant bits).
+ * MLORA_ACT_MXFP4: X is quantized along d_in into the workspace by the
+ * conversion of mlora_microscale_quantize, and both operands go through the
+ * 4-bit matrix cores, Y = Q(X) W; the backward's dX = dY W^T is the
+ * straight-through reading of that quantizer.
+ *
+ * offsets may be NULL with n_experts = 1 (all rows are the expert's).  order
+ * may be NULL when neither x_by_order nor y_by_order is set.  Both are read
+ * by the kernels only.  Values that mlora_group_rows would not write reach
+ * no memory outside the buffers: offsets are clamped to [0, rows], an order
+ * entry outside [0, rows) reads row 0 and its output row is not written.
+ */
+typedef struct {
+  int64_t rows;            /* grouped rows, 0 <= rows < 2^31, a multiple of top_k */
+  int64_t d_in, d_out;
+  int32_t n_experts;       /* 1 .. MLORA_MAX_EXPERTS */
+  int32_t dtype;           /* mlora_dtype */
+  int32_t w_layout;        /* MLORA_W0_KN or MLORA_W0_NK */
+  int32_t w_format;        /* MLORA_W0_BF16 (the dtype's own values) or MLORA_W0_MXFP4 */
+  int32_t act_format;      /* MLORA_ACT_BF16 or, over MXFP4 weights, MLORA_ACT_MXFP4 */
+  int32_t top_k;           /* 1 .. 64 */
+  int32_t x_by_order;
+  int32_t y_by_order;
+  int32_t grad_accumulate; /* 0: dW is overwritten; 1: this call's gradient is added to it */
+} mlora_expert_shape;
+
+/* Workspace of forward and backward for this shape or one with fewer rows (0
+ * when none is needed).  Nothing in it has to be kept between calls; calls
+ * that may overlap (streams, replays of captured graphs) need one each. */
+mlora_status mlora_expert_workspace(const mlora_expert_shape *shape, int64_t *bytes);
+
+/* Y per the formulas above.  Pointers 16-byte aligned (offsets and order:
+ * 4-byte).  Enqueued on `stream`, kernels only, so the call can be captured
+ * into a graph.  With rows = 0 nothing is launched. */
+mlora_status mlora_expert_forward(const mlora_expert_shape *shape, const void *X, const void *W,
+                                  const int32_t *offsets, const int32_t *order, void *Y, void *workspace,
+                                  size_t ws_bytes, void *stream);
+
+/* dX and dW; either may be NULL to skip it (X may be NULL without dW, W
+ * without dX).  With rows = 0, dW is zeroed (or kept, grad_accumulate).  Sums
+ * have a fixed order: results are bitwise repeatable. */
+mlora_status mlora_expert_backward(const mlora_expert_shape *shape, const void *dY, const void *X,
+                                   const void *W, const int32_t *offsets, const int32_t *order, void *dX,
+                                   float *dW, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mlora_microscale_quantize -- a matrix to MXFP4, the format of an
+ * MLORA_W0_MXFP4 base and of the expert weights above.
+ *
+ * X [rows][cols], bf16 (MLORA_BF16) or fp32 (MLORA_FP32), row r starting at
+ * element r * ld (ld >= cols).  Blocks are 32 consecutive elements of a row
+ * (down = 0: cols a multiple of 32; a [d_out][d_in] weight, or activations) or
+ * of a column (down = 1: rows a multiple of 32, cols of 8; a [d_in][d_out]
+ * weight).  Per block, by the OCP microscaling conversion: shared exponent
+ * floor(log2 max|x|) - 2 clamped to [-127, 127] (-127 for a block of zeros),
+ * elements x 2^-exponent rounded to the nearest E2M1 value, ties to even,
+ * magnitudes past 6 saturating to 6.  A block that holds a NaN or an infinity
+ * gets scale code 255 (its values decode to NaN) and element codes 0.
+ *
+ * q: the packed buffer of rows * cols / 2 code bytes [rows][cols / 2] (two
+ * per byte along a row, the even element in the low four bits) followed by
+ * rows * cols / 32 scale codes, [rows][cols / 32] (down = 0) or
+ * [cols][rows / 32] (down = 1).  values: NULL, or [rows][cols] dense of X's
+ * type, the decoded elements (exact).  q and values must not overlap X or
+ * each other.  X, q and values 16-byte aligned; ld a multiple of 8 (bf16) or
+ * 4 (fp32).  One kernel.
+ */
+mlora_status mlora_microscale_quantize(const void *X, mlora_dtype dtype, int64_t rows, int64_t cols,
+                                       int64_t ld, int32_t down, void *q, void *values, void *stream);
 
 /* Per-kernel timing.  Launches of the selected kinds are bracketed by HIP
  * events on the stream they run on; mlora_profile_read waits for them, adds
