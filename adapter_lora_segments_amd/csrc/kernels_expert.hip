@@ -4,6 +4,8 @@
 #include "expert_common.hpp"
 #include "gemm_common.hpp"
 
+#include <type_traits>
+
 namespace mlora {
 
 // 16 zero bytes that copies past a reduction's end read.
@@ -12,6 +14,26 @@ __device__ __constant__ uint32_t g_expert_zero[64] = {0};
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// 16 bytes per lane into LDS from a wave-uniform base plus a 32-bit lane
+// offset: the base lives in scalar registers.  M0 as in dma16_at.
+__device__ __forceinline__ uint64_t uniform64(const void* p) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p);
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b) |
+         ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32);
+}
+__device__ __forceinline__ void dma16_sv(uint64_t sbase, uint32_t voff, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(voff), "s"(sbase)
+      : "memory");
+}
 
 // How an operand's elements lie in memory and in LDS.
 //   KC: contiguous along the reduction; a unit is one row of 128 bytes per
@@ -32,6 +54,117 @@ __device__ __forceinline__ int nx16(int kr) { return ((kr & 1) ? 4 : 0) ^ ((kr &
 // puts them on the two halves of the banks.
 __device__ __forceinline__ int nx32(int kr) { return (kr & 4) ? 8 : 0; }
 
+// A workgroup's tile: 64 FI rows (dW: rows of dW_e) x 256 columns of expert e.
+struct Tile {
+  int e, row0, mrows;   // grouped rows [row0, row0 + mrows); dW: row0 is the group's first row, mrows the tile's
+  int m0, n0;           // first row of dW_e (else 0) and first column
+  int klen;             // length of the reduction
+};
+template <int BM, bool DW>
+__device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
+  const int nN = (g.N + 255) / 256;
+  Tile t;
+  if constexpr (DW) {
+    const int nM = (g.M + BM - 1) / BM, TT = nM * nN;
+    const int b = blockIdx.x, G = gridDim.x, xcd = b & 7, q = b >> 3, per = G >> 3, rem = G & 7;
+    const int L = xcd * per + min(xcd, rem) + q;
+    t.e = L / TT;
+    const int i = L - t.e * TT;
+    constexpr int GM = 4;
+    const int fm = i / (GM * nN) * GM, gm = min(GM, nM - fm), within = i - fm * nN;
+    t.m0 = (fm + within % gm) * BM;
+    t.n0 = within / gm * 256;
+    int hi;
+    group_rows(g, t.e, t.row0, hi);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.klen = __builtin_amdgcn_readfirstlane(hi) - t.row0;
+    t.mrows = min(BM, g.M - t.m0);
+  } else {
+    const RowTile r = row_tile<BM, 4>(g, nN);
+    t = Tile{r.e, r.row0, r.mrows, 0, r.tn * 256, g.K};
+  }
+  return t;
+}
+
+// Row of C for tile row m, or -1 (past the tile, or an order entry that names
+// no row).
+__device__ __forceinline__ int out_row(const ExpertArgs& g, const Tile& t, int m) {
+  if (m >= t.mrows) return -1;
+  const int s = t.row0 + m, v = g.mc.by_order ? g.order[s] : s;
+  return (unsigned)v < (unsigned)g.rows ? v : -1;
+}
+
+// Epilogues.  acc[fi][fj][4 gg + x] holds C[m = wrow + 32 fi + l32][n = wcol
+// + 32 fj + 8 gg + 4 half + x].  fp32 goes straight to memory, four columns a
+// lane; bf16 through LDS (every wave is past its last read of the ring):
+// 512-byte rows of 32 16-byte granules, granule c of row m at c ^ (m & 31), so
+// the rows a fragment writes and the granules a row read takes both spread
+// over the banks and every store writes whole 512-byte rows.
+template <int FI, bool DW>
+__device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][4], const Tile& t, int w,
+                                          int lane) {
+  const int half = lane >> 5, l32 = lane & 31, wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+#pragma unroll
+  for (int fi = 0; fi < FI; ++fi) {
+    const int m = wrow + 32 * fi + l32;
+    const int row = DW ? (m < t.mrows ? t.m0 + m : -1) : out_row(g, t, m);
+    if (row < 0) continue;
+    float* crow = static_cast<float*>(g.C) + (DW ? (int64_t)t.e * g.c_expert : 0) + (int64_t)row * g.ldc;
+#pragma unroll
+    for (int fj = 0; fj < 4; ++fj) {
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg) {
+        const int n = t.n0 + wcol + 32 * fj + 8 * gg + 4 * half;
+        if (n >= g.N) continue;
+        f32x4 v = {acc[fi][fj][4 * gg], acc[fi][fj][4 * gg + 1], acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]};
+        f32x4* dst = reinterpret_cast<f32x4*>(crow + n);
+        if (DW && g.accumulate) v += *dst;
+        *dst = v;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+// dW of a group without rows: zeros (kept when accumulating).
+template <int BM>
+__device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
+  if (g.accumulate) return;
+  float* c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
+  const int n = t.n0 + 4 * (threadIdx.x & 63);
+  if (n >= g.N) return;
+  for (int m = threadIdx.x >> 6; m < t.mrows; m += 4)
+    *reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n) = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+template <int FI>
+__device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&acc)[FI][4], char* ct, const Tile& t,
+                                           int w, int lane) {
+  const int half = lane >> 5, l32 = lane & 31, wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+  __syncthreads();
+#pragma unroll
+  for (int fi = 0; fi < FI; ++fi) {
+    const int m = wrow + 32 * fi + l32;
+#pragma unroll
+    for (int fj = 0; fj < 4; ++fj)
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg) {
+        const int c = (wcol >> 3) + 4 * fj + gg;
+        u32x2 pk;
+        pk[0] = pack_bf16x2(acc[fi][fj][4 * gg + 0], acc[fi][fj][4 * gg + 1]);
+        pk[1] = pack_bf16x2(acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]);
+        *reinterpret_cast<u32x2*>(ct + m * 512 + 16 * (c ^ (m & 31)) + 8 * half) = pk;
+      }
+  }
+  __syncthreads();
+  const int gc = lane & 31, n = t.n0 + 8 * gc;
+#pragma unroll 4
+  for (int it = 0; it < 8 * FI; ++it) {
+    const int m = 16 * FI * w + 2 * it + half;
+    const int row = out_row(g, t, m);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(ct + m * 512 + 16 * (gc ^ (m & 31)));
+    if (row >= 0 && n < g.N) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (int64_t)row * g.ldc + n) = x;
+  }
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -50,32 +183,11 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
   constexpr int EPI = F32 || DW ? 0 : BM * 512;                             // the epilogue's bf16 tile
   __shared__ u32x4 ring[(2 * (UA + UB) > EPI ? 2 * (UA + UB) : EPI) / 16];
 
-  const int nN = (g.N + BN - 1) / BN;
-  int e, row0, mrows, n0, klen, m0 = 0;
-  if constexpr (DW) {
-    const int nM = (g.M + BM - 1) / BM, TT = nM * nN;
-    const int b = blockIdx.x, G = gridDim.x, xcd = b & 7, q = b >> 3, per = G >> 3, rem = G & 7;
-    const int L = xcd * per + min(xcd, rem) + q;
-    e = L / TT;
-    const int t = L - e * TT;
-    constexpr int GM = 4;
-    const int grp = t / (GM * nN), fm = grp * GM, gm = min(GM, nM - fm), within = t - fm * nN;
-    m0 = (fm + within % gm) * BM;
-    n0 = within / gm * BN;
-    int hi;
-    group_rows(g, e, row0, hi);
-    klen = hi - row0;
-    mrows = min(BM, g.M - m0);
-  } else {
-    const RowTile t = row_tile<BM, 4>(g, nN);
-    if (t.mrows <= 0) return;
-    e = t.e;
-    row0 = t.row0;
-    mrows = t.mrows;
-    n0 = t.tn * BN;
-    klen = g.K;
-  }
+  const Tile tl = find_tile<BM, DW>(g);
+  if (!DW && tl.mrows <= 0) return;
+  const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
   const int nsteps = (klen + KD - 1) / KD;
+  if (DW && nsteps == 0) return store_zero<BM>(g, tl);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -212,7 +324,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
     }
   };
 
-  if (nsteps > 0) issue(0);
+  issue(0);
   for (int t = 0; t < nsteps; ++t) {
     // step t has landed, and every wave is done with the other buffer
     wait_vm_barrier<0>();
@@ -253,65 +365,329 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
-  // acc[fi][fj][4 gg + x] holds C[m = wrow + 32 fi + l32][n = wcol + 32 fj + 8 gg + 4 half + x]
-  if constexpr (F32 || DW) {
+  if constexpr (F32 || DW) store_f32<FI, DW>(g, acc, tl, w, lane);
+  else store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Pipelined tile kernel for bf16 operands (and E2M1 weights): the base GEMM's
+// schedule over ragged groups.  A 64 FI x 256 tile per workgroup of four
+// waves, 64-deep steps, one unit of LDS per operand and step.  While step s is
+// computed, step s + 1 and the A unit of step s + 2 are in flight: with 32 KiB
+// units (FI = 4) five of them fill the 160 KiB, unit u in slot u mod 5; other
+// sizes hold three whole steps.
+//
+// A step is four 16-deep slices with fragments double buffered in registers;
+// the reads and copies sit between the MFMAs of a slice.  Step s:
+//   slices 0-1: read the next slice; copy the A unit of step s + 2;
+//   slice 2: read slice 3; then wait until this wave's copies of step s + 1
+//     have landed (the A unit of step s + 2 may be in flight) and its reads are
+//     done, and meet the other waves: step s + 1 is complete in LDS and nobody
+//     reads step s any more;
+//   slice 3: read step s + 1's first slice; copy the B unit of step s + 2.
+// E2M1 weights: half h of a wave takes the step's 32-block h, whose 32 codes
+// are one 16-byte read per step; word ks of it becomes slice ks's eight bf16
+// by four conversions while the slice before is computed, so the weights
+// cross LDS at 4 bits and no decoded copy exists.
+// ---------------------------------------------------------------------------
+template <int AL, int BL, int FI, bool DW, bool GATHER>
+__global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
+  constexpr int FJ = 4, BM = 64 * FI, BN = 256, KD = 64, NS = FI * FJ;
+  constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + BN * 4 : BN * 128;
+  constexpr bool RING5 = UA == UB;
+  constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : 8;   // 1 KiB copies per wave and unit
+  constexpr int CBW = CB + (BL == F4 ? 1 : 0);           // and the scale dwords
+  constexpr int RING = RING5 ? 5 * UA : 3 * (UA + UB);
+  constexpr int LDS = DW || RING >= BM * 512 ? RING : BM * 512;   // the epilogue's bf16 tile takes BM x 512
+  __shared__ u32x4 ring[LDS / 16];
+
+  const Tile tl = find_tile<BM, DW>(g);
+  if (!DW && tl.mrows <= 0) return;
+  const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
+  const int nsteps = (klen + KD - 1) / KD;
+  if (DW && nsteps == 0) return store_zero<BM>(g, tl);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+  const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
+  const uint8_t* const Be = DW ? g.B : g.B + (int64_t)e * g.b_expert;
+
+  // Copy sources.  k-contiguous: copy i of a wave takes tile rows 8 (C w + i)
+  // + lane / 8 at LDS position lane % 8, which holds chunk (lane % 8) ^
+  // kx8(row).  n-contiguous: k-rows RPC (C w + i) + lane / CPR, position lane
+  // % CPR, chunk ^ nx16(k-row).
+  constexpr int CPRA = BM / 8, RPCA = 64 / CPRA, CPRB = BN / 8, RPCB = 64 / CPRB;
+  const uint8_t* ap[AL == KC ? CA : 1];  // rows of A anywhere: one pointer per copy
+  uint32_t ao[CA], bo[CB];               // else byte offsets from a base that advances by steps
+  int ac[CA], bc[CB];                    // KC: chunk; NC: k-row of the step
 #pragma unroll
-    for (int fi = 0; fi < FI; ++fi) {
-      const int m = wrow + 32 * fi + l32;
-      if (m >= mrows) continue;
-      int64_t row;
-      if (DW) {
-        row = m0 + m;
-      } else {
-        const int s = row0 + m, v = g.mc.by_order ? g.order[s] : s;
-        if ((unsigned)v >= (unsigned)g.rows) continue;
-        row = v;
-      }
-      float* crow = static_cast<float*>(g.C) + (DW ? (int64_t)e * g.c_expert : 0) + row * g.ldc;
-#pragma unroll
-      for (int fj = 0; fj < FJ; ++fj)
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-          const int n = n0 + wcol + 32 * fj + 8 * gg + 4 * half;
-          if (n >= g.N) continue;
-          f32x4 v = {acc[fi][fj][4 * gg], acc[fi][fj][4 * gg + 1], acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]};
-          f32x4* dst = reinterpret_cast<f32x4*>(crow + n);
-          if (DW && g.accumulate) {
-            const f32x4 old = *dst;
-            v += old;
-          }
-          *dst = v;
-        }
-    }
-  } else {
-    __syncthreads();
-    char* ct = reinterpret_cast<char*>(&ring[0]);
-#pragma unroll
-    for (int fi = 0; fi < FI; ++fi) {
-      const int m = wrow + 32 * fi + l32;
-#pragma unroll
-      for (int fj = 0; fj < FJ; ++fj)
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg) {
-          const int c = (wcol >> 3) + 4 * fj + gg;
-          u32x2 pk;
-          pk[0] = pack_bf16x2(acc[fi][fj][4 * gg + 0], acc[fi][fj][4 * gg + 1]);
-          pk[1] = pack_bf16x2(acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]);
-          *reinterpret_cast<u32x2*>(ct + m * 512 + 16 * (c ^ (m & 31)) + 8 * half) = pk;
-        }
-    }
-    __syncthreads();
-    const int gc = lane & 31;
-    for (int it = 0; it < BM / 8; ++it) {
-      const int m = (BM / 4) * w + 2 * it + half;
-      const int n = n0 + 8 * gc;
-      if (m >= mrows || n >= g.N) continue;
-      const int s = row0 + m, v = g.mc.by_order ? g.order[s] : s;
-      if ((unsigned)v >= (unsigned)g.rows) continue;
-      const u32x4 x = *reinterpret_cast<const u32x4*>(ct + m * 512 + 16 * (gc ^ (m & 31)));
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (int64_t)v * g.ldc + n) = x;
+  for (int i = 0; i < CA; ++i) {
+    if constexpr (AL == KC) {
+      const int r = 8 * (CA * w + i) + (lane >> 3);
+      ac[i] = (lane & 7) ^ kx8(r);
+      ao[i] = 0;
+      ap[i] = g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * g.lda * 2 + 16 * ac[i];
+    } else {
+      ac[i] = RPCA * (CA * w + i) + lane / CPRA;
+      const int col = min(m0 + 8 * ((lane % CPRA) ^ nx16(ac[i])), g.M - 8);
+      ao[i] = GATHER ? (uint32_t)(col * 2) : (uint32_t)(((int64_t)ac[i] * g.lda + col) * 2);
     }
   }
+#pragma unroll
+  for (int i = 0; i < CB; ++i) {
+    if constexpr (BL == KC) {
+      const int r = 8 * (CB * w + i) + (lane >> 3);
+      bc[i] = (lane & 7) ^ kx8(r);
+      bo[i] = (uint32_t)((int64_t)(min(n0 + r, g.N - 1) - n0) * g.ldb * 2 + 16 * bc[i]);
+    } else if constexpr (BL == NC) {
+      bc[i] = RPCB * (CB * w + i) + lane / CPRB;
+      const int col = min(n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
+      bo[i] = GATHER ? (uint32_t)(col * 2) : (uint32_t)(((int64_t)bc[i] * g.ldb + (col - n0)) * 2);
+    } else {
+      const int r = 32 * (2 * w + i) + (lane >> 1);
+      bc[i] = 0;
+      bo[i] = (uint32_t)((int64_t)(min(n0 + r, g.N - 1) - n0) * (g.ldb / 2) +
+                         16 * ((lane & 1) ^ ((r >> 3) & 1)));
+    }
+  }
+  const uint8_t* sp = nullptr;
+  if constexpr (BL == F4) sp = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
+  // bases of step 0 and bytes per step
+  const uint8_t* const baseA = AL == NC && !GATHER ? g.A + (int64_t)row0 * g.lda * 2 : g.A;
+  const uint8_t* const baseB =
+      BL == KC ? Be + (int64_t)n0 * g.ldb * 2
+               : BL == F4 ? Be + (int64_t)n0 * (g.ldb / 2)
+                          : (DW && !GATHER ? Be + ((int64_t)row0 * g.ldb + n0) * 2 : (DW ? Be : Be + (int64_t)n0 * 2));
+  const int64_t stepA = (int64_t)KD * g.lda * 2;
+  const int64_t stepB = BL == KC ? 128 : BL == F4 ? 32 : (int64_t)KD * g.ldb * 2;
+
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
+  auto slot = [](int u) -> uint32_t {
+    if constexpr (RING5) return (uint32_t)(u % 5) * UA;
+    else return (uint32_t)((u >> 1) % 3) * (UA + UB) + ((u & 1) ? UA : 0);
+  };
+  // Copy i of step t's A (B) unit.  CHECK: the step may pass the end of the
+  // reduction, and what does reads zeros.
+  auto copy_a = [&](int t, int i, auto check) {
+    const uint32_t lds = lds0 + slot(2 * t) + 1024u * (uint32_t)(CA * w + i);
+    if constexpr (AL == KC) {
+      const uint8_t* src = ap[i] + 128 * (int64_t)t;
+      dma16_at(!check.value || t * KD + 8 * ac[i] < klen ? src : zero, lds);
+    } else if constexpr (GATHER) {
+      const int k = t * KD + ac[i];
+      const bool on = k < klen;
+      const int64_t row = source_row(g, g.ma, row0 + (on ? k : 0));
+      dma16_at(on ? baseA + row * g.lda * 2 + ao[i] : zero, lds);
+    } else if constexpr (check.value) {
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseA + t * stepA));
+      dma16_at(t * KD + ac[i] < klen ? at + ao[i] : zero, lds);
+    } else {
+      dma16_sv(uniform64(baseA + t * stepA), ao[i], lds);
+    }
+  };
+  auto copy_b = [&](int t, int i, auto check) {
+    const uint32_t lds = lds0 + slot(2 * t + 1) + 1024u * (uint32_t)(CB * w + i);
+    if constexpr (BL == NC && GATHER) {
+      const int k = t * KD + bc[i];
+      const bool on = k < klen;
+      const int64_t row = source_row(g, g.mb, row0 + (on ? k : 0));
+      dma16_at(on ? baseB + row * g.ldb * 2 + bo[i] : zero, lds);
+    } else if constexpr (check.value) {
+      const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + 8 * bc[i] < klen;
+      const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseB + t * stepB));
+      dma16_at(on ? at + bo[i] : zero, lds);
+    } else {
+      dma16_sv(uniform64(baseB + t * stepB), bo[i], lds);
+    }
+  };
+  auto copy_scales = [&](int t, auto check) {
+    if constexpr (BL == F4)
+      dma4_at(!check.value || t * KD < klen ? sp + 4 * (t >> 1) : zero,
+              lds0 + slot(2 * t + 1) + BN * 32 + 256u * (uint32_t)w);
+  };
+
+  f32x16 acc[FI][FJ];
+#pragma unroll
+  for (int a = 0; a < FI; ++a)
+#pragma unroll
+    for (int b = 0; b < FJ; ++b)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
+
+  // Fragment reads: a lane part plus the step's slot, made once per step (the
+  // empty asm keeps the slot from being folded into every read), plus
+  // immediates.  k-contiguous: one lane part per slice; n-contiguous: one per
+  // fragment, slices and the second half of the k-rows as immediates (nx16
+  // depends on k-row bits 0, 1 and 3 only, which the lane fixes).
+  const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
+  uint32_t al[4], bl[4];
+  auto lane_kc = [&](int r, int ks) {
+    const int c = BL == F4 ? 4 * half + ks : 2 * ks + half;
+    return (uint32_t)((r * 8 + (c ^ kx8(l32))) * 16);
+  };
+  auto lane_nc = [&](int cpr, int col0) {
+    const int gq = lane >> 4, sq = lane & 15, kr = 8 * (gq >> 1) + (sq >> 2);
+    const int n = col0 + 16 * (gq & 1) + 4 * (sq & 3);
+    return (uint32_t)((kr * cpr + ((n >> 3) ^ nx16(kr))) * 16 + 2 * (n & 7));
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    al[i] = AL == KC ? lane_kc(wrow + l32, i) : lane_nc(CPRA, wrow + 32 * (i < FI ? i : 0));
+    if constexpr (BL == KC) bl[i] = lane_kc(wcol + l32, i);
+    else if constexpr (BL == NC) bl[i] = lane_nc(CPRB, wcol + 32 * i);
+    else bl[i] = (uint32_t)(((wcol + 32 * i + l32) * 2 + (half ^ ((l32 >> 3) & 1))) * 16);
+  }
+  struct Bases {
+    uint32_t a[4], b[4];
+  };
+  auto step_bases = [&](int s, Bases& bs, int ks0, int ks1) {
+    const uint32_t sa = slot(2 * s), sb = slot(2 * s + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (AL == NC ? i < FI : (i >= ks0 && i <= ks1)) {
+        bs.a[i] = al[i] + sa;
+        asm volatile("" : "+v"(bs.a[i]));
+      }
+      if (BL != KC || (i >= ks0 && i <= ks1)) {
+        bs.b[i] = bl[i] + sb;
+        asm volatile("" : "+v"(bs.b[i]));
+      }
+    }
+  };
+  auto read_tr = [&](uint32_t at, int cpr, int ks) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const MLORA_LDS char* p = base + at + 256 * cpr * ks;
+    const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MLORA_LDS s16x4*)p);
+    const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MLORA_LDS s16x4*)(p + 64 * cpr));
+    const u32x2 u0 = __builtin_bit_cast(u32x2, v0), u1 = __builtin_bit_cast(u32x2, v1);
+    return u32x4{u0[0], u0[1], u1[0], u1[1]};
+  };
+  u32x4 fa[2][FI], fb[2][FJ];
+  u32x4 cw[FJ];       // E2M1: the step's codes of this lane's block, and its scales
+  float cs[FJ];
+  auto read_a = [&](const Bases& bs, int ks, int f, u32x4 (&ra)[FI]) {
+    if constexpr (AL == KC) ra[f] = *(const MLORA_LDS u32x4*)(base + bs.a[ks] + 4096 * f);
+    else ra[f] = read_tr(bs.a[f], CPRA, ks);
+  };
+  auto read_b = [&](const Bases& bs, int ks, int f, u32x4 (&rb)[FJ]) {
+    if constexpr (BL == KC) rb[f] = *(const MLORA_LDS u32x4*)(base + bs.b[ks] + 4096 * f);
+    else if constexpr (BL == NC) rb[f] = read_tr(bs.b[f], CPRB, ks);
+    else rb[f] = bf16_of_e2m1(cw[f][ks], cs[f]);
+  };
+  // E2M1 codes and scales of step s (bases bs).
+  auto read_codes = [&](const Bases& bs, int s, int f) {
+    if constexpr (BL == F4) {
+      cw[f] = *(const MLORA_LDS u32x4*)(base + bs.b[f]);
+      const uint32_t sw = *(const MLORA_LDS uint32_t*)(base + slot(2 * s + 1) + BN * 32 + 4 * (wcol + 32 * f + l32));
+      cs[f] = __uint_as_float(((sw >> (16 * (s & 1) + 8 * half)) & 255u) << 23);
+    }
+  };
+  // What MFMA slot q of a slice reads of slice ks (bases bs): fragments in the
+  // order the first MFMAs need them, two per slot, or one where a fragment is
+  // two transposing reads or four conversions.
+  constexpr int RPS = AL == KC && BL == KC ? 2 : 1;
+  auto reads_at = [&](int q, const Bases& bs, int ks, u32x4 (&ra)[FI], u32x4 (&rb)[FJ]) {
+#pragma unroll
+    for (int j = 0; j < RPS; ++j) {
+      const int r = RPS * q + j;
+      if (r == 0) read_a(bs, ks, 0, ra);
+      else if (r <= FJ) read_b(bs, ks, r - 1, rb);
+      else if (r < FI + FJ) read_a(bs, ks, r - FJ, ra);
+    }
+  };
+  auto next_step_reads_at = [&](int q, const Bases& bs, int s, u32x4 (&ra)[FI], u32x4 (&rb)[FJ]) {
+    if constexpr (BL != F4) {
+      reads_at(q, bs, 0, ra, rb);
+    } else {
+      if (q < 2) {
+        read_codes(bs, s, 2 * q);
+        read_codes(bs, s, 2 * q + 1);
+      } else if (q == 2) {
+#pragma unroll
+        for (int f = 0; f < FI; ++f) read_a(bs, 0, f, ra);
+      }
+      if (q >= NS - FJ) read_b(bs, 0, q - (NS - FJ), rb);
+    }
+  };
+  constexpr int C0 = BL == F4 ? 3 : (FI + FJ + RPS - 1) / RPS;   // first slot that carries a copy
+  // Copies j of n spread over the slots from C0 on.
+  auto copies_at = [&](int q, int n, auto&& f) {
+    const int room = NS - C0, per = (n + room - 1) / room;
+    if (q < C0) return;
+#pragma unroll
+    for (int j = 0; j < per; ++j)
+      if ((q - C0) * per + j < n) f((q - C0) * per + j);
+  };
+  auto mma = [&](int q, const u32x4 (&ra)[FI], const u32x4 (&rb)[FJ]) {
+    acc[q >> 2][q & 3] = mfma32(rb[q & 3], ra[q >> 2], acc[q >> 2][q & 3]);
+  };
+
+  // Step kinds: 0, step s + 2 lies inside the reduction; 1, it reaches past
+  // its end; 2, it does not exist: nothing is copied and the barrier waits for
+  // every copy in flight.
+  auto step_block = [&](int s, auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    constexpr bool COPY = KIND != 2;
+    const std::integral_constant<bool, KIND == 1> check{};
+    Bases cur;
+    step_bases(s, cur, 1, 3);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int ks = 0; ks < 3; ++ks) {
+#pragma unroll
+      for (int q = 0; q < NS; ++q) {
+        mma(q, fa[ks & 1], fb[ks & 1]);
+        reads_at(q, cur, ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
+        if (COPY && ks < 2) copies_at(q, CA / 2, [&](int j) { copy_a(s + 2, ks * (CA / 2) + j, check); });
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_vm_barrier<COPY ? CA : 0>();
+    Bases nxt;
+    step_bases(s + 1, nxt, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      mma(q, fa[1], fb[1]);
+      next_step_reads_at(q, nxt, s + 1, fa[0], fb[0]);
+      if (COPY)
+        copies_at(q, CBW, [&](int j) {
+          if (j < CB) copy_b(s + 2, j, check);
+          else copy_scales(s + 2, check);
+        });
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // steps 0 and 1; step 0's first slice once every wave's copies of it have landed
+  const std::integral_constant<bool, true> check{};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+#pragma unroll
+    for (int i = 0; i < CA; ++i) copy_a(t, i, check);
+#pragma unroll
+    for (int i = 0; i < CB; ++i) copy_b(t, i, check);
+    copy_scales(t, check);
+  }
+  wait_vm_barrier<CA + CBW>();
+  Bases b0;
+  step_bases(0, b0, 0, 0);
+#pragma unroll
+  for (int f = 0; f < FJ; ++f) read_codes(b0, 0, f);
+#pragma unroll
+  for (int f = 0; f < FI; ++f) read_a(b0, 0, f, fa[0]);
+#pragma unroll
+  for (int f = 0; f < FJ; ++f) read_b(b0, 0, f, fb[0]);
+  int s = 0;
+  for (; (s + 3) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
+  for (; s + 2 < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
+  for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  if constexpr (DW) store_f32<FI, DW>(g, acc, tl, w, lane);
+  else store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,10 +704,9 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
   constexpr int UA = BM * 64, UB = BN * 64, CA = FI, CB = 4;
   constexpr int STAGE = UA + UB + (BM + BN) * 4;
   __shared__ u32x4 ring[(2 * STAGE > BM * 512 ? 2 * STAGE : BM * 512) / 16];
-  const int nN = (g.N + BN - 1) / BN;
-  const RowTile tile = row_tile<BM, 4>(g, nN);
-  if (tile.mrows <= 0) return;
-  const int e = tile.e, row0 = tile.row0, mrows = tile.mrows, n0 = tile.tn * BN;
+  const Tile tl = find_tile<BM, false>(g);
+  if (tl.mrows <= 0) return;
+  const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, n0 = tl.n0;
   const int nsteps = g.K / 128;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -413,49 +788,28 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-  __syncthreads();
-  char* ct = reinterpret_cast<char*>(&ring[0]);
-#pragma unroll
-  for (int fi = 0; fi < FI; ++fi) {
-    const int m = wrow + 32 * fi + l32;
-#pragma unroll
-    for (int fj = 0; fj < FJ; ++fj)
-#pragma unroll
-      for (int gg = 0; gg < 4; ++gg) {
-        const int c = (wcol >> 3) + 4 * fj + gg;
-        u32x2 pk;
-        pk[0] = pack_bf16x2(acc[fi][fj][4 * gg + 0], acc[fi][fj][4 * gg + 1]);
-        pk[1] = pack_bf16x2(acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]);
-        *reinterpret_cast<u32x2*>(ct + m * 512 + 16 * (c ^ (m & 31)) + 8 * half) = pk;
-      }
-  }
-  __syncthreads();
-  const int gc = lane & 31;
-  for (int it = 0; it < BM / 8; ++it) {
-    const int m = (BM / 4) * w + 2 * it + half;
-    const int n = n0 + 8 * gc;
-    if (m >= mrows || n >= g.N) continue;
-    const int s = row0 + m, v = g.mc.by_order ? g.order[s] : s;
-    if ((unsigned)v >= (unsigned)g.rows) continue;
-    const u32x4 x = *reinterpret_cast<const u32x4*>(ct + m * 512 + 16 * (gc ^ (m & 31)));
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (int64_t)v * g.ldc + n) = x;
-  }
+  store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
 }
 
 namespace {
 
-template <bool F32, int AL, int BL, int FI>
-void rows_tile(const ExpertArgs& a, hipStream_t s) {
-  const int64_t nN = (a.N + 255) / 256;
-  const int64_t grid = max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, 64 * FI) * nN;
-  hipLaunchKernelGGL((k_expert_tile<F32, AL, BL, FI, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
+int64_t rows_grid(const ExpertArgs& a, int bm) {
+  return max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, bm) * ((a.N + 255) / 256);
 }
 template <bool F32, int BL>
 void rows_size(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96) rows_tile<F32, KC, BL, 1>(a, s);
-  else if (mean <= 384) rows_tile<F32, KC, BL, 2>(a, s);
-  else rows_tile<F32, KC, BL, 4>(a, s);
+  if (mean <= 96) {
+    hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
+  } else if (mean <= 384) {
+    const dim3 grid((unsigned)rows_grid(a, 128));
+    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 2, false>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 2, false, false>), grid, dim3(256), 0, s, a);
+  } else {
+    const dim3 grid((unsigned)rows_grid(a, 256));
+    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 4, false>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 4, false, false>), grid, dim3(256), 0, s, a);
+  }
 }
 template <int FI>
 void mx4_tile(const ExpertArgs& a, hipStream_t s) {
@@ -494,8 +848,11 @@ void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
   const int64_t nN = (a.N + 255) / 256;
   const int64_t grid = E * ((a.M + 255) / 256) * nN;
-  if (f32) hipLaunchKernelGGL((k_expert_tile<true, NC, NC, 4, true>), dim3((unsigned)grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_expert_tile<false, NC, NC, 4, true>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  const dim3 dg((unsigned)grid);
+  if (f32) hipLaunchKernelGGL((k_expert_tile<true, NC, NC, 4, true>), dg, dim3(256), 0, s, a);
+  else if (a.ma.by_order || a.mb.by_order)
+    hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, true>), dg, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, false>), dg, dim3(256), 0, s, a);
 }
 
 }  // namespace mlora
