@@ -65,11 +65,25 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
   const int nN = (g.N + 255) / 256;
   Tile t;
   if constexpr (DW) {
-    const int nM = (g.M + BM - 1) / BM, TT = nM * nN;
-    const int b = blockIdx.x, G = gridDim.x, xcd = b & 7, q = b >> 3, per = G >> 3, rem = G & 7;
-    const int L = xcd * per + min(xcd, rem) + q;
-    t.e = L / TT;
-    const int i = L - t.e * TT;
+    // Experts have reductions of different lengths: every expert's tiles are
+    // spread over all XCDs, and up to 64 experts run longest first, so the
+    // launch does not end on one XCD's long tiles.
+    const int nM = (g.M + BM - 1) / BM, TT = nM * nN, share = (TT + 7) / 8;
+    const int xcd = blockIdx.x & 7, q = blockIdx.x >> 3;
+    int i = xcd * share + q % share;
+    t.e = q / share;
+    if (g.offsets && g.n_experts <= 64) {
+      const int lane = threadIdx.x & 63;
+      int lo = 0, hi = -1;
+      if (lane < g.n_experts) group_rows(g, lane, lo, hi);
+      const int n = hi - lo;
+      int rank = 0;
+      for (int j = 0; j < g.n_experts; ++j) {
+        const int nj = __builtin_amdgcn_readlane(n, j);
+        rank += nj > n || (nj == n && j < lane) ? 1 : 0;
+      }
+      t.e = __builtin_ctzll(__ballot(lane < g.n_experts && rank == t.e));
+    }
     constexpr int GM = 4;
     const int fm = i / (GM * nN) * GM, gm = min(GM, nM - fm), within = i - fm * nN;
     t.m0 = (fm + within % gm) * BM;
@@ -78,7 +92,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
     group_rows(g, t.e, t.row0, hi);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.klen = __builtin_amdgcn_readfirstlane(hi) - t.row0;
-    t.mrows = min(BM, g.M - t.m0);
+    t.mrows = i < TT ? min(BM, g.M - t.m0) : 0;
   } else {
     const RowTile r = row_tile<BM, 4>(g, nN);
     t = Tile{r.e, r.row0, r.mrows, 0, r.tn * 256, g.K};
@@ -125,6 +139,43 @@ __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&ac
     }
   }
 }
+// dW through LDS: 64 rows x 256 columns a time (one fragment row of every
+// wave) in one of two 64 KiB buffers, granule c of row m at c ^ (m & 31), so
+// every store instruction writes one whole row of 1 KiB.
+template <int FI>
+__device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc)[FI][4], char* ct, const Tile& t,
+                                         int w, int lane) {
+  const int half = lane >> 5, l32 = lane & 31, wcol = 128 * (w & 1);
+  float* const c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
+  const int n = t.n0 + 4 * lane;
+  __syncthreads();
+#pragma unroll
+  for (int fi = 0; fi < FI; ++fi) {
+    char* buf = ct + (fi & 1) * 65536;
+    const int mw = 32 * (w >> 1) + l32;
+#pragma unroll
+    for (int fj = 0; fj < 4; ++fj)
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg) {
+        const f32x4 v = {acc[fi][fj][4 * gg], acc[fi][fj][4 * gg + 1], acc[fi][fj][4 * gg + 2],
+                         acc[fi][fj][4 * gg + 3]};
+        *reinterpret_cast<f32x4*>(buf + mw * 1024 + 16 * (((wcol >> 2) + 8 * fj + 2 * gg + half) ^ (mw & 31))) = v;
+      }
+    __syncthreads();
+#pragma unroll 4
+    for (int it = 0; it < 16; ++it) {
+      const int mr = 16 * w + it;
+      const int m = 32 * FI * (mr >> 5) + 32 * fi + (mr & 31);
+      f32x4 v = *reinterpret_cast<const f32x4*>(buf + mr * 1024 + 16 * (lane ^ (mr & 31)));
+      if (m < t.mrows && n < g.N) {
+        f32x4* dst = reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n);
+        if (g.accumulate) v += *dst;
+        *dst = v;
+      }
+    }
+  }
+}
+
 // dW of a group without rows: zeros (kept when accumulating).
 template <int BM>
 __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
@@ -184,7 +235,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
   __shared__ u32x4 ring[(2 * (UA + UB) > EPI ? 2 * (UA + UB) : EPI) / 16];
 
   const Tile tl = find_tile<BM, DW>(g);
-  if (!DW && tl.mrows <= 0) return;
+  if (tl.mrows <= 0) return;
   const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
   const int nsteps = (klen + KD - 1) / KD;
   if (DW && nsteps == 0) return store_zero<BM>(g, tl);
@@ -402,7 +453,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   __shared__ u32x4 ring[LDS / 16];
 
   const Tile tl = find_tile<BM, DW>(g);
-  if (!DW && tl.mrows <= 0) return;
+  if (tl.mrows <= 0) return;
   const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
   const int nsteps = (klen + KD - 1) / KD;
   if (DW && nsteps == 0) return store_zero<BM>(g, tl);
@@ -468,6 +519,27 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     if constexpr (RING5) return (uint32_t)(u % 5) * UA;
     else return (uint32_t)((u >> 1) % 3) * (UA + UB) + ((u & 1) ? UA : 0);
   };
+  // Order entries of this wave's 16 k-rows of a step, by scalar loads (they
+  // wait on lgkmcnt, not on the counter that tracks the copies in flight), and
+  // the row that copy i of either operand reads: k-row 16 w + 2 i + lane / 32.
+  static_assert(!GATHER || (AL == NC && BL == NC && FI == 4), "both operands copy two k-rows at a time");
+  int oidx[GATHER ? 16 : 1];
+  auto load_order = [&](int t) {
+    if constexpr (GATHER) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) oidx[j] = ldc(g.order + row0 + min(t * KD + 16 * w + j, klen - 1));
+    }
+  };
+  auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t ld, int i, int t) -> const uint8_t* {
+    const int k = row0 + t * KD + 16 * w + 2 * i;
+    auto at = [&](int h) -> int64_t {
+      return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], g.rows), map.div)
+                           : (int64_t)(k + h)) *
+             ld * 2;
+    };
+    const int64_t r0 = at(0), r1 = at(1);
+    return from + (half ? r1 : r0);
+  };
   // Copy i of step t's A (B) unit.  CHECK: the step may pass the end of the
   // reduction, and what does reads zeros.
   auto copy_a = [&](int t, int i, auto check) {
@@ -476,10 +548,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       const uint8_t* src = ap[i] + 128 * (int64_t)t;
       dma16_at(!check.value || t * KD + 8 * ac[i] < klen ? src : zero, lds);
     } else if constexpr (GATHER) {
-      const int k = t * KD + ac[i];
-      const bool on = k < klen;
-      const int64_t row = source_row(g, g.ma, row0 + (on ? k : 0));
-      dma16_at(on ? baseA + row * g.lda * 2 + ao[i] : zero, lds);
+      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, g.ma, g.lda, i, t) + ao[i] : zero, lds);
     } else if constexpr (check.value) {
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseA + t * stepA));
       dma16_at(t * KD + ac[i] < klen ? at + ao[i] : zero, lds);
@@ -490,10 +559,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   auto copy_b = [&](int t, int i, auto check) {
     const uint32_t lds = lds0 + slot(2 * t + 1) + 1024u * (uint32_t)(CB * w + i);
     if constexpr (BL == NC && GATHER) {
-      const int k = t * KD + bc[i];
-      const bool on = k < klen;
-      const int64_t row = source_row(g, g.mb, row0 + (on ? k : 0));
-      dma16_at(on ? baseB + row * g.ldb * 2 + bo[i] : zero, lds);
+      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, g.mb, g.ldb, i, t) + bo[i] : zero, lds);
     } else if constexpr (check.value) {
       const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + 8 * bc[i] < klen;
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseB + t * stepB));
@@ -632,6 +698,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     constexpr bool COPY = KIND != 2;
     const std::integral_constant<bool, KIND == 1> check{};
     Bases cur;
+    if (COPY) load_order(s + 2);
     step_bases(s, cur, 1, 3);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -666,6 +733,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   const std::integral_constant<bool, true> check{};
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
+    load_order(t);
 #pragma unroll
     for (int i = 0; i < CA; ++i) copy_a(t, i, check);
 #pragma unroll
@@ -686,7 +754,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   for (; s + 2 < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
   for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  if constexpr (DW) store_f32<FI, DW>(g, acc, tl, w, lane);
+  if constexpr (DW) store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
   else store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
 }
 
@@ -696,14 +764,18 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
 // dword of scale codes per row and operand.  Chunk c of row r sits at
 // c ^ ((r >> 2) & 3), which spreads a read group's rows over the banks; lane
 // r + 32 h holds row r's 32-block h of a 64-deep slice (16 bytes, the low
-// nibble first) and supplies its scale.
+// nibble first) and supplies its scale.  A step is two slices, 1024 cycles of
+// MFMA at FI = 4, less than a copy's latency: four stages keep three steps in
+// flight.
 // ---------------------------------------------------------------------------
 template <int FI>
 __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
   constexpr int FJ = 4, BM = 64 * FI, BN = 256;
-  constexpr int UA = BM * 64, UB = BN * 64, CA = FI, CB = 4;
-  constexpr int STAGE = UA + UB + (BM + BN) * 4;
-  __shared__ u32x4 ring[(2 * STAGE > BM * 512 ? 2 * STAGE : BM * 512) / 16];
+  constexpr int UA = BM * 64, UB = BN * 64, CA = FI, CB = 4, NS = FI * FJ;
+  constexpr int NR = 4;                               // stages
+  constexpr int STAGE = UA + UB + 1024 + BN * 4;      // scale dwords: 256 of A (BM used), 256 of B
+  constexpr int COPIES = CA + CB + 2;                 // per wave and step
+  __shared__ u32x4 ring[(NR * STAGE > BM * 512 ? NR * STAGE : BM * 512) / 16];
   const Tile tl = find_tile<BM, false>(g);
   if (tl.mrows <= 0) return;
   const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, n0 = tl.n0;
@@ -727,18 +799,19 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
     bp[i] = g.B + (int64_t)e * g.b_expert + (int64_t)min(n0 + r, g.N - 1) * (g.K / 2) +
             16 * ((lane & 3) ^ ((r >> 2) & 3));
   }
-  // scale dwords: wave w copies rows 64 w .. of A (waves below FI) and of B
-  const uint8_t* as = g.a_scale + source_row(g, g.ma, row0 + min(64 * min(w, FI - 1) + lane, mrows - 1)) * kb;
+  // scale dwords: wave w copies those of rows 64 w .. of A and of B
+  const uint8_t* as = g.a_scale + source_row(g, g.ma, row0 + min(64 * w + lane, mrows - 1)) * kb;
   const uint8_t* bs = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * kb;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
-  auto issue = [&](int t) {
-    const uint32_t u = lds0 + (uint32_t)(t & 1) * STAGE;
-#pragma unroll
-    for (int i = 0; i < CA; ++i) dma16_at(ap[i] + 64 * (int64_t)t, u + 1024u * (uint32_t)(CA * w + i));
-#pragma unroll
-    for (int i = 0; i < CB; ++i) dma16_at(bp[i] + 64 * (int64_t)t, u + UA + 1024u * (uint32_t)(CB * w + i));
-    if (w < FI) dma4_at(as + 4 * t, u + UA + UB + 256u * (uint32_t)w);
-    dma4_at(bs + 4 * t, u + UA + UB + BM * 4 + 256u * (uint32_t)w);
+  auto copy_a = [&](int t, int i) {
+    const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
+    if (i < CA) dma16_at(ap[i] + 64 * (int64_t)t, u + 1024u * (uint32_t)(CA * w + i));
+    else dma4_at(as + 4 * t, u + UA + UB + 256u * (uint32_t)w);
+  };
+  auto copy_b = [&](int t, int i) {
+    const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
+    if (i < CB) dma16_at(bp[i] + 64 * (int64_t)t, u + UA + 1024u * (uint32_t)(CB * w + i));
+    else dma4_at(bs + 4 * t, u + UA + UB + 1024 + 256u * (uint32_t)w);
   };
 
   f32x16 acc[FI][FJ];
@@ -749,45 +822,99 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
 #pragma unroll
       for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
   const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
-  auto frag = [&](uint32_t unit, int r, int sl) -> i32x8 {
-    const u32x4 p = *(const MLORA_LDS u32x4*)(base + unit + (r * 4 + ((2 * sl + half) ^ ((r >> 2) & 3))) * 16);
-    return __builtin_bit_cast(i32x8, __builtin_shufflevector(p, zero4(), 0, 1, 2, 3, 4, 5, 6, 7));
+  u32x4 fa[2][FI], fb[2][FJ];
+  int sa[FI], sb[FJ], na[FI], nb[FJ];   // scales of the step, and of the next one
+  // Lane parts of the reads; fragment f is 32 rows (2048 bytes) on.
+  uint32_t al[2], bl[2];
+#pragma unroll
+  for (int sl = 0; sl < 2; ++sl) {
+    const int c = (2 * sl + half) ^ ((l32 >> 2) & 3);
+    al[sl] = (uint32_t)(((wrow + l32) * 4 + c) * 16);
+    bl[sl] = (uint32_t)(((wcol + l32) * 4 + c) * 16 + UA);
+  }
+  // Read r of slice sl of step t: fragments in the order the first MFMAs need
+  // them, with their scales (shifted to this lane's block) on slice 0.
+  auto read = [&](int t, int sl, int r) {
+    const uint32_t u = (uint32_t)(t % NR) * STAGE;
+    if (r == 0 || (r > FJ && r < FI + FJ)) {
+      const int f = r == 0 ? 0 : r - FJ;
+      fa[sl][f] = *(const MLORA_LDS u32x4*)(base + u + al[sl] + 2048 * f);
+      if (sl == 0)
+        na[f] = (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + 4 * (wrow + 32 * f + l32)) >> (8 * half));
+    } else if (r <= FJ) {
+      const int f = r - 1;
+      fb[sl][f] = *(const MLORA_LDS u32x4*)(base + u + bl[sl] + 2048 * f);
+      if (sl == 0)
+        nb[f] =
+            (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + 1024 + 4 * (wcol + 32 * f + l32)) >> (8 * half));
+    }
   };
-
-  issue(0);
-  for (int t = 0; t < nsteps; ++t) {
-    wait_vm_barrier<0>();
-    if (t + 1 < nsteps) issue(t + 1);
-    const uint32_t u = (uint32_t)(t & 1) * STAGE;
-    int sa[FI], sb[FJ];
+  auto mma = [&](auto sl_tag, int q) {
+    constexpr int SL = decltype(sl_tag)::value;
+    const int fi = q >> 2, fj = q & 3;
+    acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        __builtin_bit_cast(i32x8, __builtin_shufflevector(fb[SL][fj], zero4(), 0, 1, 2, 3, 4, 5, 6, 7)),
+        __builtin_bit_cast(i32x8, __builtin_shufflevector(fa[SL][fi], zero4(), 0, 1, 2, 3, 4, 5, 6, 7)), acc[fi][fj], 4,
+        4, 2 * SL, sb[fj], 2 * SL, sa[fi]);
+  };
+  // Step s: slice 0 reads slice 1 and copies the A unit of step
+  // s + 3 into the stage that step s - 1 left; then step s + 1 has landed for
+  // every wave (steps s + 2 and the A unit of s + 3 may be in flight) and
+  // slice 1 reads its first slice and copies the B unit of step s + 3.  The
+  // last three steps copy nothing and wait for everything.
+  auto step = [&](int s, auto copy_tag) {
+    constexpr bool COPY = decltype(copy_tag)::value;
+    constexpr int C0 = (FI + FJ + 1) / 2, ROOM = NS - C0;
 #pragma unroll
-    for (int f = 0; f < FI; ++f)
-      sa[f] = (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + 4 * (wrow + 32 * f + l32)) >> (8 * half));
+    for (int f = 0; f < FI; ++f) sa[f] = na[f];
 #pragma unroll
-    for (int f = 0; f < FJ; ++f)
-      sb[f] = (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + BM * 4 + 4 * (wcol + 32 * f + l32)) >> (8 * half));
+    for (int f = 0; f < FJ; ++f) sb[f] = nb[f];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int sl = 0; sl < 2; ++sl) {
-      i32x8 fa[FI], fb[FJ];
+    for (int q = 0; q < NS; ++q) {
+      mma(std::integral_constant<int, 0>(), q);
+      read(s, 1, 2 * q);
+      read(s, 1, 2 * q + 1);
+      if (COPY && q >= C0) {
+        constexpr int PER = (CA + 1 + ROOM - 1) / ROOM;
 #pragma unroll
-      for (int f = 0; f < FI; ++f) fa[f] = frag(u, wrow + 32 * f + l32, sl);
-#pragma unroll
-      for (int f = 0; f < FJ; ++f) fb[f] = frag(u + UA, wcol + 32 * f + l32, sl);
-#pragma unroll
-      for (int fi = 0; fi < FI; ++fi)
-#pragma unroll
-        for (int fj = 0; fj < FJ; ++fj) {
-          if (sl == 0)
-            acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[fj], fa[fi], acc[fi][fj], 4, 4, 0, sb[fj],
-                                                                          0, sa[fi]);
-          else
-            acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[fj], fa[fi], acc[fi][fj], 4, 4, 2, sb[fj],
-                                                                          2, sa[fi]);
-        }
+        for (int j = 0; j < PER; ++j)
+          if ((q - C0) * PER + j < CA + 1) copy_a(s + 3, (q - C0) * PER + j);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_vm_barrier<COPY ? COPIES + CA + 1 : 0>();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      mma(std::integral_constant<int, 1>(), q);
+      read(s + 1, 0, 2 * q);
+      read(s + 1, 0, 2 * q + 1);
+      if (COPY && q >= C0) {
+        constexpr int PER = (CB + 1 + ROOM - 1) / ROOM;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if ((q - C0) * PER + j < CB + 1) copy_b(s + 3, (q - C0) * PER + j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  for (int t = 0; t < 3 && t < nsteps; ++t) {
+#pragma unroll
+    for (int i = 0; i <= CA; ++i) copy_a(t, i);
+#pragma unroll
+    for (int i = 0; i <= CB; ++i) copy_b(t, i);
   }
+  if (nsteps >= 3) wait_vm_barrier<2 * COPIES>();
+  else wait_vm_barrier<0>();
+#pragma unroll
+  for (int r = 0; r < FI + FJ; ++r) read(0, 0, r);
+  int s = 0;
+  for (; s + 3 < nsteps; ++s) step(s, std::true_type());
+  for (; s < nsteps; ++s) step(s, std::false_type());
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
 }
 
@@ -846,8 +973,7 @@ void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStre
 
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
-  const int64_t nN = (a.N + 255) / 256;
-  const int64_t grid = E * ((a.M + 255) / 256) * nN;
+  const int64_t grid = 8 * E * (((a.M + 255) / 256 * ((a.N + 255) / 256) + 7) / 8);
   const dim3 dg((unsigned)grid);
   if (f32) hipLaunchKernelGGL((k_expert_tile<true, NC, NC, 4, true>), dg, dim3(256), 0, s, a);
   else if (a.ma.by_order || a.mb.by_order)

@@ -24,7 +24,7 @@ struct FewTraits {
   static constexpr int NJ = WIDE ? 4 : 1;                         // accumulators per row block
   // one batch of loads covers this much of the reduction
   static constexpr int KD = FORM == W16_KC ? 128 : FORM == W16_NC ? 32 : FORM == W32_KC ? 64 : FORM == W32_NC ? 16
-                            : FORM == W4_A16 ? 128 : 512;
+                            : 512;
 };
 
 __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -165,20 +165,36 @@ __global__ __launch_bounds__(512) void k_expert_few(ExpertArgs a) {
           for (int m = 0; m < MB; ++m)
             acc[m][j] = mfma16f(__uint_as_float(wv[i][j]), __uint_as_float(xv[m][i]), acc[m][j]);
     } else if constexpr (FORM == W4_A16) {
-      // lane: block g of the batch, 32 codes in 16 bytes
-      const u32x4 cw = *reinterpret_cast<const u32x4*>(wp + k0 / 2 + 16 * g);
-      const float sc = __uint_as_float((uint32_t)ws[k0 / 32 + g] << 23);
-      u32x4 xv[MB][4];
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xv[m][i] = *reinterpret_cast<const u32x4*>(xp[m] + (int64_t)(k0 + 32 * g + 8 * i) * 2);
+      // four pieces of 128: lane block g of each, 32 codes in 16 bytes
+      u32x4 cw[4], xv[MB][4][4];
+      uint32_t sw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const u32x4 wv = bf16_of_e2m1(cw[i], sc);
+        const int k = k0 + 128 * i;
+        const int kk = k < K ? k : 0;
+        cw[i] = *reinterpret_cast<const u32x4*>(wp + kk / 2 + 16 * g);
+        sw[i] = ws[kk / 32 + g];
+      }
 #pragma unroll
-        for (int m = 0; m < MB; ++m) acc[m][0] = mfma16(wv, xv[m][i], acc[m][0]);
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + 128 * i;
+        const int kk = k < K ? k : 0;
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            xv[m][i][j] = *reinterpret_cast<const u32x4*>(xp[m] + (int64_t)(kk + 32 * g + 8 * j) * 2);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (k0 + 128 * i >= K) break;
+        const float sc = __uint_as_float(sw[i] << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x4 wv = bf16_of_e2m1(cw[i][j], sc);
+#pragma unroll
+          for (int m = 0; m < MB; ++m) acc[m][0] = mfma16(wv, xv[m][i][j], acc[m][0]);
+        }
       }
     } else {
       // four pieces of 128: lane block g of each
