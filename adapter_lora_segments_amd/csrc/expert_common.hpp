@@ -48,13 +48,9 @@ template <int BM, int GM>
 __device__ __forceinline__ RowTile row_tile(const ExpertArgs& a, int nN) {
   const int lane = threadIdx.x & 63;
   const int E = a.offsets ? a.n_experts : 1;
-  auto tiles_of = [&](int e, int& lo) {
-    if (e >= E) {
-      lo = 0;
-      return 0;
-    }
-    int hi;
-    group_rows(a, e, lo, hi);
+  auto tiles_of = [&](int e, int& lo, int& hi) {
+    lo = hi = 0;
+    if (e < E) group_rows(a, e, lo, hi);
     return (hi - lo + BM - 1) / BM;
   };
   auto scan = [&](int v) {
@@ -65,13 +61,13 @@ __device__ __forceinline__ RowTile row_tile(const ExpertArgs& a, int nN) {
     }
     return v;
   };
-  int lo = 0;
-  int cnt = tiles_of(lane, lo);        // chunk 0's; the search below starts with it
+  int lo, hi;
+  int cnt = tiles_of(lane, lo, hi);        // chunk 0's; the search below starts with it
   int inc = scan(cnt);
   int TM = __builtin_amdgcn_readlane(inc, 63);
   for (int c = 64; c < E; c += 64) {
-    int l2;
-    TM += __builtin_amdgcn_readlane(scan(tiles_of(c + lane, l2)), 63);
+    int lo2, hi2;
+    TM += __builtin_amdgcn_readlane(scan(tiles_of(c + lane, lo2, hi2)), 63);
   }
   const int T = TM * nN, b = blockIdx.x;
   const int xcd = b & 7, q = b >> 3, per = T >> 3, rem = T & 7;
@@ -86,18 +82,16 @@ __device__ __forceinline__ RowTile row_tile(const ExpertArgs& a, int nN) {
   // the group whose tiles hold tm
   for (int c = 0, before = 0; c < E; c += 64) {
     if (c > 0) {
-      cnt = tiles_of(c + lane, lo);
+      cnt = tiles_of(c + lane, lo, hi);
       inc = scan(cnt);
     }
     const uint64_t past = __ballot(before + inc > tm);
     if (past != 0) {
       const int l = __builtin_ctzll(past);
       const int first = before + __builtin_amdgcn_readlane(inc - cnt, l);
-      int glo, ghi;
-      group_rows(a, c + l, glo, ghi);
       t.e = c + l;
-      t.row0 = glo + (tm - first) * BM;
-      t.mrows = min(BM, ghi - t.row0);
+      t.row0 = __builtin_amdgcn_readlane(lo, l) + (tm - first) * BM;
+      t.mrows = min(BM, __builtin_amdgcn_readlane(hi, l) - t.row0);
       break;
     }
     before += __builtin_amdgcn_readlane(inc, 63);

@@ -423,19 +423,20 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
 // ---------------------------------------------------------------------------
 // Pipelined tile kernel for bf16 operands (and E2M1 weights): the base GEMM's
 // schedule over ragged groups.  A 64 FI x 256 tile per workgroup of four
-// waves, 64-deep steps, one unit of LDS per operand and step.  While step s is
-// computed, step s + 1 and the A unit of step s + 2 are in flight: with 32 KiB
-// units (FI = 4) five of them fill the 160 KiB, unit u in slot u mod 5; other
-// sizes hold three whole steps.
+// waves, 64-deep steps, one unit of LDS per operand and step.  The ring holds
+// as many steps as fit (at most six) and a step copies D steps ahead; with
+// 32 KiB units (FI = 4, D = 2) five units fill the 160 KiB, unit u in slot
+// u mod 5: while step s is computed, step s + 1 and the A unit of step s + 2
+// are in flight.
 //
 // A step is four 16-deep slices with fragments double buffered in registers;
 // the reads and copies sit between the MFMAs of a slice.  Step s:
-//   slices 0-1: read the next slice; copy the A unit of step s + 2;
+//   slices 0-1: read the next slice; copy the A unit of step s + D;
 //   slice 2: read slice 3; then wait until this wave's copies of step s + 1
-//     have landed (the A unit of step s + 2 may be in flight) and its reads are
-//     done, and meet the other waves: step s + 1 is complete in LDS and nobody
-//     reads step s any more;
-//   slice 3: read step s + 1's first slice; copy the B unit of step s + 2.
+//     have landed (later steps may be in flight) and its reads are done, and
+//     meet the other waves: step s + 1 is complete in LDS and nobody reads
+//     step s any more;
+//   slice 3: read step s + 1's first slice; copy the B unit of step s + D.
 // E2M1 weights: half h of a wave takes the step's 32-block h, whose 32 codes
 // are one 16-byte read per step; word ks of it becomes slice ks's eight bf16
 // by four conversions while the slice before is computed, so the weights
@@ -445,10 +446,12 @@ template <int AL, int BL, int FI, bool DW, bool GATHER>
 __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   constexpr int FJ = 4, BM = 64 * FI, BN = 256, KD = 64, NS = FI * FJ;
   constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + BN * 4 : BN * 128;
-  constexpr bool RING5 = UA == UB;
+  constexpr bool RING5 = FI == 4 && BL != F4;
+  constexpr int NR = RING5 ? 2 : (160 * 1024) / (UA + UB) > 6 ? 6 : (160 * 1024) / (UA + UB);
+  constexpr int D = RING5 ? 2 : NR - 1;                  // steps ahead that a step copies
   constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : 8;   // 1 KiB copies per wave and unit
   constexpr int CBW = CB + (BL == F4 ? 1 : 0);           // and the scale dwords
-  constexpr int RING = RING5 ? 5 * UA : 3 * (UA + UB);
+  constexpr int RING = RING5 ? 5 * UA : NR * (UA + UB);
   constexpr int LDS = DW || RING >= BM * 512 ? RING : BM * 512;   // the epilogue's bf16 tile takes BM x 512
   __shared__ u32x4 ring[LDS / 16];
 
@@ -517,7 +520,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
   auto slot = [](int u) -> uint32_t {
     if constexpr (RING5) return (uint32_t)(u % 5) * UA;
-    else return (uint32_t)((u >> 1) % 3) * (UA + UB) + ((u & 1) ? UA : 0);
+    else return (uint32_t)((u >> 1) % NR) * (UA + UB) + ((u & 1) ? UA : 0);
   };
   // Order entries of this wave's 16 k-rows of a step, by scalar loads (they
   // wait on lgkmcnt, not on the counter that tracks the copies in flight), and
@@ -652,8 +655,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   };
   // What MFMA slot q of a slice reads of slice ks (bases bs): fragments in the
   // order the first MFMAs need them, two per slot, or one where a fragment is
-  // two transposing reads or four conversions.
-  constexpr int RPS = AL == KC && BL == KC ? 2 : 1;
+  // two transposing reads or four conversions and the slice has the slots.
+  constexpr int RPS = (AL == KC && BL == KC) || FI == 1 ? 2 : 1;
   auto reads_at = [&](int q, const Bases& bs, int ks, u32x4 (&ra)[FI], u32x4 (&rb)[FJ]) {
 #pragma unroll
     for (int j = 0; j < RPS; ++j) {
@@ -690,7 +693,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     acc[q >> 2][q & 3] = mfma32(rb[q & 3], ra[q >> 2], acc[q >> 2][q & 3]);
   };
 
-  // Step kinds: 0, step s + 2 lies inside the reduction; 1, it reaches past
+  // Step kinds: 0, step s + D lies inside the reduction; 1, it reaches past
   // its end; 2, it does not exist: nothing is copied and the barrier waits for
   // every copy in flight.
   auto step_block = [&](int s, auto kind) {
@@ -698,7 +701,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     constexpr bool COPY = KIND != 2;
     const std::integral_constant<bool, KIND == 1> check{};
     Bases cur;
-    if (COPY) load_order(s + 2);
+    if (COPY) load_order(s + D);
     step_bases(s, cur, 1, 3);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -707,12 +710,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       for (int q = 0; q < NS; ++q) {
         mma(q, fa[ks & 1], fb[ks & 1]);
         reads_at(q, cur, ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
-        if (COPY && ks < 2) copies_at(q, CA / 2, [&](int j) { copy_a(s + 2, ks * (CA / 2) + j, check); });
+        if (COPY && ks < 2) copies_at(q, CA / 2, [&](int j) { copy_a(s + D, ks * (CA / 2) + j, check); });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_vm_barrier<COPY ? CA : 0>();
+    wait_vm_barrier<COPY ? (D - 2) * (CA + CBW) + CA : 0>();
     Bases nxt;
     step_bases(s + 1, nxt, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
@@ -722,17 +725,17 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       next_step_reads_at(q, nxt, s + 1, fa[0], fb[0]);
       if (COPY)
         copies_at(q, CBW, [&](int j) {
-          if (j < CB) copy_b(s + 2, j, check);
-          else copy_scales(s + 2, check);
+          if (j < CB) copy_b(s + D, j, check);
+          else copy_scales(s + D, check);
         });
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // steps 0 and 1; step 0's first slice once every wave's copies of it have landed
+  // the first D steps; step 0's first slice once every wave's copies of it have landed
   const std::integral_constant<bool, true> check{};
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < D; ++t) {
     load_order(t);
 #pragma unroll
     for (int i = 0; i < CA; ++i) copy_a(t, i, check);
@@ -740,7 +743,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     for (int i = 0; i < CB; ++i) copy_b(t, i, check);
     copy_scales(t, check);
   }
-  wait_vm_barrier<CA + CBW>();
+  wait_vm_barrier<(D - 1) * (CA + CBW)>();
   Bases b0;
   step_bases(0, b0, 0, 0);
 #pragma unroll
@@ -750,8 +753,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
 #pragma unroll
   for (int f = 0; f < FJ; ++f) read_b(b0, 0, f, fb[0]);
   int s = 0;
-  for (; (s + 3) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
-  for (; s + 2 < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
+  for (; (s + D + 1) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
+  for (; s + D < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
   for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   if constexpr (DW) store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
@@ -766,16 +769,20 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
 // r + 32 h holds row r's 32-block h of a 64-deep slice (16 bytes, the low
 // nibble first) and supplies its scale.  A step is two slices, 1024 cycles of
 // MFMA at FI = 4, less than a copy's latency: four stages keep three steps in
-// flight.
+// flight.  A copy of scale dwords touches a row per lane, four times the
+// addresses of a copy of codes; S16 (K a multiple of 512, so a row's 16 scale
+// bytes are aligned) copies four steps' scales at once instead.
 // ---------------------------------------------------------------------------
-template <int FI>
+template <int FI, bool S16>
 __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
   constexpr int FJ = 4, BM = 64 * FI, BN = 256;
   constexpr int UA = BM * 64, UB = BN * 64, CA = FI, CB = 4, NS = FI * FJ;
   constexpr int NR = 4;                               // stages
-  constexpr int STAGE = UA + UB + 1024 + BN * 4;      // scale dwords: 256 of A (BM used), 256 of B
-  constexpr int COPIES = CA + CB + 2;                 // per wave and step
-  __shared__ u32x4 ring[(NR * STAGE > BM * 512 ? NR * STAGE : BM * 512) / 16];
+  constexpr int STAGE = UA + UB + (S16 ? 0 : 2048);   // with the scale dwords of 256 rows of A and of B
+  constexpr int SCL = NR * STAGE;                     // S16: two chunks of 16 scale bytes for 256 + 256 rows
+  constexpr int COPIES = CA + CB + (S16 ? 0 : 2);     // per wave and step
+  constexpr int LDS = SCL + (S16 ? 16384 : 0);
+  __shared__ u32x4 ring[(LDS > BM * 512 ? LDS : BM * 512) / 16];
   const Tile tl = find_tile<BM, false>(g);
   if (tl.mrows <= 0) return;
   const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, n0 = tl.n0;
@@ -803,15 +810,32 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
   const uint8_t* as = g.a_scale + source_row(g, g.ma, row0 + min(64 * w + lane, mrows - 1)) * kb;
   const uint8_t* bs = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * kb;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
+  const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
   auto copy_a = [&](int t, int i) {
     const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
-    if (i < CA) dma16_at(ap[i] + 64 * (int64_t)t, u + 1024u * (uint32_t)(CA * w + i));
-    else dma4_at(as + 4 * t, u + UA + UB + 256u * (uint32_t)w);
+    if (i < CA) {
+      dma16_at(ap[i] + 64 * (int64_t)t, u + 1024u * (uint32_t)(CA * w + i));
+    } else if constexpr (S16) {
+      if ((t & 3) == 0) dma16_at(as + 4 * t, lds0 + SCL + 8192u * ((t >> 2) & 1) + 1024u * (uint32_t)w);
+    } else {
+      dma4_at(as + 4 * t, u + UA + UB + 256u * (uint32_t)w);
+    }
   };
   auto copy_b = [&](int t, int i) {
     const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
-    if (i < CB) dma16_at(bp[i] + 64 * (int64_t)t, u + UA + 1024u * (uint32_t)(CB * w + i));
-    else dma4_at(bs + 4 * t, u + UA + UB + 1024 + 256u * (uint32_t)w);
+    if (i < CB) {
+      dma16_at(bp[i] + 64 * (int64_t)t, u + UA + 1024u * (uint32_t)(CB * w + i));
+    } else if constexpr (S16) {
+      if ((t & 3) == 0) dma16_at(bs + 4 * t, lds0 + SCL + 4096 + 8192u * ((t >> 2) & 1) + 1024u * (uint32_t)w);
+    } else {
+      dma4_at(bs + 4 * t, u + UA + UB + 1024 + 256u * (uint32_t)w);
+    }
+  };
+  // Scale dword of row r of operand op for step t.
+  auto scale_at = [&](int t, int op, int r) -> uint32_t {
+    if constexpr (S16)
+      return *(const MLORA_LDS uint32_t*)(base + SCL + 8192 * ((t >> 2) & 1) + 4096 * op + 16 * r + 4 * (t & 3));
+    else return *(const MLORA_LDS uint32_t*)(base + (uint32_t)(t % NR) * STAGE + UA + UB + 1024 * op + 4 * r);
   };
 
   f32x16 acc[FI][FJ];
@@ -821,7 +845,6 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
     for (int b = 0; b < FJ; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
-  const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
   u32x4 fa[2][FI], fb[2][FJ];
   int sa[FI], sb[FJ], na[FI], nb[FJ];   // scales of the step, and of the next one
   // Lane parts of the reads; fragment f is 32 rows (2048 bytes) on.
@@ -840,13 +863,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
       const int f = r == 0 ? 0 : r - FJ;
       fa[sl][f] = *(const MLORA_LDS u32x4*)(base + u + al[sl] + 2048 * f);
       if (sl == 0)
-        na[f] = (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + 4 * (wrow + 32 * f + l32)) >> (8 * half));
+        na[f] = (int)(scale_at(t, 0, wrow + 32 * f + l32) >> (8 * half));
     } else if (r <= FJ) {
       const int f = r - 1;
       fb[sl][f] = *(const MLORA_LDS u32x4*)(base + u + bl[sl] + 2048 * f);
       if (sl == 0)
-        nb[f] =
-            (int)(*(const MLORA_LDS uint32_t*)(base + u + UA + UB + 1024 + 4 * (wcol + 32 * f + l32)) >> (8 * half));
+        nb[f] = (int)(scale_at(t, 1, wcol + 32 * f + l32) >> (8 * half));
     }
   };
   auto mma = [&](auto sl_tag, int q) {
@@ -884,7 +906,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
       __builtin_amdgcn_sched_barrier(0);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_vm_barrier<COPY ? COPIES + CA + 1 : 0>();
+    // (counts without the scale copies of every fourth step: a stricter wait)
+    wait_vm_barrier<COPY ? COPIES + CA + (S16 ? 0 : 1) : 0>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
@@ -927,7 +950,9 @@ template <bool F32, int BL>
 void rows_size(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
   if (mean <= 96) {
-    hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)rows_grid(a, 64));
+    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 1, false>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 1, false, false>), grid, dim3(256), 0, s, a);
   } else if (mean <= 384) {
     const dim3 grid((unsigned)rows_grid(a, 128));
     if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 2, false>), grid, dim3(256), 0, s, a);
@@ -942,7 +967,8 @@ template <int FI>
 void mx4_tile(const ExpertArgs& a, hipStream_t s) {
   const int64_t nN = (a.N + 255) / 256;
   const int64_t grid = max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, 64 * FI) * nN;
-  hipLaunchKernelGGL((k_expert_mx4<FI>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  if (a.K % 512 == 0) hipLaunchKernelGGL((k_expert_mx4<FI, true>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_expert_mx4<FI, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
 }
 
 }  // namespace
