@@ -44,7 +44,11 @@ __device__ __forceinline__ void dma16_sv(uint64_t sbase, uint32_t voff, uint32_t
 //   F4: E2M1 codes along the reduction, 32 bytes (64 elements) per tile row,
 //       chunk h of row r at h ^ ((r >> 3) & 1), and one dword of scale codes
 //       per row that covers the step (it holds 128 elements' scales).
-enum { KC = 0, NC = 1, F4 = 2 };
+//   X4: E2M1 codes along the reduction on both sides, for the scaled matrix
+//       instruction: a KC unit of 256 codes per row, and 8 scale bytes per row
+//       and step in LDS of their own.  X4D: the same for rows whose scale
+//       codes are aligned to dwords only.
+enum { KC = 0, NC = 1, F4 = 2, X4 = 3, X4D = 4 };
 
 // Chunk swizzle of an n-contiguous bf16 row (see the base GEMM): XOR of 4, 8
 // and 9 over bits 0, 1 and 3 of the k-row, which gives every transposing read
@@ -115,9 +119,9 @@ __device__ __forceinline__ int out_row(const ExpertArgs& g, const Tile& t, int m
 // the rows a fragment writes and the granules a row read takes both spread
 // over the banks and every store writes whole 512-byte rows.
 template <int FI, bool DW>
-__device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][4], const Tile& t, int w,
-                                          int lane) {
-  const int half = lane >> 5, l32 = lane & 31, wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+__device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][4], const Tile& t, int wrow,
+                                          int wcol, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
 #pragma unroll
   for (int fi = 0; fi < FI; ++fi) {
     const int m = wrow + 32 * fi + l32;
@@ -186,16 +190,16 @@ __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
   for (int m = threadIdx.x >> 6; m < t.mrows; m += 4)
     *reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n) = f32x4{0.f, 0.f, 0.f, 0.f};
 }
-template <int FI>
-__device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&acc)[FI][4], char* ct, const Tile& t,
-                                           int w, int lane) {
-  const int half = lane >> 5, l32 = lane & 31, wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+template <int BM, int FIW, int FJW>
+__device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&acc)[FIW][FJW], char* ct, const Tile& t,
+                                           int wrow, int wcol, int w, int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
   __syncthreads();
 #pragma unroll
-  for (int fi = 0; fi < FI; ++fi) {
+  for (int fi = 0; fi < FIW; ++fi) {
     const int m = wrow + 32 * fi + l32;
 #pragma unroll
-    for (int fj = 0; fj < 4; ++fj)
+    for (int fj = 0; fj < FJW; ++fj)
 #pragma unroll
       for (int gg = 0; gg < 4; ++gg) {
         const int c = (wcol >> 3) + 4 * fj + gg;
@@ -208,8 +212,8 @@ __device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&a
   __syncthreads();
   const int gc = lane & 31, n = t.n0 + 8 * gc;
 #pragma unroll 4
-  for (int it = 0; it < 8 * FI; ++it) {
-    const int m = 16 * FI * w + 2 * it + half;
+  for (int it = 0; it < BM / 8; ++it) {
+    const int m = BM / 4 * w + 2 * it + half;
     const int row = out_row(g, t, m);
     const u32x4 x = *reinterpret_cast<const u32x4*>(ct + m * 512 + 16 * (gc ^ (m & 31)));
     if (row >= 0 && n < g.N) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (int64_t)row * g.ldc + n) = x;
@@ -219,20 +223,21 @@ __device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&a
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Tile kernel.  A workgroup of four waves (2 x 2) makes a 64 FI x 256 tile,
-// each wave 32 FI x 128 in accumulators.  Steps of 64 bf16 (32 fp32) of the
-// reduction are copied straight from global memory into LDS, double
-// buffered: step t + 1 is in flight while step t is computed.
+// fp32 tile kernel.  A workgroup of four waves (2 x 2) makes a 64 FI x 256
+// tile, each wave 32 FI x 128 in accumulators.  Steps of 32 of the reduction
+// are copied straight from global memory into LDS, double buffered: step t + 1
+// is in flight while step t is computed.  fp32 matrix instructions run at a
+// sixteenth of the bf16 rate, so a step's 16384 cycles (FI = 4) hide its copies
+// without a deeper ring.
 //   DW = false: C[rc(s)][n] over the rows of one group (rows form)
 //   DW = true:  C_e[m][n] = sum over the group's rows (both operands NC)
 // ---------------------------------------------------------------------------
-template <bool F32, int AL, int BL, int FI, bool DW>
-__global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
-  constexpr int FJ = 4, BM = 64 * FI, BN = 256, ESZ = F32 ? 4 : 2, EPC = 16 / ESZ, KD = 128 / ESZ;
-  constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + BN * 4 : BN * 128;  // bytes of a step's units
-  constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : UB / 4096;              // 1 KiB copies per wave
-  constexpr int EPI = F32 || DW ? 0 : BM * 512;                             // the epilogue's bf16 tile
-  __shared__ u32x4 ring[(2 * (UA + UB) > EPI ? 2 * (UA + UB) : EPI) / 16];
+template <int AL, int BL, int FI, bool DW>
+__global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
+  constexpr int FJ = 4, BM = 64 * FI, BN = 256, KD = 32;
+  constexpr int UA = BM * 128, UB = BN * 128;          // bytes of a step's units
+  constexpr int CA = UA / 4096, CB = UB / 4096;        // 1 KiB copies per wave
+  __shared__ u32x4 ring[2 * (UA + UB) / 16];
 
   const Tile tl = find_tile<BM, DW>(g);
   if (tl.mrows <= 0) return;
@@ -244,61 +249,39 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
-
   const uint8_t* const Be = DW ? g.B : g.B + (int64_t)e * g.b_expert;
   const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
 
-  // Row pointers of the k-contiguous operands' copies: copy i of a wave takes
-  // tile rows 8 (CA w + i) + lane / 8, LDS position lane % 8.
+  // k-contiguous: copy i of a wave takes tile rows 8 (C w + i) + lane / 8, LDS
+  // position lane % 8.
   const uint8_t* ap[CA];
-  int ac[CA];
-  if constexpr (AL == KC) {
-#pragma unroll
-    for (int i = 0; i < CA; ++i) {
-      const int r = 8 * (CA * w + i) + (lane >> 3);
-      ac[i] = (lane & 7) ^ kx8(r);
-      ap[i] = g.A + (source_row(g, g.ma, row0 + min(r, mrows - 1)) * g.lda) * ESZ + 16 * ac[i];
-    }
-  }
   const uint8_t* bp[CB];
-  int bc[CB];
-  if constexpr (BL == KC) {
+  int ac[CA], bc[CB];
 #pragma unroll
-    for (int i = 0; i < CB; ++i) {
-      const int r = 8 * (CB * w + i) + (lane >> 3);
-      bc[i] = (lane & 7) ^ kx8(r);
-      bp[i] = Be + ((int64_t)min(n0 + r, g.N - 1) * g.ldb) * ESZ + 16 * bc[i];
-    }
+  for (int i = 0; i < CA; ++i) {
+    const int r = 8 * (CA * w + i) + (lane >> 3);
+    ac[i] = (lane & 7) ^ kx8(r);
+    ap[i] = AL == KC ? g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * g.lda * 4 + 16 * ac[i] : g.A;
   }
-  const uint8_t* sp = nullptr;
-  if constexpr (BL == F4) {
-    // copy i: tile rows 32 (2 w + i) + lane / 2, position lane % 2
 #pragma unroll
-    for (int i = 0; i < CB; ++i) {
-      const int r = 32 * (2 * w + i) + (lane >> 1);
-      bc[i] = (lane & 1) ^ ((r >> 3) & 1);
-      bp[i] = Be + (int64_t)min(n0 + r, g.N - 1) * (g.ldb / 2) + 16 * bc[i];
-    }
-    sp = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
+  for (int i = 0; i < CB; ++i) {
+    const int r = 8 * (CB * w + i) + (lane >> 3);
+    bc[i] = (lane & 7) ^ kx8(r);
+    bp[i] = BL == KC ? Be + (int64_t)min(n0 + r, g.N - 1) * g.ldb * 4 + 16 * bc[i] : Be;
   }
-
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
 
-  // Copies of an n-contiguous unit of RW columns from column c0 of `base`.
-  auto copy_nc = [&](auto rw_tag, const uint8_t* base, int64_t ld, int c0, int cmax, const RowMap& map, bool rows_map,
+  // Copies of an n-contiguous unit of RW columns from column c0 of `from`.
+  auto copy_nc = [&](auto rw_tag, const uint8_t* from, int64_t ld, int c0, int cmax, const RowMap& map, bool mapped,
                      int t, uint32_t lds) {
-    constexpr int RW = decltype(rw_tag)::value, CPR = RW * ESZ / 16, RPC = 64 / CPR, NCP = RW / 32;
+    constexpr int RW = decltype(rw_tag)::value, CPR = RW / 4, RPC = 64 / CPR, NCP = RW / 32;
 #pragma unroll
     for (int i = 0; i < NCP; ++i) {
       const int kr = RPC * (NCP * w + i) + lane / CPR;
-      const int c = (lane % CPR) ^ (F32 ? nx32(kr) : nx16(kr));
+      const int col = min(c0 + 4 * ((lane % CPR) ^ nx32(kr)), cmax - 4);
       const int k = t * KD + kr;
-      const int col = min(c0 + EPC * c, cmax - EPC);
       const uint8_t* src = zero;
-      if (k < klen) {
-        const int64_t row = rows_map ? source_row(g, map, row0 + k) : (int64_t)k;
-        src = base + (row * ld + col) * ESZ;
-      }
+      if (k < klen) src = from + ((mapped ? source_row(g, map, row0 + k) : (int64_t)k) * ld + col) * 4;
       dma16_at(src, lds + 1024u * (uint32_t)(NCP * w + i));
     }
   };
@@ -307,20 +290,16 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
     if constexpr (AL == KC) {
 #pragma unroll
       for (int i = 0; i < CA; ++i)
-        dma16_at(t * KD + EPC * ac[i] < klen ? ap[i] + 128 * (int64_t)t : zero, ua + 1024u * (uint32_t)(CA * w + i));
+        dma16_at(t * KD + 4 * ac[i] < klen ? ap[i] + 128 * (int64_t)t : zero, ua + 1024u * (uint32_t)(CA * w + i));
     } else {
       copy_nc(std::integral_constant<int, BM>(), g.A, g.lda, m0, g.M, g.ma, true, t, ua);
     }
     if constexpr (BL == KC) {
 #pragma unroll
       for (int i = 0; i < CB; ++i)
-        dma16_at(t * KD + EPC * bc[i] < klen ? bp[i] + 128 * (int64_t)t : zero, ub + 1024u * (uint32_t)(CB * w + i));
-    } else if constexpr (BL == NC) {
-      copy_nc(std::integral_constant<int, BN>(), Be, g.ldb, n0, g.N, g.mb, DW, t, ub);
+        dma16_at(t * KD + 4 * bc[i] < klen ? bp[i] + 128 * (int64_t)t : zero, ub + 1024u * (uint32_t)(CB * w + i));
     } else {
-#pragma unroll
-      for (int i = 0; i < CB; ++i) dma16_at(bp[i] + 32 * (int64_t)t, ub + 1024u * (uint32_t)(CB * w + i));
-      dma4_at(sp + 4 * (t >> 1), ub + BN * 32 + 256u * (uint32_t)w);
+      copy_nc(std::integral_constant<int, BN>(), Be, g.ldb, n0, g.N, g.mb, DW, t, ub);
     }
   };
 
@@ -333,46 +312,21 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
       for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
 
   const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
-  // Fragment of slice ks: eight bf16 (four fp32) of the reduction per lane.
-  // F4 weights: half h of the wave takes the step's block h, so slice ks of
-  // the k-contiguous operand is chunk 4 h + ks instead of 2 ks + h.
-  auto frag_kc = [&](uint32_t unit, int r, int ks) {
-    const int c = BL == F4 ? 4 * half + ks : 2 * ks + half;
-    return *(const MLORA_LDS u32x4*)(base + unit + (r * 8 + (c ^ kx8(r))) * 16);
-  };
-  auto frag_nc = [&](auto rw_tag, uint32_t unit, int n, int ks) {
-    constexpr int RW = decltype(rw_tag)::value, CPR = RW * ESZ / 16;
+  // Four values of the reduction per lane: slice ks, half h holds 8 ks + 4 h ..
+  auto frag = [&](auto kc_tag, auto rw_tag, uint32_t unit, int r0, int ks) {
+    constexpr int CPR = decltype(rw_tag)::value / 4;
+    const int r = r0 + l32;
     u32x4 out;
-    if constexpr (F32) {
+    if constexpr (decltype(kc_tag)::value) {
+      out = *(const MLORA_LDS u32x4*)(base + unit + (r * 8 + ((2 * ks + half) ^ kx8(r))) * 16);
+    } else {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int kr = 8 * ks + 4 * half + x, col = n + l32;
-        out[x] = *(const MLORA_LDS uint32_t*)(base + unit + (kr * CPR + ((col >> 2) ^ nx32(kr))) * 16 + 4 * (col & 3));
-      }
-    } else {
-      typedef short s16x4 __attribute__((ext_vector_type(4)));
-      const int gq = lane >> 4, s = lane & 15;
-      const int col = n + 16 * (gq & 1) + 4 * (s & 3);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kr = 16 * ks + 8 * (gq >> 1) + (s >> 2) + 4 * h;
-        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (MLORA_LDS s16x4*)(base + unit + (kr * CPR + ((col >> 3) ^ nx16(kr))) * 16 + 2 * (col & 7)));
-        const u32x2 u = __builtin_bit_cast(u32x2, v);
-        out[2 * h] = u[0];
-        out[2 * h + 1] = u[1];
+        const int kr = 8 * ks + 4 * half + x;
+        out[x] = *(const MLORA_LDS uint32_t*)(base + unit + (kr * CPR + ((r >> 2) ^ nx32(kr))) * 16 + 4 * (r & 3));
       }
     }
     return out;
-  };
-  auto mma = [&](f32x16& c, const u32x4& a, const u32x4& b) {
-    if constexpr (F32) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[x]), __uint_as_float(b[x]), c, 0, 0, 0);
-    } else {
-      c = mfma32(a, b, c);
-    }
   };
 
   issue(0);
@@ -381,43 +335,29 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
     wait_vm_barrier<0>();
     if (t + 1 < nsteps) issue(t + 1);
     const uint32_t ua = (uint32_t)(t & 1) * (UA + UB), ub = ua + UA;
-    u32x4 codes[FJ];
-    float scale[FJ];
-    if constexpr (BL == F4) {
-#pragma unroll
-      for (int f = 0; f < FJ; ++f) {
-        const int r = wcol + 32 * f + l32;
-        codes[f] = *(const MLORA_LDS u32x4*)(base + ub + (r * 2 + (half ^ ((r >> 3) & 1))) * 16);
-        const uint32_t sw = *(const MLORA_LDS uint32_t*)(base + ub + BN * 32 + 4 * r);
-        scale[f] = __uint_as_float(((sw >> (16 * (t & 1) + 8 * half)) & 255u) << 23);
-      }
-    }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       u32x4 fa[FI], fb[FJ];
 #pragma unroll
-      for (int f = 0; f < FI; ++f) {
-        if constexpr (AL == KC) fa[f] = frag_kc(ua, wrow + 32 * f + l32, ks);
-        else fa[f] = frag_nc(std::integral_constant<int, BM>(), ua, wrow + 32 * f, ks);
-      }
+      for (int f = 0; f < FI; ++f)
+        fa[f] = frag(std::integral_constant<bool, AL == KC>(), std::integral_constant<int, BM>(), ua, wrow + 32 * f, ks);
 #pragma unroll
-      for (int f = 0; f < FJ; ++f) {
-        if constexpr (BL == KC) fb[f] = frag_kc(ub, wcol + 32 * f + l32, ks);
-        else if constexpr (BL == NC) fb[f] = frag_nc(std::integral_constant<int, BN>(), ub, wcol + 32 * f, ks);
-        else fb[f] = bf16_of_e2m1(codes[f][ks], scale[f]);
-      }
+      for (int f = 0; f < FJ; ++f)
+        fb[f] = frag(std::integral_constant<bool, BL == KC>(), std::integral_constant<int, BN>(), ub, wcol + 32 * f, ks);
 #pragma unroll
-      for (int fi = 0; fi < FI; ++fi)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int fj = 0; fj < FJ; ++fj) mma(acc[fi][fj], fb[fj], fa[fi]);
+        for (int fi = 0; fi < FI; ++fi)
+#pragma unroll
+          for (int fj = 0; fj < FJ; ++fj)
+            acc[fi][fj] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(fb[fj][x]), __uint_as_float(fa[fi][x]),
+                                                               acc[fi][fj], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
     // this wave's reads are done before the next barrier lets others overwrite
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-
-  if constexpr (F32 || DW) store_f32<FI, DW>(g, acc, tl, w, lane);
-  else store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+  store_f32<FI, DW>(g, acc, tl, wrow, wcol, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -444,15 +384,23 @@ __global__ __launch_bounds__(256, 1) void k_expert_tile(ExpertArgs g) {
 // ---------------------------------------------------------------------------
 template <int AL, int BL, int FI, bool DW, bool GATHER>
 __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
-  constexpr int FJ = 4, BM = 64 * FI, BN = 256, KD = 64, NS = FI * FJ;
+  constexpr bool S4 = AL >= X4, S16 = AL == X4;          // both operands E2M1; their scales' alignment
+  constexpr bool AK = AL != NC, BK = BL == KC || S4;     // k-contiguous 128-byte rows
+  constexpr int BM = 64 * FI, BN = 256, KD = S4 ? 256 : 64, EPC = S4 ? 32 : 8;
+  // Waves along M: with E2M1 weights each wave decodes its own columns, so the
+  // four waves share the columns out and all take every row.
+  constexpr int WM = BL == F4 ? 1 : 2, FIW = BM / 32 / WM, FJW = BN / 32 / (4 / WM), NS = FIW * FJW;
   constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + BN * 4 : BN * 128;
-  constexpr bool RING5 = FI == 4 && BL != F4;
-  constexpr int NR = RING5 ? 2 : (160 * 1024) / (UA + UB) > 6 ? 6 : (160 * 1024) / (UA + UB);
-  constexpr int D = RING5 ? 2 : NR - 1;                  // steps ahead that a step copies
+  // Ring: five units (RING5), four units (RING4: the scales take the rest), or
+  // NR whole steps; D: steps ahead that a step copies.
+  constexpr bool RING5 = FI == 4 && !S4 && BL != F4, RING4 = FI == 4 && S4;
+  constexpr int SCL = S4 ? 16384 : 0, FIT = (160 * 1024 - SCL) / (UA + UB);
+  constexpr int NR = RING5 || RING4 ? 2 : FIT > 6 ? 6 : FIT;
+  constexpr int D = RING5 || RING4 ? 2 : NR - 1;
   constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : 8;   // 1 KiB copies per wave and unit
   constexpr int CBW = CB + (BL == F4 ? 1 : 0);           // and the scale dwords
   constexpr int RING = RING5 ? 5 * UA : NR * (UA + UB);
-  constexpr int LDS = DW || RING >= BM * 512 ? RING : BM * 512;   // the epilogue's bf16 tile takes BM x 512
+  constexpr int LDS = DW || RING + SCL >= BM * 512 ? RING + SCL : BM * 512;   // the epilogue's bf16 tile takes BM x 512
   __shared__ u32x4 ring[LDS / 16];
 
   const Tile tl = find_tile<BM, DW>(g);
@@ -464,62 +412,64 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
-  const int wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+  const int wrow = WM == 2 ? 32 * FIW * (w >> 1) : 0, wcol = WM == 2 ? 128 * (w & 1) : 64 * w;
   const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
   const uint8_t* const Be = DW ? g.B : g.B + (int64_t)e * g.b_expert;
+  // bytes of a row of either operand
+  const int64_t arow = S4 ? g.lda / 2 : g.lda * 2, brow = BL == F4 || S4 ? g.ldb / 2 : g.ldb * 2;
 
   // Copy sources.  k-contiguous: copy i of a wave takes tile rows 8 (C w + i)
   // + lane / 8 at LDS position lane % 8, which holds chunk (lane % 8) ^
   // kx8(row).  n-contiguous: k-rows RPC (C w + i) + lane / CPR, position lane
   // % CPR, chunk ^ nx16(k-row).
   constexpr int CPRA = BM / 8, RPCA = 64 / CPRA, CPRB = BN / 8, RPCB = 64 / CPRB;
-  const uint8_t* ap[AL == KC ? CA : 1];  // rows of A anywhere: one pointer per copy
+  const uint8_t* ap[AK ? CA : 1];  // rows of A anywhere: one pointer per copy
   uint32_t ao[CA], bo[CB];               // else byte offsets from a base that advances by steps
   int ac[CA], bc[CB];                    // KC: chunk; NC: k-row of the step
 #pragma unroll
   for (int i = 0; i < CA; ++i) {
-    if constexpr (AL == KC) {
+    if constexpr (AK) {
       const int r = 8 * (CA * w + i) + (lane >> 3);
       ac[i] = (lane & 7) ^ kx8(r);
       ao[i] = 0;
-      ap[i] = g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * g.lda * 2 + 16 * ac[i];
+      ap[i] = g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * arow + 16 * ac[i];
     } else {
       ac[i] = RPCA * (CA * w + i) + lane / CPRA;
       const int col = min(m0 + 8 * ((lane % CPRA) ^ nx16(ac[i])), g.M - 8);
-      ao[i] = GATHER ? (uint32_t)(col * 2) : (uint32_t)(((int64_t)ac[i] * g.lda + col) * 2);
+      ao[i] = (uint32_t)((GATHER ? 0 : ac[i] * arow) + col * 2);
     }
   }
 #pragma unroll
   for (int i = 0; i < CB; ++i) {
-    if constexpr (BL == KC) {
+    if constexpr (BK) {
       const int r = 8 * (CB * w + i) + (lane >> 3);
       bc[i] = (lane & 7) ^ kx8(r);
-      bo[i] = (uint32_t)((int64_t)(min(n0 + r, g.N - 1) - n0) * g.ldb * 2 + 16 * bc[i]);
+      bo[i] = (uint32_t)((min(n0 + r, g.N - 1) - n0) * brow + 16 * bc[i]);
     } else if constexpr (BL == NC) {
       bc[i] = RPCB * (CB * w + i) + lane / CPRB;
       const int col = min(n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
-      bo[i] = GATHER ? (uint32_t)(col * 2) : (uint32_t)(((int64_t)bc[i] * g.ldb + (col - n0)) * 2);
+      bo[i] = (uint32_t)(GATHER ? col * 2 : bc[i] * brow + (col - n0) * 2);
     } else {
       const int r = 32 * (2 * w + i) + (lane >> 1);
       bc[i] = 0;
-      bo[i] = (uint32_t)((int64_t)(min(n0 + r, g.N - 1) - n0) * (g.ldb / 2) +
-                         16 * ((lane & 1) ^ ((r >> 3) & 1)));
+      bo[i] = (uint32_t)((min(n0 + r, g.N - 1) - n0) * brow + 16 * ((lane & 1) ^ ((r >> 3) & 1)));
     }
   }
+  // scale codes: F4 and X4 rows of B, wave w copying those of rows 64 w ..; X4 rows of A the same way
   const uint8_t* sp = nullptr;
-  if constexpr (BL == F4) sp = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
+  const uint8_t* sq = nullptr;
+  if constexpr (BL == F4 || S4) sp = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
+  if constexpr (S4) sq = g.a_scale + source_row(g, g.ma, row0 + min(64 * w + lane, mrows - 1)) * (g.lda / 32);
   // bases of step 0 and bytes per step
-  const uint8_t* const baseA = AL == NC && !GATHER ? g.A + (int64_t)row0 * g.lda * 2 : g.A;
-  const uint8_t* const baseB =
-      BL == KC ? Be + (int64_t)n0 * g.ldb * 2
-               : BL == F4 ? Be + (int64_t)n0 * (g.ldb / 2)
-                          : (DW && !GATHER ? Be + ((int64_t)row0 * g.ldb + n0) * 2 : (DW ? Be : Be + (int64_t)n0 * 2));
-  const int64_t stepA = (int64_t)KD * g.lda * 2;
-  const int64_t stepB = BL == KC ? 128 : BL == F4 ? 32 : (int64_t)KD * g.ldb * 2;
+  const uint8_t* const baseA = AL == NC && !GATHER ? g.A + row0 * arow : g.A;
+  const uint8_t* const baseB = BL != NC ? Be + n0 * brow : (GATHER ? Be : Be + (DW ? row0 * brow : 0) + n0 * 2);
+  const int64_t stepA = KD * arow;
+  const int64_t stepB = BK ? 128 : BL == F4 ? 32 : KD * brow;
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
   auto slot = [](int u) -> uint32_t {
     if constexpr (RING5) return (uint32_t)(u % 5) * UA;
+    else if constexpr (RING4) return (uint32_t)(u & 3) * UA;
     else return (uint32_t)((u >> 1) % NR) * (UA + UB) + ((u & 1) ? UA : 0);
   };
   // Order entries of this wave's 16 k-rows of a step, by scalar loads (they
@@ -533,12 +483,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       for (int j = 0; j < 16; ++j) oidx[j] = ldc(g.order + row0 + min(t * KD + 16 * w + j, klen - 1));
     }
   };
-  auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t ld, int i, int t) -> const uint8_t* {
+  auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t row_bytes, int i, int t) -> const uint8_t* {
     const int k = row0 + t * KD + 16 * w + 2 * i;
     auto at = [&](int h) -> int64_t {
       return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], g.rows), map.div)
                            : (int64_t)(k + h)) *
-             ld * 2;
+             row_bytes;
     };
     const int64_t r0 = at(0), r1 = at(1);
     return from + (half ? r1 : r0);
@@ -547,11 +497,11 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   // reduction, and what does reads zeros.
   auto copy_a = [&](int t, int i, auto check) {
     const uint32_t lds = lds0 + slot(2 * t) + 1024u * (uint32_t)(CA * w + i);
-    if constexpr (AL == KC) {
+    if constexpr (AK) {
       const uint8_t* src = ap[i] + 128 * (int64_t)t;
-      dma16_at(!check.value || t * KD + 8 * ac[i] < klen ? src : zero, lds);
+      dma16_at(!check.value || t * KD + EPC * ac[i] < klen ? src : zero, lds);
     } else if constexpr (GATHER) {
-      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, g.ma, g.lda, i, t) + ao[i] : zero, lds);
+      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, g.ma, arow, i, t) + ao[i] : zero, lds);
     } else if constexpr (check.value) {
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseA + t * stepA));
       dma16_at(t * KD + ac[i] < klen ? at + ao[i] : zero, lds);
@@ -562,26 +512,49 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   auto copy_b = [&](int t, int i, auto check) {
     const uint32_t lds = lds0 + slot(2 * t + 1) + 1024u * (uint32_t)(CB * w + i);
     if constexpr (BL == NC && GATHER) {
-      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, g.mb, g.ldb, i, t) + bo[i] : zero, lds);
+      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, g.mb, brow, i, t) + bo[i] : zero, lds);
     } else if constexpr (check.value) {
-      const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + 8 * bc[i] < klen;
+      const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + EPC * bc[i] < klen;
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseB + t * stepB));
       dma16_at(on ? at + bo[i] : zero, lds);
     } else {
       dma16_sv(uniform64(baseB + t * stepB), bo[i], lds);
     }
   };
+  // X4 scale codes: 8 bytes per row and step.  A copy of dwords touches a row
+  // per lane, four times the addresses of a copy of codes, so where a row's 16
+  // bytes are aligned (S16: K a multiple of 512) two steps' codes are copied at
+  // once: [chunk & 1][operand][row] of 16 bytes; else [step & 3][dword]
+  // [operand][row] of 4.  (The waits below count neither: they are stricter
+  // by what is in flight.)
   auto copy_scales = [&](int t, auto check) {
-    if constexpr (BL == F4)
+    if constexpr (BL == F4) {
       dma4_at(!check.value || t * KD < klen ? sp + 4 * (t >> 1) : zero,
               lds0 + slot(2 * t + 1) + BN * 32 + 256u * (uint32_t)w);
+    } else if constexpr (S4) {
+      if constexpr (S16) {
+        // even steps: A's codes of the two steps from t on; odd steps: B's of
+        // the two after t, so every step has one copy and no branch
+        const int odd = t & 1, c = (t + 1) >> 1;
+        dma16_at(c * 512 < klen ? (odd ? sp : sq) + 16 * c : zero,
+                 lds0 + RING + 8192u * (c & 1) + 4096u * odd + 1024u * (uint32_t)w);
+      } else {
+        const uint32_t at = lds0 + RING + 4096u * (t & 3) + 256u * (uint32_t)w;
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const bool on = t * KD + 128 * d < klen;
+          dma4_at(on ? sq + 8 * t + 4 * d : zero, at + 2048 * d);
+          dma4_at(on ? sp + 8 * t + 4 * d : zero, at + 2048 * d + 1024);
+        }
+      }
+    }
   };
 
-  f32x16 acc[FI][FJ];
+  f32x16 acc[FIW][FJW];
 #pragma unroll
-  for (int a = 0; a < FI; ++a)
+  for (int a = 0; a < FIW; ++a)
 #pragma unroll
-    for (int b = 0; b < FJ; ++b)
+    for (int b = 0; b < FJW; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
 
@@ -603,26 +576,32 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    al[i] = AL == KC ? lane_kc(wrow + l32, i) : lane_nc(CPRA, wrow + 32 * (i < FI ? i : 0));
-    if constexpr (BL == KC) bl[i] = lane_kc(wcol + l32, i);
+    al[i] = AK ? lane_kc(wrow + l32, i) : lane_nc(CPRA, wrow + 32 * (i < FIW ? i : 0));
+    if constexpr (BK) bl[i] = lane_kc(wcol + l32, i);
     else if constexpr (BL == NC) bl[i] = lane_nc(CPRB, wcol + 32 * i);
-    else bl[i] = (uint32_t)(((wcol + 32 * i + l32) * 2 + (half ^ ((l32 >> 3) & 1))) * 16);
+    else bl[i] = (uint32_t)(((wcol + 32 * (i < FJW ? i : 0) + l32) * 2 + (half ^ ((l32 >> 3) & 1))) * 16);
   }
   struct Bases {
-    uint32_t a[4], b[4];
+    uint32_t a[4], b[4], sa, sb;   // and X4's scales of A and B
   };
   auto step_bases = [&](int s, Bases& bs, int ks0, int ks1) {
     const uint32_t sa = slot(2 * s), sb = slot(2 * s + 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (AL == NC ? i < FI : (i >= ks0 && i <= ks1)) {
+      if (AL == NC ? i < FIW : (i >= ks0 && i <= ks1)) {
         bs.a[i] = al[i] + sa;
         asm volatile("" : "+v"(bs.a[i]));
       }
-      if (BL != KC || (i >= ks0 && i <= ks1)) {
+      if (BK ? (i >= ks0 && i <= ks1) : i < FJW) {
         bs.b[i] = bl[i] + sb;
         asm volatile("" : "+v"(bs.b[i]));
       }
+    }
+    if constexpr (S4) {
+      const uint32_t at = RING + (S16 ? 8192u * ((s >> 1) & 1) + 8u * (s & 1) : 4096u * (s & 3));
+      bs.sa = at + (S16 ? 16u : 4u) * (uint32_t)(wrow + l32);
+      bs.sb = at + (S16 ? 4096u : 1024u) + (S16 ? 16u : 4u) * (uint32_t)(wcol + l32);
+      asm volatile("" : "+v"(bs.sa), "+v"(bs.sb));
     }
   };
   auto read_tr = [&](uint32_t at, int cpr, int ks) {
@@ -633,15 +612,16 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     const u32x2 u0 = __builtin_bit_cast(u32x2, v0), u1 = __builtin_bit_cast(u32x2, v1);
     return u32x4{u0[0], u0[1], u1[0], u1[1]};
   };
-  u32x4 fa[2][FI], fb[2][FJ];
-  u32x4 cw[FJ];       // E2M1: the step's codes of this lane's block, and its scales
-  float cs[FJ];
-  auto read_a = [&](const Bases& bs, int ks, int f, u32x4 (&ra)[FI]) {
-    if constexpr (AL == KC) ra[f] = *(const MLORA_LDS u32x4*)(base + bs.a[ks] + 4096 * f);
+  u32x4 fa[2][FIW], fb[2][FJW];
+  u32x4 cw[FJW];                    // F4: the step's codes of this lane's block, and their scale
+  float cs[FJW];
+  int sa[2][FIW], sb[2][FJW];       // X4: scale dwords of slices 0-1 and 2-3, shifted to this lane's block
+  auto read_a = [&](const Bases& bs, int ks, int f, u32x4 (&ra)[FIW]) {
+    if constexpr (AK) ra[f] = *(const MLORA_LDS u32x4*)(base + bs.a[ks] + 4096 * f);
     else ra[f] = read_tr(bs.a[f], CPRA, ks);
   };
-  auto read_b = [&](const Bases& bs, int ks, int f, u32x4 (&rb)[FJ]) {
-    if constexpr (BL == KC) rb[f] = *(const MLORA_LDS u32x4*)(base + bs.b[ks] + 4096 * f);
+  auto read_b = [&](const Bases& bs, int ks, int f, u32x4 (&rb)[FJW]) {
+    if constexpr (BK) rb[f] = *(const MLORA_LDS u32x4*)(base + bs.b[ks] + 4096 * f);
     else if constexpr (BL == NC) rb[f] = read_tr(bs.b[f], CPRB, ks);
     else rb[f] = bf16_of_e2m1(cw[f][ks], cs[f]);
   };
@@ -653,34 +633,43 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       cs[f] = __uint_as_float(((sw >> (16 * (s & 1) + 8 * half)) & 255u) << 23);
     }
   };
-  // What MFMA slot q of a slice reads of slice ks (bases bs): fragments in the
-  // order the first MFMAs need them, two per slot, or one where a fragment is
-  // two transposing reads or four conversions and the slice has the slots.
-  constexpr int RPS = (AL == KC && BL == KC) || FI == 1 ? 2 : 1;
-  auto reads_at = [&](int q, const Bases& bs, int ks, u32x4 (&ra)[FI], u32x4 (&rb)[FJ]) {
+  // X4: scale dword d of fragment f, from either operand's base.
+  auto read_scale = [&](uint32_t at, int d, int f) {
+    return (int)(*(const MLORA_LDS uint32_t*)(base + at + (S16 ? 512 * f + 4 * d : 128 * f + 2048 * d)) >> (8 * half));
+  };
+  // What MFMA slot q of a slice reads of slice ks (bases bs):
+  // fragments in the order the first MFMAs need them, two per slot, or one
+  // where a fragment is two transposing reads or four conversions and the
+  // slice has the slots; X4: with the scales of slices ks and ks + 1.
+  constexpr int RPS = (AK && BK) || FI == 1 ? 2 : 1;
+  auto reads_at = [&](int q, const Bases& bs, int ks, u32x4 (&ra)[FIW], u32x4 (&rb)[FJW]) {
 #pragma unroll
     for (int j = 0; j < RPS; ++j) {
       const int r = RPS * q + j;
-      if (r == 0) read_a(bs, ks, 0, ra);
-      else if (r <= FJ) read_b(bs, ks, r - 1, rb);
-      else if (r < FI + FJ) read_a(bs, ks, r - FJ, ra);
+      if (r == 0 || (r > FJW && r < FIW + FJW)) {
+        const int f = r == 0 ? 0 : r - FJW;
+        read_a(bs, ks, f, ra);
+        if (S4 && (ks & 1) == 0) sa[ks >> 1][f] = read_scale(bs.sa, ks >> 1, f);
+      } else if (r <= FJW) {
+        read_b(bs, ks, r - 1, rb);
+        if (S4 && (ks & 1) == 0) sb[ks >> 1][r - 1] = read_scale(bs.sb, ks >> 1, r - 1);
+      }
     }
   };
-  auto next_step_reads_at = [&](int q, const Bases& bs, int s, u32x4 (&ra)[FI], u32x4 (&rb)[FJ]) {
+  auto next_step_reads_at = [&](int q, const Bases& bs, int t, u32x4 (&ra)[FIW], u32x4 (&rb)[FJW]) {
     if constexpr (BL != F4) {
       reads_at(q, bs, 0, ra, rb);
     } else {
-      if (q < 2) {
-        read_codes(bs, s, 2 * q);
-        read_codes(bs, s, 2 * q + 1);
-      } else if (q == 2) {
+      // the step's codes first, its conversions last
+      if (q < FJW) read_codes(bs, t, q);
 #pragma unroll
-        for (int f = 0; f < FI; ++f) read_a(bs, 0, f, ra);
-      }
-      if (q >= NS - FJ) read_b(bs, 0, q - (NS - FJ), rb);
+      for (int f = 0; f < FIW; ++f)
+        if (q == (NS >= FIW + 2 * FJW ? FJW + f : FJW - 1)) read_a(bs, 0, f, ra);
+      if (q >= NS - FJW) read_b(bs, 0, q - (NS - FJW), rb);
     }
   };
-  constexpr int C0 = BL == F4 ? 3 : (FI + FJ + RPS - 1) / RPS;   // first slot that carries a copy
+  // first slot that carries a copy
+  constexpr int READS = (FIW + FJW + RPS - 1) / RPS, C0 = READS < NS / 2 ? READS : NS / 2;
   // Copies j of n spread over the slots from C0 on.
   auto copies_at = [&](int q, int n, auto&& f) {
     const int room = NS - C0, per = (n + room - 1) / room;
@@ -689,17 +678,29 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     for (int j = 0; j < per; ++j)
       if ((q - C0) * per + j < n) f((q - C0) * per + j);
   };
-  auto mma = [&](int q, const u32x4 (&ra)[FI], const u32x4 (&rb)[FJ]) {
-    acc[q >> 2][q & 3] = mfma32(rb[q & 3], ra[q >> 2], acc[q >> 2][q & 3]);
+  auto mma = [&](int q, int ks, const u32x4 (&ra)[FIW], const u32x4 (&rb)[FJW]) {
+    const int fi = q / FJW, fj = q % FJW;
+    if constexpr (S4) {
+      const i32x8 b8 = __builtin_bit_cast(i32x8, __builtin_shufflevector(rb[fj], zero4(), 0, 1, 2, 3, 4, 5, 6, 7));
+      const i32x8 a8 = __builtin_bit_cast(i32x8, __builtin_shufflevector(ra[fi], zero4(), 0, 1, 2, 3, 4, 5, 6, 7));
+      const int sbv = sb[ks >> 1][fj], sav = sa[ks >> 1][fi];
+      if (ks & 1)
+        acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[fi][fj], 4, 4, 2, sbv, 2, sav);
+      else
+        acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[fi][fj], 4, 4, 0, sbv, 0, sav);
+    } else {
+      acc[fi][fj] = mfma32(rb[fj], ra[fi], acc[fi][fj]);
+    }
   };
 
   // Step kinds: 0, step s + D lies inside the reduction; 1, it reaches past
   // its end; 2, it does not exist: nothing is copied and the barrier waits for
-  // every copy in flight.
+  // every copy in flight.  RING4 has no spare unit for A: its unit of step
+  // s + 1 is copied in slice 0 of step s (kind 3: step s + 1 is the last).
   auto step_block = [&](int s, auto kind) {
     constexpr int KIND = decltype(kind)::value;
-    constexpr bool COPY = KIND != 2;
-    const std::integral_constant<bool, KIND == 1> check{};
+    constexpr bool COPY = KIND < 2, COPY_A = RING4 ? KIND != 2 : COPY;
+    const std::integral_constant<bool, KIND != 0> check{};
     Bases cur;
     if (COPY) load_order(s + D);
     step_bases(s, cur, 1, 3);
@@ -708,23 +709,24 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     for (int ks = 0; ks < 3; ++ks) {
 #pragma unroll
       for (int q = 0; q < NS; ++q) {
-        mma(q, fa[ks & 1], fb[ks & 1]);
+        mma(q, ks, fa[ks & 1], fb[ks & 1]);
         reads_at(q, cur, ks + 1, fa[(ks + 1) & 1], fb[(ks + 1) & 1]);
-        if (COPY && ks < 2) copies_at(q, CA / 2, [&](int j) { copy_a(s + D, ks * (CA / 2) + j, check); });
+        if (RING4 && COPY_A && ks == 0) copies_at(q, CA, [&](int j) { copy_a(s + 1, j, check); });
+        if (!RING4 && COPY_A && ks < 2) copies_at(q, CA / 2, [&](int j) { copy_a(s + D, ks * (CA / 2) + j, check); });
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_vm_barrier<COPY ? (D - 2) * (CA + CBW) + CA : 0>();
+    wait_vm_barrier<COPY && !RING4 ? (D - 2) * (CA + CBW) + CA : 0>();
     Bases nxt;
     step_bases(s + 1, nxt, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int q = 0; q < NS; ++q) {
-      mma(q, fa[1], fb[1]);
+      mma(q, 3, fa[1], fb[1]);
       next_step_reads_at(q, nxt, s + 1, fa[0], fb[0]);
       if (COPY)
-        copies_at(q, CBW, [&](int j) {
+        copies_at(q, CB + 1, [&](int j) {
           if (j < CB) copy_b(s + D, j, check);
           else copy_scales(s + D, check);
         });
@@ -734,211 +736,42 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
 
   // the first D steps; step 0's first slice once every wave's copies of it have landed
   const std::integral_constant<bool, true> check{};
+  if constexpr (S16) dma16_at(sp, lds0 + RING + 4096u + 1024u * (uint32_t)w);   // B's scales of steps 0 and 1
 #pragma unroll
   for (int t = 0; t < D; ++t) {
     load_order(t);
+    if (!(RING4 && t == 1)) {
 #pragma unroll
-    for (int i = 0; i < CA; ++i) copy_a(t, i, check);
+      for (int i = 0; i < CA; ++i) copy_a(t, i, check);
+    }
 #pragma unroll
     for (int i = 0; i < CB; ++i) copy_b(t, i, check);
     copy_scales(t, check);
   }
-  wait_vm_barrier<(D - 1) * (CA + CBW)>();
+  wait_vm_barrier<RING4 ? CB : (D - 1) * (CA + CBW)>();
   Bases b0;
   step_bases(0, b0, 0, 0);
 #pragma unroll
-  for (int f = 0; f < FJ; ++f) read_codes(b0, 0, f);
+  for (int f = 0; f < FJW; ++f) read_codes(b0, 0, f);
 #pragma unroll
-  for (int f = 0; f < FI; ++f) read_a(b0, 0, f, fa[0]);
+  for (int f = 0; f < FIW; ++f) {
+    read_a(b0, 0, f, fa[0]);
+    if (S4) sa[0][f] = read_scale(b0.sa, 0, f);
+  }
 #pragma unroll
-  for (int f = 0; f < FJ; ++f) read_b(b0, 0, f, fb[0]);
+  for (int f = 0; f < FJW; ++f) {
+    read_b(b0, 0, f, fb[0]);
+    if (S4) sb[0][f] = read_scale(b0.sb, 0, f);
+  }
   int s = 0;
   for (; (s + D + 1) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
   for (; s + D < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
+  if constexpr (RING4)
+    for (; s + 1 < nsteps; ++s) step_block(s, std::integral_constant<int, 3>());
   for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   if constexpr (DW) store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
-  else store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
-}
-
-// ---------------------------------------------------------------------------
-// MXFP4 x MXFP4: both operands as E2M1 codes on the scaled matrix cores.
-// 256 x 256 tile, steps of 128 of the reduction: 64 bytes of codes and one
-// dword of scale codes per row and operand.  Chunk c of row r sits at
-// c ^ ((r >> 2) & 3), which spreads a read group's rows over the banks; lane
-// r + 32 h holds row r's 32-block h of a 64-deep slice (16 bytes, the low
-// nibble first) and supplies its scale.  A step is two slices, 1024 cycles of
-// MFMA at FI = 4, less than a copy's latency: four stages keep three steps in
-// flight.  A copy of scale dwords touches a row per lane, four times the
-// addresses of a copy of codes; S16 (K a multiple of 512, so a row's 16 scale
-// bytes are aligned) copies four steps' scales at once instead.
-// ---------------------------------------------------------------------------
-template <int FI, bool S16>
-__global__ __launch_bounds__(256, 1) void k_expert_mx4(ExpertArgs g) {
-  constexpr int FJ = 4, BM = 64 * FI, BN = 256;
-  constexpr int UA = BM * 64, UB = BN * 64, CA = FI, CB = 4, NS = FI * FJ;
-  constexpr int NR = 4;                               // stages
-  constexpr int STAGE = UA + UB + (S16 ? 0 : 2048);   // with the scale dwords of 256 rows of A and of B
-  constexpr int SCL = NR * STAGE;                     // S16: two chunks of 16 scale bytes for 256 + 256 rows
-  constexpr int COPIES = CA + CB + (S16 ? 0 : 2);     // per wave and step
-  constexpr int LDS = SCL + (S16 ? 16384 : 0);
-  __shared__ u32x4 ring[(LDS > BM * 512 ? LDS : BM * 512) / 16];
-  const Tile tl = find_tile<BM, false>(g);
-  if (tl.mrows <= 0) return;
-  const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, n0 = tl.n0;
-  const int nsteps = g.K / 128;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5, l32 = lane & 31;
-  const int wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
-  const int64_t kb = g.K / 32;
-
-  const uint8_t* ap[CA];
-  const uint8_t* bp[CB];
-#pragma unroll
-  for (int i = 0; i < CA; ++i) {
-    const int r = 16 * (CA * w + i) + (lane >> 2);
-    ap[i] = g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * (g.K / 2) + 16 * ((lane & 3) ^ ((r >> 2) & 3));
-  }
-#pragma unroll
-  for (int i = 0; i < CB; ++i) {
-    const int r = 16 * (CB * w + i) + (lane >> 2);
-    bp[i] = g.B + (int64_t)e * g.b_expert + (int64_t)min(n0 + r, g.N - 1) * (g.K / 2) +
-            16 * ((lane & 3) ^ ((r >> 2) & 3));
-  }
-  // scale dwords: wave w copies those of rows 64 w .. of A and of B
-  const uint8_t* as = g.a_scale + source_row(g, g.ma, row0 + min(64 * w + lane, mrows - 1)) * kb;
-  const uint8_t* bs = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * kb;
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
-  const MLORA_LDS char* const base = (const MLORA_LDS char*)(MLORA_LDS void*)&ring[0];
-  auto copy_a = [&](int t, int i) {
-    const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
-    if (i < CA) {
-      dma16_at(ap[i] + 64 * (int64_t)t, u + 1024u * (uint32_t)(CA * w + i));
-    } else if constexpr (S16) {
-      if ((t & 3) == 0) dma16_at(as + 4 * t, lds0 + SCL + 8192u * ((t >> 2) & 1) + 1024u * (uint32_t)w);
-    } else {
-      dma4_at(as + 4 * t, u + UA + UB + 256u * (uint32_t)w);
-    }
-  };
-  auto copy_b = [&](int t, int i) {
-    const uint32_t u = lds0 + (uint32_t)(t % NR) * STAGE;
-    if (i < CB) {
-      dma16_at(bp[i] + 64 * (int64_t)t, u + UA + 1024u * (uint32_t)(CB * w + i));
-    } else if constexpr (S16) {
-      if ((t & 3) == 0) dma16_at(bs + 4 * t, lds0 + SCL + 4096 + 8192u * ((t >> 2) & 1) + 1024u * (uint32_t)w);
-    } else {
-      dma4_at(bs + 4 * t, u + UA + UB + 1024 + 256u * (uint32_t)w);
-    }
-  };
-  // Scale dword of row r of operand op for step t.
-  auto scale_at = [&](int t, int op, int r) -> uint32_t {
-    if constexpr (S16)
-      return *(const MLORA_LDS uint32_t*)(base + SCL + 8192 * ((t >> 2) & 1) + 4096 * op + 16 * r + 4 * (t & 3));
-    else return *(const MLORA_LDS uint32_t*)(base + (uint32_t)(t % NR) * STAGE + UA + UB + 1024 * op + 4 * r);
-  };
-
-  f32x16 acc[FI][FJ];
-#pragma unroll
-  for (int a = 0; a < FI; ++a)
-#pragma unroll
-    for (int b = 0; b < FJ; ++b)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
-  u32x4 fa[2][FI], fb[2][FJ];
-  int sa[FI], sb[FJ], na[FI], nb[FJ];   // scales of the step, and of the next one
-  // Lane parts of the reads; fragment f is 32 rows (2048 bytes) on.
-  uint32_t al[2], bl[2];
-#pragma unroll
-  for (int sl = 0; sl < 2; ++sl) {
-    const int c = (2 * sl + half) ^ ((l32 >> 2) & 3);
-    al[sl] = (uint32_t)(((wrow + l32) * 4 + c) * 16);
-    bl[sl] = (uint32_t)(((wcol + l32) * 4 + c) * 16 + UA);
-  }
-  // Read r of slice sl of step t: fragments in the order the first MFMAs need
-  // them, with their scales (shifted to this lane's block) on slice 0.
-  auto read = [&](int t, int sl, int r) {
-    const uint32_t u = (uint32_t)(t % NR) * STAGE;
-    if (r == 0 || (r > FJ && r < FI + FJ)) {
-      const int f = r == 0 ? 0 : r - FJ;
-      fa[sl][f] = *(const MLORA_LDS u32x4*)(base + u + al[sl] + 2048 * f);
-      if (sl == 0)
-        na[f] = (int)(scale_at(t, 0, wrow + 32 * f + l32) >> (8 * half));
-    } else if (r <= FJ) {
-      const int f = r - 1;
-      fb[sl][f] = *(const MLORA_LDS u32x4*)(base + u + bl[sl] + 2048 * f);
-      if (sl == 0)
-        nb[f] = (int)(scale_at(t, 1, wcol + 32 * f + l32) >> (8 * half));
-    }
-  };
-  auto mma = [&](auto sl_tag, int q) {
-    constexpr int SL = decltype(sl_tag)::value;
-    const int fi = q >> 2, fj = q & 3;
-    acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-        __builtin_bit_cast(i32x8, __builtin_shufflevector(fb[SL][fj], zero4(), 0, 1, 2, 3, 4, 5, 6, 7)),
-        __builtin_bit_cast(i32x8, __builtin_shufflevector(fa[SL][fi], zero4(), 0, 1, 2, 3, 4, 5, 6, 7)), acc[fi][fj], 4,
-        4, 2 * SL, sb[fj], 2 * SL, sa[fi]);
-  };
-  // Step s: slice 0 reads slice 1 and copies the A unit of step
-  // s + 3 into the stage that step s - 1 left; then step s + 1 has landed for
-  // every wave (steps s + 2 and the A unit of s + 3 may be in flight) and
-  // slice 1 reads its first slice and copies the B unit of step s + 3.  The
-  // last three steps copy nothing and wait for everything.
-  auto step = [&](int s, auto copy_tag) {
-    constexpr bool COPY = decltype(copy_tag)::value;
-    constexpr int C0 = (FI + FJ + 1) / 2, ROOM = NS - C0;
-#pragma unroll
-    for (int f = 0; f < FI; ++f) sa[f] = na[f];
-#pragma unroll
-    for (int f = 0; f < FJ; ++f) sb[f] = nb[f];
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int q = 0; q < NS; ++q) {
-      mma(std::integral_constant<int, 0>(), q);
-      read(s, 1, 2 * q);
-      read(s, 1, 2 * q + 1);
-      if (COPY && q >= C0) {
-        constexpr int PER = (CA + 1 + ROOM - 1) / ROOM;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if ((q - C0) * PER + j < CA + 1) copy_a(s + 3, (q - C0) * PER + j);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    // (counts without the scale copies of every fourth step: a stricter wait)
-    wait_vm_barrier<COPY ? COPIES + CA + (S16 ? 0 : 1) : 0>();
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int q = 0; q < NS; ++q) {
-      mma(std::integral_constant<int, 1>(), q);
-      read(s + 1, 0, 2 * q);
-      read(s + 1, 0, 2 * q + 1);
-      if (COPY && q >= C0) {
-        constexpr int PER = (CB + 1 + ROOM - 1) / ROOM;
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if ((q - C0) * PER + j < CB + 1) copy_b(s + 3, (q - C0) * PER + j);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-
-  for (int t = 0; t < 3 && t < nsteps; ++t) {
-#pragma unroll
-    for (int i = 0; i <= CA; ++i) copy_a(t, i);
-#pragma unroll
-    for (int i = 0; i <= CB; ++i) copy_b(t, i);
-  }
-  if (nsteps >= 3) wait_vm_barrier<2 * COPIES>();
-  else wait_vm_barrier<0>();
-#pragma unroll
-  for (int r = 0; r < FI + FJ; ++r) read(0, 0, r);
-  int s = 0;
-  for (; s + 3 < nsteps; ++s) step(s, std::true_type());
-  for (; s < nsteps; ++s) step(s, std::false_type());
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  store_bf16<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+  else store_bf16<BM>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, wrow, wcol, w, lane);
 }
 
 namespace {
@@ -946,29 +779,25 @@ namespace {
 int64_t rows_grid(const ExpertArgs& a, int bm) {
   return max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, bm) * ((a.N + 255) / 256);
 }
-template <bool F32, int BL>
+template <int AL, int BL>
 void rows_size(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96) {
-    const dim3 grid((unsigned)rows_grid(a, 64));
-    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 1, false>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 1, false, false>), grid, dim3(256), 0, s, a);
-  } else if (mean <= 384) {
-    const dim3 grid((unsigned)rows_grid(a, 128));
-    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 2, false>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 2, false, false>), grid, dim3(256), 0, s, a);
-  } else {
-    const dim3 grid((unsigned)rows_grid(a, 256));
-    if constexpr (F32) hipLaunchKernelGGL((k_expert_tile<F32, KC, BL, 4, false>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_expert_pipe<KC, BL, 4, false, false>), grid, dim3(256), 0, s, a);
-  }
+  if (mean <= 96)
+    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 1, false, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
+  else if (mean <= 384)
+    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 2, false, false>), dim3((unsigned)rows_grid(a, 128)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 4, false, false>), dim3((unsigned)rows_grid(a, 256)), dim3(256), 0, s, a);
 }
-template <int FI>
-void mx4_tile(const ExpertArgs& a, hipStream_t s) {
-  const int64_t nN = (a.N + 255) / 256;
-  const int64_t grid = max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, 64 * FI) * nN;
-  if (a.K % 512 == 0) hipLaunchKernelGGL((k_expert_mx4<FI, true>), dim3((unsigned)grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_expert_mx4<FI, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
+template <int BL>
+void rows_f32(const ExpertArgs& a, hipStream_t s) {
+  const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
+  if (mean <= 96)
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
+  else if (mean <= 384)
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 2, false>), dim3((unsigned)rows_grid(a, 128)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 4, false>), dim3((unsigned)rows_grid(a, 256)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -979,20 +808,17 @@ void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStre
   if (mean <= 32) return launch_expert_few(form, b_kc, mean <= 16 ? 1 : 2, a, s);
   switch (form) {
     case ExpertForm::kBf16:
-      if (b_kc) rows_size<false, KC>(a, s);
-      else rows_size<false, NC>(a, s);
+      if (b_kc) rows_size<KC, KC>(a, s);
+      else rows_size<KC, NC>(a, s);
       break;
     case ExpertForm::kF32:
-      if (b_kc) rows_size<true, KC>(a, s);
-      else rows_size<true, NC>(a, s);
+      if (b_kc) rows_f32<KC>(a, s);
+      else rows_f32<NC>(a, s);
       break;
-    case ExpertForm::kW4A16:
-      rows_size<false, F4>(a, s);
-      break;
+    case ExpertForm::kW4A16: rows_size<KC, F4>(a, s); break;
     case ExpertForm::kW4A4:
-      if (mean <= 96) mx4_tile<1>(a, s);
-      else if (mean <= 384) mx4_tile<2>(a, s);
-      else mx4_tile<4>(a, s);
+      if (a.K % 512 == 0) rows_size<X4, X4>(a, s);
+      else rows_size<X4D, X4D>(a, s);
       break;
   }
 }
@@ -1001,7 +827,7 @@ void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
   const int64_t grid = 8 * E * (((a.M + 255) / 256 * ((a.N + 255) / 256) + 7) / 8);
   const dim3 dg((unsigned)grid);
-  if (f32) hipLaunchKernelGGL((k_expert_tile<true, NC, NC, 4, true>), dg, dim3(256), 0, s, a);
+  if (f32) hipLaunchKernelGGL((k_expert_f32<NC, NC, 4, true>), dg, dim3(256), 0, s, a);
   else if (a.ma.by_order || a.mb.by_order)
     hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, true>), dg, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, false>), dg, dim3(256), 0, s, a);
