@@ -31,77 +31,79 @@ __device__ __forceinline__ void group_rows(const ExpertArgs& a, int e, int& lo, 
   hi = max(lo, min(a.offsets[e + 1], a.rows));
 }
 
-// A workgroup's tile in the rows form: rows [row0, row0 + mrows) of expert e,
+// A tile in the rows form: rows [row0, row0 + mrows) of expert e,
 // column tile tn.  mrows = 0: nothing to do.
 struct RowTile {
   int e, row0, mrows, tn;
 };
 
-// The tile of workgroup blockIdx.x among the row tiles of BM rows that the
-// groups' sizes give (known on the device only; the grid covers their upper
-// bound).  Lane l sums the tiles of group 64 c + l in chunk c, so a router of
-// up to 64 experts costs one pair of loads and one wave scan.  Workgroup b
-// runs on XCD b mod 8; each XCD takes a contiguous run of the actual tiles,
-// and tiles go down GM row tiles before moving along N, so tiles that run
-// together share rows and columns in the XCD's L2.
+// The row tiles of BM rows that the groups' sizes give (known on the device
+// only; a grid covers their upper bound).  Lane l sums the tiles of group
+// 64 c + l in chunk c, so a router of up to 64 experts costs one pair of loads
+// and one wave scan.  Tile b belongs to XCD b mod 8 (a workgroup's, and
+// b + gridDim.x's when the grid is a multiple of 8); each XCD takes a
+// contiguous run of the actual tiles, and tiles go down GM row tiles before
+// moving along N, so tiles that run together share rows and columns in the
+// XCD's L2.
 template <int BM, int GM>
-__device__ __forceinline__ RowTile row_tile(const ExpertArgs& a, int nN) {
-  const int lane = threadIdx.x & 63;
-  const int E = a.offsets ? a.n_experts : 1;
-  auto tiles_of = [&](int e, int& lo, int& hi) {
-    lo = hi = 0;
-    if (e < E) group_rows(a, e, lo, hi);
-    return (hi - lo + BM - 1) / BM;
-  };
-  auto scan = [&](int v) {
+struct RowTiles {
+  int E, nN, TM;
+  int lo, hi, cnt, inc;   // this lane's group of chunk 0: rows, tiles, tiles up to and with it
+
+  __device__ __forceinline__ void group(const ExpertArgs& a, int c, int& l, int& h, int& n, int& sum) const {
+    const int lane = threadIdx.x & 63;
+    l = h = 0;
+    if (c + lane < E) group_rows(a, c + lane, l, h);
+    n = (h - l + BM - 1) / BM;
+    sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(v, d);
-      if (lane >= d) v += u;
+      const int u = __shfl_up(sum, d);
+      if (lane >= d) sum += u;
     }
-    return v;
-  };
-  int lo, hi;
-  int cnt = tiles_of(lane, lo, hi);        // chunk 0's; the search below starts with it
-  int inc = scan(cnt);
-  int TM = __builtin_amdgcn_readlane(inc, 63);
-  for (int c = 64; c < E; c += 64) {
-    int lo2, hi2;
-    TM += __builtin_amdgcn_readlane(scan(tiles_of(c + lane, lo2, hi2)), 63);
   }
-  const int T = TM * nN, b = blockIdx.x;
-  const int xcd = b & 7, q = b >> 3, per = T >> 3, rem = T & 7;
-  if (q >= per + (xcd < rem ? 1 : 0)) return RowTile{0, 0, 0, 0};
-  const int L = xcd * per + min(xcd, rem) + q;
-  const int grp = L / (GM * nN), fm = grp * GM, gm = min(GM, TM - fm);
-  const int within = L - fm * nN;
-  const int tm = fm + within % gm;
-  RowTile t;
-  t.tn = within / gm;
-  t.e = t.row0 = t.mrows = 0;
-  // the group whose tiles hold tm
-  for (int c = 0, before = 0; c < E; c += 64) {
-    if (c > 0) {
-      cnt = tiles_of(c + lane, lo, hi);
-      inc = scan(cnt);
+  __device__ __forceinline__ RowTiles(const ExpertArgs& a, int n_tiles) : nN(n_tiles) {
+    E = a.offsets ? a.n_experts : 1;
+    group(a, 0, lo, hi, cnt, inc);
+    TM = __builtin_amdgcn_readlane(inc, 63);
+    for (int c = 64; c < E; c += 64) {
+      int l2, h2, c2, i2;
+      group(a, c, l2, h2, c2, i2);
+      TM += __builtin_amdgcn_readlane(i2, 63);
     }
-    const uint64_t past = __ballot(before + inc > tm);
-    if (past != 0) {
-      const int l = __builtin_ctzll(past);
-      const int first = before + __builtin_amdgcn_readlane(inc - cnt, l);
-      t.e = c + l;
-      t.row0 = __builtin_amdgcn_readlane(lo, l) + (tm - first) * BM;
-      t.mrows = min(BM, __builtin_amdgcn_readlane(hi, l) - t.row0);
-      break;
-    }
-    before += __builtin_amdgcn_readlane(inc, 63);
   }
-  t.e = __builtin_amdgcn_readfirstlane(t.e);
-  t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-  t.mrows = __builtin_amdgcn_readfirstlane(t.mrows);
-  t.tn = __builtin_amdgcn_readfirstlane(t.tn);
-  return t;
-}
+  // Tile b; mrows = 0 past the last one.
+  __device__ __forceinline__ RowTile at(const ExpertArgs& a, int b) const {
+    const int T = TM * nN, xcd = b & 7, q = b >> 3, per = T >> 3, rem = T & 7;
+    RowTile t{0, 0, 0, 0};
+    if (q >= per + (xcd < rem ? 1 : 0)) return t;
+    const int L = xcd * per + min(xcd, rem) + q;
+    const int fm = L / (GM * nN) * GM, gm = min(GM, TM - fm);
+    const int within = L - fm * nN;
+    const int tm = fm + within % gm;
+    t.tn = within / gm;
+    // the group whose tiles hold tm
+    int l1 = lo, h1 = hi, n1 = cnt, i1 = inc;
+    for (int c = 0, before = 0; c < E; c += 64) {
+      if (c > 0) group(a, c, l1, h1, n1, i1);
+      const uint64_t past = __ballot(before + i1 > tm);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int first = before + __builtin_amdgcn_readlane(i1 - n1, l);
+        t.e = c + l;
+        t.row0 = __builtin_amdgcn_readlane(l1, l) + (tm - first) * BM;
+        t.mrows = min(BM, __builtin_amdgcn_readlane(h1, l) - t.row0);
+        break;
+      }
+      before += __builtin_amdgcn_readlane(i1, 63);
+    }
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.mrows = __builtin_amdgcn_readfirstlane(t.mrows);
+    t.tn = __builtin_amdgcn_readfirstlane(t.tn);
+    return t;
+  }
+};
 
 // Eight E2M1 codes (one word) times 2^(x - 127) -> eight bf16, exact.
 __device__ __forceinline__ u32x4 bf16_of_e2m1(uint32_t w, float scale) {

@@ -35,6 +35,10 @@ __device__ __forceinline__ void dma16_sv(uint64_t sbase, uint32_t voff, uint32_t
       : "memory");
 }
 
+// Meets the other waves once this wave's LDS accesses are done.  Unlike
+// __syncthreads it leaves copies and stores in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // How an operand's elements lie in memory and in LDS.
 //   KC: contiguous along the reduction; a unit is one row of 128 bytes per
 //       tile row (64 bf16 or 32 fp32 of the reduction), chunk c (16 bytes) of
@@ -98,7 +102,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
     t.klen = __builtin_amdgcn_readfirstlane(hi) - t.row0;
     t.mrows = i < TT ? min(BM, g.M - t.m0) : 0;
   } else {
-    const RowTile r = row_tile<BM, 4>(g, nN);
+    const RowTile r = RowTiles<BM, 4>(g, nN).at(g, blockIdx.x);
     t = Tile{r.e, r.row0, r.mrows, 0, r.tn * 256, g.K};
   }
   return t;
@@ -113,11 +117,8 @@ __device__ __forceinline__ int out_row(const ExpertArgs& g, const Tile& t, int m
 }
 
 // Epilogues.  acc[fi][fj][4 gg + x] holds C[m = wrow + 32 fi + l32][n = wcol
-// + 32 fj + 8 gg + 4 half + x].  fp32 goes straight to memory, four columns a
-// lane; bf16 through LDS (every wave is past its last read of the ring):
-// 512-byte rows of 32 16-byte granules, granule c of row m at c ^ (m & 31), so
-// the rows a fragment writes and the granules a row read takes both spread
-// over the banks and every store writes whole 512-byte rows.
+// + 32 fj + 8 gg + 4 half + x].  fp32 kernel: straight to memory, four columns
+// a lane.
 template <int FI, bool DW>
 __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][4], const Tile& t, int wrow,
                                           int wcol, int lane) {
@@ -190,36 +191,6 @@ __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
   for (int m = threadIdx.x >> 6; m < t.mrows; m += 4)
     *reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n) = f32x4{0.f, 0.f, 0.f, 0.f};
 }
-template <int BM, int FIW, int FJW>
-__device__ __forceinline__ void store_bf16(const ExpertArgs& g, const f32x16 (&acc)[FIW][FJW], char* ct, const Tile& t,
-                                           int wrow, int wcol, int w, int lane) {
-  const int half = lane >> 5, l32 = lane & 31;
-  __syncthreads();
-#pragma unroll
-  for (int fi = 0; fi < FIW; ++fi) {
-    const int m = wrow + 32 * fi + l32;
-#pragma unroll
-    for (int fj = 0; fj < FJW; ++fj)
-#pragma unroll
-      for (int gg = 0; gg < 4; ++gg) {
-        const int c = (wcol >> 3) + 4 * fj + gg;
-        u32x2 pk;
-        pk[0] = pack_bf16x2(acc[fi][fj][4 * gg + 0], acc[fi][fj][4 * gg + 1]);
-        pk[1] = pack_bf16x2(acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]);
-        *reinterpret_cast<u32x2*>(ct + m * 512 + 16 * (c ^ (m & 31)) + 8 * half) = pk;
-      }
-  }
-  __syncthreads();
-  const int gc = lane & 31, n = t.n0 + 8 * gc;
-#pragma unroll 4
-  for (int it = 0; it < BM / 8; ++it) {
-    const int m = BM / 4 * w + 2 * it + half;
-    const int row = out_row(g, t, m);
-    const u32x4 x = *reinterpret_cast<const u32x4*>(ct + m * 512 + 16 * (gc ^ (m & 31)));
-    if (row >= 0 && n < g.N) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (int64_t)row * g.ldc + n) = x;
-  }
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -400,13 +371,21 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : 8;   // 1 KiB copies per wave and unit
   constexpr int CBW = CB + (BL == F4 ? 1 : 0);           // and the scale dwords
   constexpr int RING = RING5 ? 5 * UA : NR * (UA + UB);
-  constexpr int LDS = DW || RING + SCL >= BM * 512 ? RING + SCL : BM * 512;   // the epilogue's bf16 tile takes BM x 512
-  __shared__ u32x4 ring[LDS / 16];
+  // What the first D steps of a tile leave free: the epilogue's rows.
+  constexpr int SPARE = RING5 ? 4 * UA : RING4 ? 2 * UA : (NR - 1) * (UA + UB);
+  static_assert(DW || (RING5 || RING4 ? UA : UA + UB) >= (WM == 2 ? 64 : 32) * 512, "an epilogue phase fits");
+  __shared__ u32x4 ring[(RING + SCL) / 16];
 
-  const Tile tl = find_tile<BM, DW>(g);
+  const RowTiles<BM, 4> tiles(g, DW ? 0 : (g.N + BN - 1) / BN);
+  auto rows_tile = [&](int b) {
+    const RowTile r = tiles.at(g, b);
+    return Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
+  };
+  Tile tl;
+  if constexpr (DW) tl = find_tile<BM, DW>(g);
+  else tl = rows_tile(blockIdx.x);
   if (tl.mrows <= 0) return;
-  const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
-  const int nsteps = (klen + KD - 1) / KD;
+  const int klen = tl.klen, nsteps = (klen + KD - 1) / KD;
   if (DW && nsteps == 0) return store_zero<BM>(g, tl);
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -414,7 +393,6 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   const int half = lane >> 5, l32 = lane & 31;
   const int wrow = WM == 2 ? 32 * FIW * (w >> 1) : 0, wcol = WM == 2 ? 128 * (w & 1) : 64 * w;
   const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
-  const uint8_t* const Be = DW ? g.B : g.B + (int64_t)e * g.b_expert;
   // bytes of a row of either operand
   const int64_t arow = S4 ? g.lda / 2 : g.lda * 2, brow = BL == F4 || S4 ? g.ldb / 2 : g.ldb * 2;
 
@@ -426,45 +404,55 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   const uint8_t* ap[AK ? CA : 1];  // rows of A anywhere: one pointer per copy
   uint32_t ao[CA], bo[CB];               // else byte offsets from a base that advances by steps
   int ac[CA], bc[CB];                    // KC: chunk; NC: k-row of the step
-#pragma unroll
-  for (int i = 0; i < CA; ++i) {
-    if constexpr (AK) {
-      const int r = 8 * (CA * w + i) + (lane >> 3);
-      ac[i] = (lane & 7) ^ kx8(r);
-      ao[i] = 0;
-      ap[i] = g.A + source_row(g, g.ma, row0 + min(r, mrows - 1)) * arow + 16 * ac[i];
-    } else {
-      ac[i] = RPCA * (CA * w + i) + lane / CPRA;
-      const int col = min(m0 + 8 * ((lane % CPRA) ^ nx16(ac[i])), g.M - 8);
-      ao[i] = (uint32_t)((GATHER ? 0 : ac[i] * arow) + col * 2);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < CB; ++i) {
-    if constexpr (BK) {
-      const int r = 8 * (CB * w + i) + (lane >> 3);
-      bc[i] = (lane & 7) ^ kx8(r);
-      bo[i] = (uint32_t)((min(n0 + r, g.N - 1) - n0) * brow + 16 * bc[i]);
-    } else if constexpr (BL == NC) {
-      bc[i] = RPCB * (CB * w + i) + lane / CPRB;
-      const int col = min(n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
-      bo[i] = (uint32_t)(GATHER ? col * 2 : bc[i] * brow + (col - n0) * 2);
-    } else {
-      const int r = 32 * (2 * w + i) + (lane >> 1);
-      bc[i] = 0;
-      bo[i] = (uint32_t)((min(n0 + r, g.N - 1) - n0) * brow + 16 * ((lane & 1) ^ ((r >> 3) & 1)));
-    }
-  }
   // scale codes: F4 and X4 rows of B, wave w copying those of rows 64 w ..; X4 rows of A the same way
   const uint8_t* sp = nullptr;
   const uint8_t* sq = nullptr;
-  if constexpr (BL == F4 || S4) sp = g.b_scale + ((int64_t)e * g.N + min(n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
-  if constexpr (S4) sq = g.a_scale + source_row(g, g.ma, row0 + min(64 * w + lane, mrows - 1)) * (g.lda / 32);
   // bases of step 0 and bytes per step
-  const uint8_t* const baseA = AL == NC && !GATHER ? g.A + row0 * arow : g.A;
-  const uint8_t* const baseB = BL != NC ? Be + n0 * brow : (GATHER ? Be : Be + (DW ? row0 * brow : 0) + n0 * 2);
+  const uint8_t* baseA = nullptr;
+  const uint8_t* baseB = nullptr;
   const int64_t stepA = KD * arow;
   const int64_t stepB = BK ? 128 : BL == F4 ? 32 : KD * brow;
+  auto place = [&](const Tile& t) {
+    // (opaque: else the loop over tiles keeps every lane's share of this in
+    // registers beside the accumulators)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+#pragma unroll
+    for (int i = 0; i < CA; ++i) {
+      if constexpr (AK) {
+        const int r = 8 * (CA * w + i) + (lane >> 3);
+        ac[i] = (lane & 7) ^ kx8(r);
+        ao[i] = 0;
+        ap[i] = g.A + source_row(g, g.ma, t.row0 + min(r, t.mrows - 1)) * arow + 16 * ac[i];
+      } else {
+        ac[i] = RPCA * (CA * w + i) + lane / CPRA;
+        const int col = min(t.m0 + 8 * ((lane % CPRA) ^ nx16(ac[i])), g.M - 8);
+        ao[i] = (uint32_t)((GATHER ? 0 : ac[i] * arow) + col * 2);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      if constexpr (BK) {
+        const int r = 8 * (CB * w + i) + (lane >> 3);
+        bc[i] = (lane & 7) ^ kx8(r);
+        bo[i] = (uint32_t)((min(t.n0 + r, g.N - 1) - t.n0) * brow + 16 * bc[i]);
+      } else if constexpr (BL == NC) {
+        bc[i] = RPCB * (CB * w + i) + lane / CPRB;
+        const int col = min(t.n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
+        bo[i] = (uint32_t)(GATHER ? col * 2 : bc[i] * brow + (col - t.n0) * 2);
+      } else {
+        const int r = 32 * (2 * w + i) + (lane >> 1);
+        bc[i] = 0;
+        bo[i] = (uint32_t)((min(t.n0 + r, g.N - 1) - t.n0) * brow + 16 * ((lane & 1) ^ ((r >> 3) & 1)));
+      }
+    }
+    if constexpr (BL == F4 || S4)
+      sp = g.b_scale + ((int64_t)t.e * g.N + min(t.n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
+    if constexpr (S4) sq = g.a_scale + source_row(g, g.ma, t.row0 + min(64 * w + lane, t.mrows - 1)) * (g.lda / 32);
+    const uint8_t* Be = DW ? g.B : g.B + (int64_t)t.e * g.b_expert;
+    baseA = AL == NC && !GATHER ? g.A + t.row0 * arow : g.A;
+    baseB = BL != NC ? Be + t.n0 * brow : (GATHER ? Be : Be + (DW ? t.row0 * brow : 0) + t.n0 * 2);
+  };
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
   auto slot = [](int u) -> uint32_t {
@@ -480,11 +468,11 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   auto load_order = [&](int t) {
     if constexpr (GATHER) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) oidx[j] = ldc(g.order + row0 + min(t * KD + 16 * w + j, klen - 1));
+      for (int j = 0; j < 16; ++j) oidx[j] = ldc(g.order + tl.row0 + min(t * KD + 16 * w + j, klen - 1));
     }
   };
   auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t row_bytes, int i, int t) -> const uint8_t* {
-    const int k = row0 + t * KD + 16 * w + 2 * i;
+    const int k = tl.row0 + t * KD + 16 * w + 2 * i;
     auto at = [&](int h) -> int64_t {
       return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], g.rows), map.div)
                            : (int64_t)(k + h)) *
@@ -551,12 +539,6 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   };
 
   f32x16 acc[FIW][FJW];
-#pragma unroll
-  for (int a = 0; a < FIW; ++a)
-#pragma unroll
-    for (int b = 0; b < FJW; ++b)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
 
   // Fragment reads: a lane part plus the step's slot, made once per step (the
   // empty asm keeps the slot from being folded into every read), plus
@@ -734,60 +716,141 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     }
   };
 
-  // the first D steps; step 0's first slice once every wave's copies of it have landed
-  const std::integral_constant<bool, true> check{};
-  if constexpr (S16) dma16_at(sp, lds0 + RING + 4096u + 1024u * (uint32_t)w);   // B's scales of steps 0 and 1
+  // The first D steps of a tile.
+  auto prologue = [&]() {
+    const std::integral_constant<bool, true> check{};
+    if constexpr (S16) dma16_at(sp, lds0 + RING + 4096u + 1024u * (uint32_t)w);   // B's scales of steps 0 and 1
 #pragma unroll
-  for (int t = 0; t < D; ++t) {
-    load_order(t);
-    if (!(RING4 && t == 1)) {
+    for (int t = 0; t < D; ++t) {
+      load_order(t);
+      if (!(RING4 && t == 1)) {
 #pragma unroll
-      for (int i = 0; i < CA; ++i) copy_a(t, i, check);
+        for (int i = 0; i < CA; ++i) copy_a(t, i, check);
+      }
+#pragma unroll
+      for (int i = 0; i < CB; ++i) copy_b(t, i, check);
+      copy_scales(t, check);
+    }
+  };
+  auto main_loop = [&]() {
+#pragma unroll
+    for (int a = 0; a < FIW; ++a)
+#pragma unroll
+      for (int b = 0; b < FJW; ++b)
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
+    // step 0's first slice once every wave's copies of it have landed
+    wait_vm_barrier<RING4 ? CB : (D - 1) * (CA + CBW)>();
+    Bases b0;
+    step_bases(0, b0, 0, 0);
+#pragma unroll
+    for (int f = 0; f < FJW; ++f) read_codes(b0, 0, f);
+#pragma unroll
+    for (int f = 0; f < FIW; ++f) {
+      read_a(b0, 0, f, fa[0]);
+      if (S4) sa[0][f] = read_scale(b0.sa, 0, f);
     }
 #pragma unroll
-    for (int i = 0; i < CB; ++i) copy_b(t, i, check);
-    copy_scales(t, check);
-  }
-  wait_vm_barrier<RING4 ? CB : (D - 1) * (CA + CBW)>();
-  Bases b0;
-  step_bases(0, b0, 0, 0);
+    for (int f = 0; f < FJW; ++f) {
+      read_b(b0, 0, f, fb[0]);
+      if (S4) sb[0][f] = read_scale(b0.sb, 0, f);
+    }
+    int s = 0;
+    for (; (s + D + 1) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
+    for (; s + D < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
+    if constexpr (RING4)
+      for (; s + 1 < nsteps; ++s) step_block(s, std::integral_constant<int, 3>());
+    for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  };
+
+  place(tl);
+  prologue();
+  if constexpr (DW) {
+    main_loop();
+    store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+  } else {
+    // The grid is one workgroup per CU: each takes every gridDim.x-th tile and
+    // starts the next one's copies before it stores this one's rows.
+    char* const ct = reinterpret_cast<char*>(&ring[0]) + SPARE;
+    constexpr int PR = WM == 2 ? 64 : 32, PI = PR / 8;      // rows of an epilogue phase; row pairs per wave
+    for (int b = blockIdx.x;;) {
+      main_loop();
+      b += gridDim.x;
+      const Tile nx = rows_tile(b);
+      int lane = threadIdx.x & 63;           // opaque, as in place
+      asm volatile("" : "+v"(lane));
+      const int half = lane >> 5, l32 = lane & 31;
+      // Phase p stores fragment row p of every wave.  Lane l holds the row of
+      // C that the wave's l-th stored row goes to (or -1), loaded before the
+      // copies (a load's use waits for every copy issued before it).
+      const int lp = (lane / (2 * PI)) % FIW, lr = PR / 4 * w + lane % (2 * PI);
+      const int lm = 32 * FIW * (lr >> 5) + 32 * lp + (lr & 31), ls = tl.row0 + min(lm, tl.mrows - 1);
+      const int lv = g.mc.by_order ? g.order[ls] : ls;
+      int orow = lm < tl.mrows && (unsigned)lv < (unsigned)g.rows ? lv : -1;
+      asm volatile("" : "+v"(orow));
+      __syncthreads();                       // every wave is past its last read of the ring
+      const int n = tl.n0 + 8 * (lane & 31);
+      if (nx.mrows > 0) {
+        place(nx);
+        prologue();
+      }
+      // 512-byte rows of 32 16-byte granules, granule c of row r at c ^ (r &
+      // 31), so the rows a fragment writes and the granules a row read takes
+      // both spread over the banks and every store writes whole rows.
 #pragma unroll
-  for (int f = 0; f < FJW; ++f) read_codes(b0, 0, f);
+      for (int p = 0; p < FIW; ++p) {
+        const int r = (WM == 2 ? 32 * (w >> 1) : 0) + l32;
 #pragma unroll
-  for (int f = 0; f < FIW; ++f) {
-    read_a(b0, 0, f, fa[0]);
-    if (S4) sa[0][f] = read_scale(b0.sa, 0, f);
-  }
+        for (int fj = 0; fj < FJW; ++fj)
 #pragma unroll
-  for (int f = 0; f < FJW; ++f) {
-    read_b(b0, 0, f, fb[0]);
-    if (S4) sb[0][f] = read_scale(b0.sb, 0, f);
+          for (int gg = 0; gg < 4; ++gg) {
+            const int c = (wcol >> 3) + 4 * fj + gg;
+            u32x2 pk;
+            pk[0] = pack_bf16x2(acc[p][fj][4 * gg + 0], acc[p][fj][4 * gg + 1]);
+            pk[1] = pack_bf16x2(acc[p][fj][4 * gg + 2], acc[p][fj][4 * gg + 3]);
+            *reinterpret_cast<u32x2*>(ct + r * 512 + 16 * (c ^ (r & 31)) + 8 * half) = pk;
+          }
+        lds_barrier();
+#pragma unroll
+        for (int it = 0; it < PI; ++it) {
+          const int mr = PR / 4 * w + 2 * it + half;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(ct + mr * 512 + 16 * ((lane & 31) ^ (mr & 31)));
+          const int r0 = __builtin_amdgcn_readlane(orow, 2 * (p * PI + it));
+          const int r1 = __builtin_amdgcn_readlane(orow, 2 * (p * PI + it) + 1);
+          const int64_t a0 = r0 * g.ldc, a1 = r1 * g.ldc;
+          if ((half ? r1 : r0) >= 0 && n < g.N)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (half ? a1 : a0) + n) = x;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (p + 1 < FIW) lds_barrier();
+      }
+      if (nx.mrows <= 0) break;
+      tl = nx;
+    }
   }
-  int s = 0;
-  for (; (s + D + 1) * KD <= klen; ++s) step_block(s, std::integral_constant<int, 0>());
-  for (; s + D < nsteps; ++s) step_block(s, std::integral_constant<int, 1>());
-  if constexpr (RING4)
-    for (; s + 1 < nsteps; ++s) step_block(s, std::integral_constant<int, 3>());
-  for (; s < nsteps; ++s) step_block(s, std::integral_constant<int, 2>());
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  if constexpr (DW) store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
-  else store_bf16<BM>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, wrow, wcol, w, lane);
 }
+
 
 namespace {
 
 int64_t rows_grid(const ExpertArgs& a, int bm) {
   return max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, bm) * ((a.N + 255) / 256);
 }
+// Pipelined kernel: at most one workgroup per CU (the ring takes its LDS),
+// each walking the tiles.
+constexpr int64_t kCus = 256;
+template <int AL, int BL, int FI>
+void rows_pipe(const ExpertArgs& a, hipStream_t s) {
+  const int64_t most = rows_grid(a, 64 * FI), grid = most < kCus ? most : kCus;
+  hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, false, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
+}
 template <int AL, int BL>
 void rows_size(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96)
-    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 1, false, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
-  else if (mean <= 384)
-    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 2, false, false>), dim3((unsigned)rows_grid(a, 128)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_expert_pipe<AL, BL, 4, false, false>), dim3((unsigned)rows_grid(a, 256)), dim3(256), 0, s, a);
+  if (mean <= 96) rows_pipe<AL, BL, 1>(a, s);
+  else if (mean <= 384) rows_pipe<AL, BL, 2>(a, s);
+  else rows_pipe<AL, BL, 4>(a, s);
 }
 template <int BL>
 void rows_f32(const ExpertArgs& a, hipStream_t s) {

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(512) void k_expert_few(ExpertArgs a) {
   constexpr int COLS = TR::COLS, NJ = TR::NJ, KD = TR::KD, NW = 8, BM = 16 * MB;
   __shared__ float sums[NW][BM][COLS + 4];
   const int nN = (a.N + COLS - 1) / COLS;
-  const RowTile t = row_tile<BM, 1>(a, nN);
+  const RowTile t = RowTiles<BM, 1>(a, nN).at(a, blockIdx.x);
   if (t.mrows <= 0) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
   const int n0 = t.tn * COLS, K = a.K;
