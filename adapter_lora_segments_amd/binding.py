@@ -16,9 +16,15 @@ from . import _lib
 from ._lib import check, lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch  # imported first so libmlora binds to torch's HIP runtime
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch  # imported first so libmlora binds to torch's HIP runtime
+        _torch_module = torch
+    return _torch_module
 
 
 class Plan:
@@ -478,28 +484,51 @@ class AdamW:
 
 # ---- grouped expert products, row grouping, MXFP4 quantization ----
 
-def _launch(tensors, stream, call):
-    """Run ``call(stream handle)`` on the device that holds ``tensors`` (None
-    entries skipped): on ``stream``, which must be of that device, or on that
-    device's current stream."""
+# These calls run in decode steps, where the host's share of a call counts:
+# the checks below look at each tensor once and build messages only to raise
+# them, and pointers reach the library as plain integers.
+
+def _need(t, name, shape, dtype):
+    """_check_t, with the common case first."""
+    if t is None or t.dtype != dtype or not t.is_cuda or (shape is not None and t.shape != shape) \
+            or not t.is_contiguous():
+        _check_t(t, name, shape, dtype)
+
+
+def _raw_stream(stream, index):
     torch = _torch()
-    index = None
-    for t in tensors:
-        if t is None:
-            continue
-        i = t.device.index
-        if index is None:
-            index = i
-        elif i != index:
-            raise ValueError(f"tensors are on different devices: cuda:{index} and cuda:{i}")
-    if stream is not None and stream.device.index != index:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-    s = stream if stream is not None else torch.cuda.current_stream(index)
+    return stream.cuda_stream
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _one_device(*tensors):
+    """Device index of ``tensors`` (None entries skipped), which must agree."""
+    index = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if index < 0:
+                index = i
+            elif i != index:
+                raise ValueError(f"tensors are on different devices: cuda:{index} and cuda:{i}")
+    return index
+
+
+def _launch(index, fn, *args):
+    """check(fn(*args)) with device ``index`` current."""
+    torch = _torch()
     if index == torch.cuda.current_device():
-        check(call(ctypes.c_void_p(s.cuda_stream)))
+        check(fn(*args))
     else:
         with torch.cuda.device(index):
-            check(call(ctypes.c_void_p(s.cuda_stream)))
+            check(fn(*args))
 
 
 def group_rows_workspace(rows: int, n_groups: int) -> int:
@@ -514,14 +543,15 @@ def mlora_group_rows(ids, n_groups: int, offsets, order, ws=None, stream=None):
     [0, n_groups): no group): offsets [n_groups + 1] and order [rows] int32;
     positions behind the last group hold -1."""
     torch = _torch()
-    _check_t(ids, "ids", (ids.numel(),), torch.int32)
-    _check_t(offsets, "offsets", (n_groups + 1,), torch.int32)
-    _check_t(order, "order", (ids.numel(),), torch.int32)
+    rows = ids.numel()
+    _need(ids, "ids", (rows,), torch.int32)
+    _need(offsets, "offsets", (n_groups + 1,), torch.int32)
+    _need(order, "order", (rows,), torch.int32)
     if ws is not None:
-        _check_t(ws, "ws", None, torch.uint8)
-    _launch((ids, offsets, order, ws), stream,
-            lambda s: lib().mlora_group_rows(_p(ids), ids.numel(), n_groups, _p(offsets), _p(order), _p(ws),
-                                             0 if ws is None else ws.numel(), s))
+        _need(ws, "ws", None, torch.uint8)
+    i = _one_device(ids, offsets, order, ws)
+    _launch(i, lib().mlora_group_rows, ids.data_ptr(), rows, n_groups, offsets.data_ptr(), order.data_ptr(), _ptr(ws),
+            0 if ws is None else ws.numel(), _raw_stream(stream, i))
     return offsets, order
 
 
@@ -538,9 +568,11 @@ class RowGroups:
         self.ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
     def group(self, ids, stream=None):
-        if ids.numel() > self.max_rows:
-            raise ValueError(f"{ids.numel()} ids for buffers of {self.max_rows} rows")
-        return mlora_group_rows(ids, self.n_groups, self.offsets, self.order[:ids.numel()], self.ws, stream)
+        rows = ids.numel()
+        if rows > self.max_rows:
+            raise ValueError(f"{rows} ids for buffers of {self.max_rows} rows")
+        order = self.order if rows == self.max_rows else self.order[:rows]
+        return mlora_group_rows(ids, self.n_groups, self.offsets, order, self.ws, stream)
 
 
 class ExpertShape:
@@ -561,44 +593,52 @@ class ExpertShape:
         self.dtype, self.w_layout, self.w_format, self.act_format = dtype, w_layout, w_format, act_format
         self.top_k, self.x_order, self.y_order = int(top_k), bool(x_order), bool(y_order)
         self.grad_accumulate = bool(grad_accumulate)
-        self.workspace_bytes = 0
+        self._c = _lib.ExpertShape(self.rows, self.d_in, self.d_out, self.n_experts, _lib.DTYPES[dtype],
+                                   _lib.W0_LAYOUTS[w_layout], _lib.W0_FORMATS[w_format],
+                                   _lib.EXPERT_ACT_FORMATS[act_format], self.top_k, int(self.x_order),
+                                   int(self.y_order), int(self.grad_accumulate))
         n = ctypes.c_int64()
         check(lib().mlora_expert_workspace(ctypes.byref(self.struct(self.rows)), ctypes.byref(n)))
         self.workspace_bytes = n.value
+        # shape of all experts' weights (MXFP4: of the packed buffer)
+        if w_format == "mxfp4":
+            self.w_shape = (microscale_bytes(self.n_experts * self.d_out, self.d_in),)
+        else:
+            self.w_shape = (self.n_experts,) + ((self.d_in, self.d_out) if w_layout == "kn" else (self.d_out, self.d_in))
 
     def struct(self, rows: int):
-        return _lib.ExpertShape(rows, self.d_in, self.d_out, self.n_experts, _lib.DTYPES[self.dtype],
-                                _lib.W0_LAYOUTS[self.w_layout], _lib.W0_FORMATS[self.w_format],
-                                _lib.EXPERT_ACT_FORMATS[self.act_format], self.top_k, int(self.x_order),
-                                int(self.y_order), int(self.grad_accumulate))
+        """The C structure for a call of ``rows`` rows (never changed once made:
+        a call on another thread may be reading it)."""
+        c = self._c
+        if c.rows != rows:
+            c = _lib.ExpertShape.from_buffer_copy(c)
+            c.rows = rows
+            self._c = c
+        return c
 
     def src_rows(self, rows: int) -> int:
         return rows // self.top_k if self.x_order else rows
-
-    @property
-    def w_shape(self):
-        """Shape of all experts' weights (MXFP4: of the packed buffer)."""
-        if self.w_format == "mxfp4":
-            return (microscale_bytes(self.n_experts * self.d_out, self.d_in),)
-        return (self.n_experts,) + ((self.d_in, self.d_out) if self.w_layout == "kn" else (self.d_out, self.d_in))
 
     def alloc_workspace(self, device="cuda"):
         torch = _torch()
         return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device) if self.workspace_bytes else None
 
 
-def _check_expert(shape: ExpertShape, rows: int, W, offsets, order, ws):
+def _check_weight(shape: ExpertShape, W):
+    torch = _torch()
+    _need(W, "W", shape.w_shape, torch.uint8 if shape.w_format == "mxfp4" else _dt(shape))
+
+
+def _check_tables(shape: ExpertShape, rows: int, offsets, order, ws):
     torch = _torch()
     if rows > shape.rows:
         raise ValueError(f"{rows} rows for a shape of at most {shape.rows}")
-    if W is not None:
-        _check_t(W, "W", shape.w_shape, torch.uint8 if shape.w_format == "mxfp4" else _dt(shape))
     if offsets is not None:
-        _check_t(offsets, "offsets", (shape.n_experts + 1,), torch.int32)
+        _need(offsets, "offsets", (shape.n_experts + 1,), torch.int32)
     if order is not None:
-        _check_t(order, "order", (rows,), torch.int32)
+        _need(order, "order", (rows,), torch.int32)
     if ws is not None:
-        _check_t(ws, "ws", None, torch.uint8)
+        _need(ws, "ws", None, torch.uint8)
 
 
 def mlora_expert_forward(shape: ExpertShape, X, W, offsets, order, Y, ws=None, stream=None):
@@ -606,15 +646,13 @@ def mlora_expert_forward(shape: ExpertShape, X, W, offsets, order, Y, ws=None, s
     of Y that belong to no group are left as they were)."""
     rows = Y.shape[0]
     dt = _dt(shape)
-    _check_t(X, "X", (shape.src_rows(rows), shape.d_in), dt)
-    _check_t(Y, "Y", (rows, shape.d_out), dt)
-    if W is None:
-        raise ValueError("W is required")
-    _check_expert(shape, rows, W, offsets, order, ws)
-    c = shape.struct(rows)
-    _launch((X, W, offsets, order, Y, ws), stream,
-            lambda s: lib().mlora_expert_forward(ctypes.byref(c), _p(X), _p(W), _p(offsets), _p(order), _p(Y),
-                                                 _p(ws), 0 if ws is None else ws.numel(), s))
+    _need(X, "X", (shape.src_rows(rows), shape.d_in), dt)
+    _need(Y, "Y", (rows, shape.d_out), dt)
+    _check_weight(shape, W)
+    _check_tables(shape, rows, offsets, order, ws)
+    i = _one_device(X, W, offsets, order, Y, ws)
+    _launch(i, lib().mlora_expert_forward, ctypes.byref(shape.struct(rows)), X.data_ptr(), W.data_ptr(), _ptr(offsets),
+            _ptr(order), Y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, i))
     return Y
 
 
@@ -624,18 +662,20 @@ def mlora_expert_backward(shape: ExpertShape, dY, X, W, offsets, order, dX, dW, 
     torch = _torch()
     rows = dY.shape[0]
     dt = _dt(shape)
-    _check_t(dY, "dY", (rows, shape.d_out), dt)
+    _need(dY, "dY", (rows, shape.d_out), dt)
     if X is not None:
-        _check_t(X, "X", (shape.src_rows(rows), shape.d_in), dt)
+        _need(X, "X", (shape.src_rows(rows), shape.d_in), dt)
+    if W is not None:
+        _check_weight(shape, W)
     if dX is not None:
-        _check_t(dX, "dX", (rows, shape.d_in), dt)
+        _need(dX, "dX", (rows, shape.d_in), dt)
     if dW is not None:
-        _check_t(dW, "dW", shape.w_shape, torch.float32)
-    _check_expert(shape, rows, W, offsets, order, ws)
-    c = shape.struct(rows)
-    _launch((dY, X, W, offsets, order, dX, dW, ws), stream,
-            lambda s: lib().mlora_expert_backward(ctypes.byref(c), _p(dY), _p(X), _p(W), _p(offsets), _p(order),
-                                                  _p(dX), _p(dW), _p(ws), 0 if ws is None else ws.numel(), s))
+        _need(dW, "dW", shape.w_shape, torch.float32)
+    _check_tables(shape, rows, offsets, order, ws)
+    i = _one_device(dY, X, W, offsets, order, dX, dW, ws)
+    _launch(i, lib().mlora_expert_backward, ctypes.byref(shape.struct(rows)), dY.data_ptr(), _ptr(X), _ptr(W),
+            _ptr(offsets), _ptr(order), _ptr(dX), _ptr(dW), _ptr(ws), 0 if ws is None else ws.numel(),
+            _raw_stream(stream, i))
     return dX
 
 
@@ -650,7 +690,7 @@ class ExpertLinear:
     def __init__(self, W, n_experts: int, d_in: int, d_out: int, max_rows: int, **options):
         torch = _torch()
         self.shape = ExpertShape(max_rows, n_experts, d_in, d_out, **options)
-        _check_expert(self.shape, 0, W, None, None, None)
+        _check_weight(self.shape, W)
         self.W = W
         self.ws = self.shape.alloc_workspace(W.device)
         self.dW = None
@@ -709,12 +749,11 @@ def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", strea
     n = microscale_bytes(rows, cols)
     if q is None:
         q = torch.empty(n, dtype=torch.uint8, device=X.device)
-    _check_t(q, "q", (n,), torch.uint8)
+    _need(q, "q", (n,), torch.uint8)
     if values is not None:
-        _check_t(values, "values", (rows, cols), X.dtype)
-    dt = _lib.DTYPES["bf16" if X.dtype == torch.bfloat16 else "fp32"]
-    ld = X.stride(0) if rows > 1 else cols
-    _launch((X, q, values), stream,
-            lambda s: lib().mlora_microscale_quantize(_p(X), dt, rows, cols, ld, 1 if along == "rows" else 0, _p(q),
-                                                      _p(values), s))
+        _need(values, "values", (rows, cols), X.dtype)
+    i = _one_device(X, q, values)
+    _launch(i, lib().mlora_microscale_quantize, X.data_ptr(), 1 if X.dtype == torch.bfloat16 else 0, rows, cols,
+            X.stride(0) if rows > 1 else cols, 1 if along == "rows" else 0, q.data_ptr(), _ptr(values),
+            _raw_stream(stream, i))
     return q

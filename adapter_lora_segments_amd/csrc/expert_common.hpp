@@ -7,6 +7,16 @@
 
 namespace mlora {
 
+// The kernel's ExpertArgs (its only parameter) read from the kernel argument
+// segment where they are used.  Kept in scalar registers across a loop over
+// tiles they would push the loop's own scalars out; the empty asm hides that
+// two calls give the same pointer.
+__device__ __forceinline__ const ExpertArgs& kernel_args() {
+  auto p = (const __attribute__((address_space(4))) ExpertArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ExpertArgs*)p;
+}
+
 // n / d for 0 <= n < 2^31 (div_by).
 __device__ __forceinline__ uint32_t div_fast(uint32_t n, const DivBy& d) {
   return d.mul ? __umulhi(n, d.mul) >> d.shift : n;

@@ -43,8 +43,8 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 //   KC: contiguous along the reduction; a unit is one row of 128 bytes per
 //       tile row (64 bf16 or 32 fp32 of the reduction), chunk c (16 bytes) of
 //       row r at c ^ kx8(r).
-//   NC: contiguous along the output; a unit is one row of 256 output elements
-//       per reduction step element.
+//   NC: contiguous along the output; a unit is one row of the tile's output
+//       elements per reduction step element.
 //   F4: E2M1 codes along the reduction, 32 bytes (64 elements) per tile row,
 //       chunk h of row r at h ^ ((r >> 3) & 1), and one dword of scale codes
 //       per row that covers the step (it holds 128 elements' scales).
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
 
 // ---------------------------------------------------------------------------
 // Pipelined tile kernel for bf16 operands (and E2M1 weights): the base GEMM's
-// schedule over ragged groups.  A 64 FI x 256 tile per workgroup of four
+// schedule over ragged groups.  A 64 FI x 64 NJ tile per workgroup of four
 // waves, 64-deep steps, one unit of LDS per operand and step.  The ring holds
 // as many steps as fit (at most six) and a step copies D steps ahead; with
 // 32 KiB units (FI = 4, D = 2) five units fill the 160 KiB, unit u in slot
@@ -353,48 +353,50 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
 // by four conversions while the slice before is computed, so the weights
 // cross LDS at 4 bits and no decoded copy exists.
 // ---------------------------------------------------------------------------
-template <int AL, int BL, int FI, bool DW, bool GATHER>
-__global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
+template <int AL, int BL, int FI, int NJ, bool DW, bool GATHER>
+__global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   constexpr bool S4 = AL >= X4, S16 = AL == X4;          // both operands E2M1; their scales' alignment
   constexpr bool AK = AL != NC, BK = BL == KC || S4;     // k-contiguous 128-byte rows
-  constexpr int BM = 64 * FI, BN = 256, KD = S4 ? 256 : 64, EPC = S4 ? 32 : 8;
+  constexpr int BM = 64 * FI, BN = 64 * NJ, KD = S4 ? 256 : 64, EPC = S4 ? 32 : 8;
   // Waves along M: with E2M1 weights each wave decodes its own columns, so the
   // four waves share the columns out and all take every row.
   constexpr int WM = BL == F4 ? 1 : 2, FIW = BM / 32 / WM, FJW = BN / 32 / (4 / WM), NS = FIW * FJW;
-  constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + BN * 4 : BN * 128;
+  constexpr int UA = BM * 128, UB = BL == F4 ? BN * 32 + 1024 : BN * 128;
   // Ring: five units (RING5), four units (RING4: the scales take the rest), or
   // NR whole steps; D: steps ahead that a step copies.
-  constexpr bool RING5 = FI == 4 && !S4 && BL != F4, RING4 = FI == 4 && S4;
+  constexpr bool RING5 = UA + UB == 65536 && !S4, RING4 = UA + UB == 65536 && S4;
   constexpr int SCL = S4 ? 16384 : 0, FIT = (160 * 1024 - SCL) / (UA + UB);
   constexpr int NR = RING5 || RING4 ? 2 : FIT > 6 ? 6 : FIT;
   constexpr int D = RING5 || RING4 ? 2 : NR - 1;
-  constexpr int CA = UA / 4096, CB = BL == F4 ? 2 : 8;   // 1 KiB copies per wave and unit
+  constexpr int CA = UA / 4096, CB = UB / 4096;          // 1 KiB copies per wave and unit
   constexpr int CBW = CB + (BL == F4 ? 1 : 0);           // and the scale dwords
   constexpr int RING = RING5 ? 5 * UA : NR * (UA + UB);
   // What the first D steps of a tile leave free: the epilogue's rows.
   constexpr int SPARE = RING5 ? 4 * UA : RING4 ? 2 * UA : (NR - 1) * (UA + UB);
-  static_assert(DW || (RING5 || RING4 ? UA : UA + UB) >= (WM == 2 ? 64 : 32) * 512, "an epilogue phase fits");
+  static_assert(DW || (RING5 || RING4 ? UA : UA + UB) >= (WM == 2 ? 64 : 32) * 2 * BN, "an epilogue phase fits");
   __shared__ u32x4 ring[(RING + SCL) / 16];
 
-  const RowTiles<BM, 4> tiles(g, DW ? 0 : (g.N + BN - 1) / BN);
+  const RowTiles<BM, 4> tiles(kernel_args(), DW ? 0 : (kernel_args().N + BN - 1) / BN);
   auto rows_tile = [&](int b) {
+    const ExpertArgs& g = kernel_args();
     const RowTile r = tiles.at(g, b);
     return Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
   };
   Tile tl;
-  if constexpr (DW) tl = find_tile<BM, DW>(g);
+  if constexpr (DW) tl = find_tile<BM, DW>(kernel_args());
   else tl = rows_tile(blockIdx.x);
   if (tl.mrows <= 0) return;
   const int klen = tl.klen, nsteps = (klen + KD - 1) / KD;
-  if (DW && nsteps == 0) return store_zero<BM>(g, tl);
+  if (DW && nsteps == 0) return store_zero<BM>(kernel_args(), tl);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
-  const int wrow = WM == 2 ? 32 * FIW * (w >> 1) : 0, wcol = WM == 2 ? 128 * (w & 1) : 64 * w;
+  const int wrow = WM == 2 ? 32 * FIW * (w >> 1) : 0, wcol = 32 * FJW * (WM == 2 ? w & 1 : w);
   const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
   // bytes of a row of either operand
-  const int64_t arow = S4 ? g.lda / 2 : g.lda * 2, brow = BL == F4 || S4 ? g.ldb / 2 : g.ldb * 2;
+  auto a_row = [](const ExpertArgs& g) -> int64_t { return S4 ? g.lda / 2 : g.lda * 2; };
+  auto b_row = [](const ExpertArgs& g) -> int64_t { return BL == F4 || S4 ? g.ldb / 2 : g.ldb * 2; };
 
   // Copy sources.  k-contiguous: copy i of a wave takes tile rows 8 (C w + i)
   // + lane / 8 at LDS position lane % 8, which holds chunk (lane % 8) ^
@@ -410,6 +412,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   // bases of step 0 and bytes per step
   const uint8_t* baseA = nullptr;
   const uint8_t* baseB = nullptr;
+  const int64_t arow = a_row(kernel_args()), brow = b_row(kernel_args());   // dead where not used below
   const int64_t stepA = KD * arow;
   const int64_t stepB = BK ? 128 : BL == F4 ? 32 : KD * brow;
   auto place = [&](const Tile& t) {
@@ -417,6 +420,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     // registers beside the accumulators)
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
+    const ExpertArgs& g = kernel_args();
+    const int64_t arow = a_row(g), brow = b_row(g);
 #pragma unroll
     for (int i = 0; i < CA; ++i) {
       if constexpr (AK) {
@@ -441,7 +446,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
         const int col = min(t.n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
         bo[i] = (uint32_t)(GATHER ? col * 2 : bc[i] * brow + (col - t.n0) * 2);
       } else {
-        const int r = 32 * (2 * w + i) + (lane >> 1);
+        const int r = 32 * (CB * w + i) + (lane >> 1);
         bc[i] = 0;
         bo[i] = (uint32_t)((min(t.n0 + r, g.N - 1) - t.n0) * brow + 16 * ((lane & 1) ^ ((r >> 3) & 1)));
       }
@@ -455,6 +460,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   };
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
+  const uint32_t lds_a = lds0 + 1024u * (uint32_t)(CA * w), lds_b = lds0 + 1024u * (uint32_t)(CB * w);
   auto slot = [](int u) -> uint32_t {
     if constexpr (RING5) return (uint32_t)(u % 5) * UA;
     else if constexpr (RING4) return (uint32_t)(u & 3) * UA;
@@ -465,16 +471,19 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   // the row that copy i of either operand reads: k-row 16 w + 2 i + lane / 32.
   static_assert(!GATHER || (AL == NC && BL == NC && FI == 4), "both operands copy two k-rows at a time");
   int oidx[GATHER ? 16 : 1];
+  const int32_t* const order = GATHER ? kernel_args().order : nullptr;
+  const RowMap ma = kernel_args().ma, mb = kernel_args().mb;   // GATHER only
+  const int nrows = kernel_args().rows;
   auto load_order = [&](int t) {
     if constexpr (GATHER) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) oidx[j] = ldc(g.order + tl.row0 + min(t * KD + 16 * w + j, klen - 1));
+      for (int j = 0; j < 16; ++j) oidx[j] = ldc(order + tl.row0 + min(t * KD + 16 * w + j, klen - 1));
     }
   };
   auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t row_bytes, int i, int t) -> const uint8_t* {
     const int k = tl.row0 + t * KD + 16 * w + 2 * i;
     auto at = [&](int h) -> int64_t {
-      return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], g.rows), map.div)
+      return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], nrows), map.div)
                            : (int64_t)(k + h)) *
              row_bytes;
     };
@@ -484,12 +493,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   // Copy i of step t's A (B) unit.  CHECK: the step may pass the end of the
   // reduction, and what does reads zeros.
   auto copy_a = [&](int t, int i, auto check) {
-    const uint32_t lds = lds0 + slot(2 * t) + 1024u * (uint32_t)(CA * w + i);
+    const uint32_t lds = lds_a + slot(2 * t) + 1024u * i;
     if constexpr (AK) {
       const uint8_t* src = ap[i] + 128 * (int64_t)t;
       dma16_at(!check.value || t * KD + EPC * ac[i] < klen ? src : zero, lds);
     } else if constexpr (GATHER) {
-      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, g.ma, arow, i, t) + ao[i] : zero, lds);
+      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, ma, arow, i, t) + ao[i] : zero, lds);
     } else if constexpr (check.value) {
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseA + t * stepA));
       dma16_at(t * KD + ac[i] < klen ? at + ao[i] : zero, lds);
@@ -498,9 +507,9 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
     }
   };
   auto copy_b = [&](int t, int i, auto check) {
-    const uint32_t lds = lds0 + slot(2 * t + 1) + 1024u * (uint32_t)(CB * w + i);
+    const uint32_t lds = lds_b + slot(2 * t + 1) + 1024u * i;
     if constexpr (BL == NC && GATHER) {
-      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, g.mb, brow, i, t) + bo[i] : zero, lds);
+      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, mb, brow, i, t) + bo[i] : zero, lds);
     } else if constexpr (check.value) {
       const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + EPC * bc[i] < klen;
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseB + t * stepB));
@@ -560,7 +569,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   for (int i = 0; i < 4; ++i) {
     al[i] = AK ? lane_kc(wrow + l32, i) : lane_nc(CPRA, wrow + 32 * (i < FIW ? i : 0));
     if constexpr (BK) bl[i] = lane_kc(wcol + l32, i);
-    else if constexpr (BL == NC) bl[i] = lane_nc(CPRB, wcol + 32 * i);
+    else if constexpr (BL == NC) bl[i] = lane_nc(CPRB, wcol + 32 * (i < FJW ? i : 0));
     else bl[i] = (uint32_t)(((wcol + 32 * (i < FJW ? i : 0) + l32) * 2 + (half ^ ((l32 >> 3) & 1))) * 16);
   }
   struct Bases {
@@ -768,12 +777,14 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
   prologue();
   if constexpr (DW) {
     main_loop();
-    store_dw<FI>(g, acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+    store_dw<FI>(kernel_args(), acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
   } else {
     // The grid is one workgroup per CU: each takes every gridDim.x-th tile and
     // starts the next one's copies before it stores this one's rows.
     char* const ct = reinterpret_cast<char*>(&ring[0]) + SPARE;
-    constexpr int PR = WM == 2 ? 64 : 32, PI = PR / 8;      // rows of an epilogue phase; row pairs per wave
+    // An epilogue phase: PR rows of GPR 16-byte granules; a store instruction
+    // covers RPI of them, a wave stores PI times.
+    constexpr int PR = WM == 2 ? 64 : 32, GPR = BN / 8, RPI = 64 / GPR, PI = PR / 4 / RPI;
     for (int b = blockIdx.x;;) {
       main_loop();
       b += gridDim.x;
@@ -781,23 +792,24 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
       int lane = threadIdx.x & 63;           // opaque, as in place
       asm volatile("" : "+v"(lane));
       const int half = lane >> 5, l32 = lane & 31;
+      const ExpertArgs& g = kernel_args();
       // Phase p stores fragment row p of every wave.  Lane l holds the row of
       // C that the wave's l-th stored row goes to (or -1), loaded before the
       // copies (a load's use waits for every copy issued before it).
-      const int lp = (lane / (2 * PI)) % FIW, lr = PR / 4 * w + lane % (2 * PI);
+      const int lp = (lane / (PR / 4)) % FIW, lr = PR / 4 * w + lane % (PR / 4);
       const int lm = 32 * FIW * (lr >> 5) + 32 * lp + (lr & 31), ls = tl.row0 + min(lm, tl.mrows - 1);
       const int lv = g.mc.by_order ? g.order[ls] : ls;
       int orow = lm < tl.mrows && (unsigned)lv < (unsigned)g.rows ? lv : -1;
       asm volatile("" : "+v"(orow));
       __syncthreads();                       // every wave is past its last read of the ring
-      const int n = tl.n0 + 8 * (lane & 31);
+      const int n = tl.n0 + 8 * (lane % GPR);
       if (nx.mrows > 0) {
         place(nx);
         prologue();
       }
-      // 512-byte rows of 32 16-byte granules, granule c of row r at c ^ (r &
-      // 31), so the rows a fragment writes and the granules a row read takes
-      // both spread over the banks and every store writes whole rows.
+      // Granule c of row r at c ^ (r % GPR), so the rows a fragment writes and
+      // the granules a row read takes both spread over the banks and every
+      // store writes whole rows.
 #pragma unroll
       for (int p = 0; p < FIW; ++p) {
         const int r = (WM == 2 ? 32 * (w >> 1) : 0) + l32;
@@ -809,18 +821,16 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
             u32x2 pk;
             pk[0] = pack_bf16x2(acc[p][fj][4 * gg + 0], acc[p][fj][4 * gg + 1]);
             pk[1] = pack_bf16x2(acc[p][fj][4 * gg + 2], acc[p][fj][4 * gg + 3]);
-            *reinterpret_cast<u32x2*>(ct + r * 512 + 16 * (c ^ (r & 31)) + 8 * half) = pk;
+            *reinterpret_cast<u32x2*>(ct + r * (2 * BN) + 16 * (c ^ (r % GPR)) + 8 * half) = pk;
           }
         lds_barrier();
 #pragma unroll
         for (int it = 0; it < PI; ++it) {
-          const int mr = PR / 4 * w + 2 * it + half;
-          const u32x4 x = *reinterpret_cast<const u32x4*>(ct + mr * 512 + 16 * ((lane & 31) ^ (mr & 31)));
-          const int r0 = __builtin_amdgcn_readlane(orow, 2 * (p * PI + it));
-          const int r1 = __builtin_amdgcn_readlane(orow, 2 * (p * PI + it) + 1);
-          const int64_t a0 = r0 * g.ldc, a1 = r1 * g.ldc;
-          if ((half ? r1 : r0) >= 0 && n < g.N)
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + (half ? a1 : a0) + n) = x;
+          const int mr = PR / 4 * w + RPI * it + lane / GPR;
+          const u32x4 x = *reinterpret_cast<const u32x4*>(ct + mr * (2 * BN) + 16 * ((lane % GPR) ^ (mr % GPR)));
+          const int row = __shfl(orow, p * (PR / 4) + RPI * it + lane / GPR);
+          if (row >= 0 && n < g.N)
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.C) + row * g.ldc + n) = x;
           __builtin_amdgcn_sched_barrier(0);
         }
         if (p + 1 < FIW) lds_barrier();
@@ -834,33 +844,33 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs g) {
 
 namespace {
 
-int64_t rows_grid(const ExpertArgs& a, int bm) {
-  return max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, bm) * ((a.N + 255) / 256);
+int64_t rows_grid(const ExpertArgs& a, int bm, int bn) {
+  return max_row_tiles(a.rows, a.offsets ? a.n_experts : 1, bm) * ((a.N + bn - 1) / bn);
 }
 // Pipelined kernel: at most one workgroup per CU (the ring takes its LDS),
 // each walking the tiles.
 constexpr int64_t kCus = 256;
-template <int AL, int BL, int FI>
+template <int AL, int BL, int FI, int NJ>
 void rows_pipe(const ExpertArgs& a, hipStream_t s) {
-  const int64_t most = rows_grid(a, 64 * FI), grid = most < kCus ? most : kCus;
-  hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, false, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  const int64_t most = rows_grid(a, 64 * FI, 64 * NJ), grid = most < kCus ? most : kCus;
+  hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, NJ, false, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
 }
 template <int AL, int BL>
 void rows_size(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96) rows_pipe<AL, BL, 1>(a, s);
-  else if (mean <= 384) rows_pipe<AL, BL, 2>(a, s);
-  else rows_pipe<AL, BL, 4>(a, s);
+  if (mean <= 96) rows_pipe<AL, BL, 1, 4>(a, s);
+  else if (mean <= 384) rows_pipe<AL, BL, 2, 4>(a, s);
+  else rows_pipe<AL, BL, 4, 4>(a, s);
 }
 template <int BL>
 void rows_f32(const ExpertArgs& a, hipStream_t s) {
   const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
   if (mean <= 96)
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64, 256)), dim3(256), 0, s, a);
   else if (mean <= 384)
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 2, false>), dim3((unsigned)rows_grid(a, 128)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 2, false>), dim3((unsigned)rows_grid(a, 128, 256)), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 4, false>), dim3((unsigned)rows_grid(a, 256)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_expert_f32<KC, BL, 4, false>), dim3((unsigned)rows_grid(a, 256, 256)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -892,8 +902,8 @@ void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const dim3 dg((unsigned)grid);
   if (f32) hipLaunchKernelGGL((k_expert_f32<NC, NC, 4, true>), dg, dim3(256), 0, s, a);
   else if (a.ma.by_order || a.mb.by_order)
-    hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, true>), dg, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, true, false>), dg, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, 4, true, true>), dg, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, 4, true, false>), dg, dim3(256), 0, s, a);
 }
 
 }  // namespace mlora

@@ -271,7 +271,8 @@ void few(const ExpertArgs& a, hipStream_t s) {
 void launch_expert_few(ExpertForm form, bool b_kc, int row_blocks, const ExpertArgs& a, hipStream_t s) {
 #define MLORA_FEW(F) \
   if (row_blocks == 1) few<F, 1>(a, s); \
-  else few<F, 2>(a, s);
+  else if (row_blocks == 2) few<F, 2>(a, s); \
+  else few<F, 4>(a, s);
   switch (form) {
     case ExpertForm::kBf16:
       if (b_kc) { MLORA_FEW(W16_KC) } else { MLORA_FEW(W16_NC) }
