@@ -62,15 +62,15 @@ __device__ __forceinline__ int nx16(int kr) { return ((kr & 1) ? 4 : 0) ^ ((kr &
 // puts them on the two halves of the banks.
 __device__ __forceinline__ int nx32(int kr) { return (kr & 4) ? 8 : 0; }
 
-// A workgroup's tile: 64 FI rows (dW: rows of dW_e) x 256 columns of expert e.
+// A workgroup's tile: BM rows (dW: rows of dW_e) x BN columns of expert e.
 struct Tile {
   int e, row0, mrows;   // grouped rows [row0, row0 + mrows); dW: row0 is the group's first row, mrows the tile's
   int m0, n0;           // first row of dW_e (else 0) and first column
   int klen;             // length of the reduction
 };
-template <int BM, bool DW>
+template <int BM, int BN, bool DW>
 __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
-  const int nN = (g.N + 255) / 256;
+  const int nN = (g.N + BN - 1) / BN;
   Tile t;
   if constexpr (DW) {
     // Experts have reductions of different lengths: every expert's tiles are
@@ -95,7 +95,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
     constexpr int GM = 4;
     const int fm = i / (GM * nN) * GM, gm = min(GM, nM - fm), within = i - fm * nN;
     t.m0 = (fm + within % gm) * BM;
-    t.n0 = within / gm * 256;
+    t.n0 = within / gm * BN;
     int hi;
     group_rows(g, t.e, t.row0, hi);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
@@ -103,7 +103,7 @@ __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
     t.mrows = i < TT ? min(BM, g.M - t.m0) : 0;
   } else {
     const RowTile r = RowTiles<BM, 4>(g, nN).at(g, blockIdx.x);
-    t = Tile{r.e, r.row0, r.mrows, 0, r.tn * 256, g.K};
+    t = Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
   }
   return t;
 }
@@ -119,8 +119,8 @@ __device__ __forceinline__ int out_row(const ExpertArgs& g, const Tile& t, int m
 // Epilogues.  acc[fi][fj][4 gg + x] holds C[m = wrow + 32 fi + l32][n = wcol
 // + 32 fj + 8 gg + 4 half + x].  fp32 kernel: straight to memory, four columns
 // a lane.
-template <int FI, bool DW>
-__device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][4], const Tile& t, int wrow,
+template <int FI, int FJ, bool DW>
+__device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&acc)[FI][FJ], const Tile& t, int wrow,
                                           int wcol, int lane) {
   const int half = lane >> 5, l32 = lane & 31;
 #pragma unroll
@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&ac
     if (row < 0) continue;
     float* crow = static_cast<float*>(g.C) + (DW ? (int64_t)t.e * g.c_expert : 0) + (int64_t)row * g.ldc;
 #pragma unroll
-    for (int fj = 0; fj < 4; ++fj) {
+    for (int fj = 0; fj < FJ; ++fj) {
 #pragma unroll
       for (int gg = 0; gg < 4; ++gg) {
         const int n = t.n0 + wcol + 32 * fj + 8 * gg + 4 * half;
@@ -144,34 +144,35 @@ __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&ac
     }
   }
 }
-// dW through LDS: 64 rows x 256 columns a time (one fragment row of every
-// wave) in one of two 64 KiB buffers, granule c of row m at c ^ (m & 31), so
-// every store instruction writes one whole row of 1 KiB.
-template <int FI>
-__device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc)[FI][4], char* ct, const Tile& t,
+// dW through LDS: 64 rows x BN columns a time (one fragment row of every wave)
+// in one of two buffers, granule c of row m at c ^ (m & 31), so every store
+// instruction writes whole rows.
+template <int FI, int FJ>
+__device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc)[FI][FJ], char* ct, const Tile& t,
                                          int w, int lane) {
-  const int half = lane >> 5, l32 = lane & 31, wcol = 128 * (w & 1);
+  constexpr int BN = 64 * FJ, GPR = BN / 4, RPI = 64 / GPR;
+  const int half = lane >> 5, l32 = lane & 31, wcol = 32 * FJ * (w & 1);
   float* const c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
-  const int n = t.n0 + 4 * lane;
+  const int n = t.n0 + 4 * (lane % GPR);
   __syncthreads();
 #pragma unroll
   for (int fi = 0; fi < FI; ++fi) {
-    char* buf = ct + (fi & 1) * 65536;
+    char* buf = ct + (fi & 1) * (64 * BN * 4);
     const int mw = 32 * (w >> 1) + l32;
 #pragma unroll
-    for (int fj = 0; fj < 4; ++fj)
+    for (int fj = 0; fj < FJ; ++fj)
 #pragma unroll
       for (int gg = 0; gg < 4; ++gg) {
         const f32x4 v = {acc[fi][fj][4 * gg], acc[fi][fj][4 * gg + 1], acc[fi][fj][4 * gg + 2],
                          acc[fi][fj][4 * gg + 3]};
-        *reinterpret_cast<f32x4*>(buf + mw * 1024 + 16 * (((wcol >> 2) + 8 * fj + 2 * gg + half) ^ (mw & 31))) = v;
+        *reinterpret_cast<f32x4*>(buf + mw * (BN * 4) + 16 * (((wcol >> 2) + 8 * fj + 2 * gg + half) ^ (mw & 31))) = v;
       }
     __syncthreads();
 #pragma unroll 4
-    for (int it = 0; it < 16; ++it) {
-      const int mr = 16 * w + it;
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int mr = 16 * w + RPI * it + lane / GPR;
       const int m = 32 * FI * (mr >> 5) + 32 * fi + (mr & 31);
-      f32x4 v = *reinterpret_cast<const f32x4*>(buf + mr * 1024 + 16 * (lane ^ (mr & 31)));
+      f32x4 v = *reinterpret_cast<const f32x4*>(buf + mr * (BN * 4) + 16 * ((lane % GPR) ^ (mr & 31)));
       if (m < t.mrows && n < g.N) {
         f32x4* dst = reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n);
         if (g.accumulate) v += *dst;
@@ -182,20 +183,21 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc
 }
 
 // dW of a group without rows: zeros (kept when accumulating).
-template <int BM>
+template <int BN>
 __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
   if (g.accumulate) return;
+  constexpr int GPR = BN / 4;
   float* c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
-  const int n = t.n0 + 4 * (threadIdx.x & 63);
+  const int n = t.n0 + 4 * (threadIdx.x % GPR);
   if (n >= g.N) return;
-  for (int m = threadIdx.x >> 6; m < t.mrows; m += 4)
+  for (int m = threadIdx.x / GPR; m < t.mrows; m += 256 / GPR)
     *reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n) = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// fp32 tile kernel.  A workgroup of four waves (2 x 2) makes a 64 FI x 256
-// tile, each wave 32 FI x 128 in accumulators.  Steps of 32 of the reduction
+// fp32 tile kernel.  A workgroup of four waves (2 x 2) makes a 64 FI x 64 NJ
+// tile, each wave 32 FI x 32 NJ in accumulators.  Steps of 32 of the reduction
 // are copied straight from global memory into LDS, double buffered: step t + 1
 // is in flight while step t is computed.  fp32 matrix instructions run at a
 // sixteenth of the bf16 rate, so a step's 16384 cycles (FI = 4) hide its copies
@@ -203,23 +205,23 @@ __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
 //   DW = false: C[rc(s)][n] over the rows of one group (rows form)
 //   DW = true:  C_e[m][n] = sum over the group's rows (both operands NC)
 // ---------------------------------------------------------------------------
-template <int AL, int BL, int FI, bool DW>
+template <int AL, int BL, int FI, int NJ, bool DW>
 __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
-  constexpr int FJ = 4, BM = 64 * FI, BN = 256, KD = 32;
+  constexpr int BM = 64 * FI, BN = 64 * NJ, KD = 32;
   constexpr int UA = BM * 128, UB = BN * 128;          // bytes of a step's units
   constexpr int CA = UA / 4096, CB = UB / 4096;        // 1 KiB copies per wave
   __shared__ u32x4 ring[2 * (UA + UB) / 16];
 
-  const Tile tl = find_tile<BM, DW>(g);
+  const Tile tl = find_tile<BM, BN, DW>(g);
   if (tl.mrows <= 0) return;
   const int e = tl.e, row0 = tl.row0, mrows = tl.mrows, m0 = tl.m0, n0 = tl.n0, klen = tl.klen;
   const int nsteps = (klen + KD - 1) / KD;
-  if (DW && nsteps == 0) return store_zero<BM>(g, tl);
+  if (DW && nsteps == 0) return store_zero<BN>(g, tl);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
-  const int wrow = 32 * FI * (w >> 1), wcol = 128 * (w & 1);
+  const int wrow = 32 * FI * (w >> 1), wcol = 32 * NJ * (w & 1);
   const uint8_t* const Be = DW ? g.B : g.B + (int64_t)e * g.b_expert;
   const uint8_t* const zero = reinterpret_cast<const uint8_t*>(g_expert_zero);
 
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
     constexpr int RW = decltype(rw_tag)::value, CPR = RW / 4, RPC = 64 / CPR, NCP = RW / 32;
 #pragma unroll
     for (int i = 0; i < NCP; ++i) {
-      const int kr = RPC * (NCP * w + i) + lane / CPR;
+      const int kr = RPC * (NCP * w + i) + lane / CPR;   // (CPR < 64: several rows a copy)
       const int col = min(c0 + 4 * ((lane % CPR) ^ nx32(kr)), cmax - 4);
       const int k = t * KD + kr;
       const uint8_t* src = zero;
@@ -274,11 +276,11 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
     }
   };
 
-  f32x16 acc[FI][FJ];
+  f32x16 acc[FI][NJ];
 #pragma unroll
   for (int a = 0; a < FI; ++a)
 #pragma unroll
-    for (int b = 0; b < FJ; ++b)
+    for (int b = 0; b < NJ; ++b)
 #pragma unroll
       for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
 
@@ -308,19 +310,19 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
     const uint32_t ua = (uint32_t)(t & 1) * (UA + UB), ub = ua + UA;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      u32x4 fa[FI], fb[FJ];
+      u32x4 fa[FI], fb[NJ];
 #pragma unroll
       for (int f = 0; f < FI; ++f)
         fa[f] = frag(std::integral_constant<bool, AL == KC>(), std::integral_constant<int, BM>(), ua, wrow + 32 * f, ks);
 #pragma unroll
-      for (int f = 0; f < FJ; ++f)
+      for (int f = 0; f < NJ; ++f)
         fb[f] = frag(std::integral_constant<bool, BL == KC>(), std::integral_constant<int, BN>(), ub, wcol + 32 * f, ks);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
         for (int fi = 0; fi < FI; ++fi)
 #pragma unroll
-          for (int fj = 0; fj < FJ; ++fj)
+          for (int fj = 0; fj < NJ; ++fj)
             acc[fi][fj] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(fb[fj][x]), __uint_as_float(fa[fi][x]),
                                                                acc[fi][fj], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
     // this wave's reads are done before the next barrier lets others overwrite
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-  store_f32<FI, DW>(g, acc, tl, wrow, wcol, lane);
+  store_f32<FI, NJ, DW>(g, acc, tl, wrow, wcol, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -383,11 +385,11 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     return Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
   };
   Tile tl;
-  if constexpr (DW) tl = find_tile<BM, DW>(kernel_args());
+  if constexpr (DW) tl = find_tile<BM, BN, DW>(kernel_args());
   else tl = rows_tile(blockIdx.x);
   if (tl.mrows <= 0) return;
   const int klen = tl.klen, nsteps = (klen + KD - 1) / KD;
-  if (DW && nsteps == 0) return store_zero<BM>(kernel_args(), tl);
+  if (DW && nsteps == 0) return store_zero<BN>(kernel_args(), tl);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -468,8 +470,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   };
   // Order entries of this wave's 16 k-rows of a step, by scalar loads (they
   // wait on lgkmcnt, not on the counter that tracks the copies in flight), and
-  // the row that copy i of either operand reads: k-row 16 w + 2 i + lane / 32.
-  static_assert(!GATHER || (AL == NC && BL == NC && FI == 4), "both operands copy two k-rows at a time");
+  // the row that copy i of either operand reads: k-row 16 w + RPC i + lane / CPR.
+  static_assert(!GATHER || (AL == NC && BL == NC && BM == BN), "both operands copy the same k-rows");
   int oidx[GATHER ? 16 : 1];
   const int32_t* const order = GATHER ? kernel_args().order : nullptr;
   const RowMap ma = kernel_args().ma, mb = kernel_args().mb;   // GATHER only
@@ -481,14 +483,16 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     }
   };
   auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t row_bytes, int i, int t) -> const uint8_t* {
-    const int k = tl.row0 + t * KD + 16 * w + 2 * i;
-    auto at = [&](int h) -> int64_t {
-      return (map.by_order ? (int64_t)div_fast(read_row(oidx[(2 * i + h) % (GATHER ? 16 : 1)], nrows), map.div)
-                           : (int64_t)(k + h)) *
-             row_bytes;
-    };
-    const int64_t r0 = at(0), r1 = at(1);
-    return from + (half ? r1 : r0);
+    const int k = tl.row0 + t * KD + 16 * w + RPCA * i;
+    int64_t at = 0;
+#pragma unroll
+    for (int h = 0; h < RPCA; ++h) {
+      const int64_t row = map.by_order
+                              ? (int64_t)div_fast(read_row(oidx[(RPCA * i + h) % (GATHER ? 16 : 1)], nrows), map.div)
+                              : (int64_t)(k + h);
+      at = lane / CPRA == h ? row * row_bytes : at;
+    }
+    return from + at;
   };
   // Copy i of step t's A (B) unit.  CHECK: the step may pass the end of the
   // reduction, and what does reads zeros.
@@ -777,7 +781,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   prologue();
   if constexpr (DW) {
     main_loop();
-    store_dw<FI>(kernel_args(), acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
+    store_dw<FIW, FJW>(kernel_args(), acc, reinterpret_cast<char*>(&ring[0]), tl, w, lane);
   } else {
     // The grid is one workgroup per CU: each takes every gridDim.x-th tile and
     // starts the next one's copies before it stores this one's rows.
@@ -855,55 +859,174 @@ void rows_pipe(const ExpertArgs& a, hipStream_t s) {
   const int64_t most = rows_grid(a, 64 * FI, 64 * NJ), grid = most < kCus ? most : kCus;
   hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, NJ, false, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
 }
-template <int AL, int BL>
-void rows_size(const ExpertArgs& a, hipStream_t s) {
-  const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96) rows_pipe<AL, BL, 1, 4>(a, s);
-  else if (mean <= 384) rows_pipe<AL, BL, 2, 4>(a, s);
-  else rows_pipe<AL, BL, 4, 4>(a, s);
+template <int BL, int FI, int NJ>
+void rows_f32_tile(const ExpertArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_expert_f32<KC, BL, FI, NJ, false>), dim3((unsigned)rows_grid(a, 64 * FI, 64 * NJ)), dim3(256),
+                     0, s, a);
 }
-template <int BL>
-void rows_f32(const ExpertArgs& a, hipStream_t s) {
-  const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 96)
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 1, false>), dim3((unsigned)rows_grid(a, 64, 256)), dim3(256), 0, s, a);
-  else if (mean <= 384)
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 2, false>), dim3((unsigned)rows_grid(a, 128, 256)), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_expert_f32<KC, BL, 4, false>), dim3((unsigned)rows_grid(a, 256, 256)), dim3(256), 0, s, a);
+}  // namespace
+
+namespace {
+
+// Which kernel and tile a product takes.  Its time is predicted for each as
+//   start + K max(lone * ceil(rounds), busy * rounds),   at least the weights' bytes at `rate`
+// with rounds = tiles / 256 CUs: `lone` is a tile's time per element of the
+// reduction while it has its CU and the caches to itself, `busy` the same when
+// the chip is full (clocks drop and the L2s are shared).  The groups' sizes
+// are not known here, so row tiles are estimated from the mean group: one
+// partial tile per group more than the rows fill, half full on average.
+// Measured with groups of equal size (microseconds, K = N = 4096 unless
+// said): bf16 weights [d_out][d_in], one expert: 8 rows 10 with the few-row
+// kernel, 24 with 64x128 tiles, 78 with 256x256; 160 rows 57 (few-row), 25
+// (64x128), 80 (256x256); 2048 rows 104 (64x128), 64 (256x128), 89 (256x256);
+// eight experts of 2048 rows 969, 538 and 462.  fp32, one expert: 48 rows 37
+// (few-row, 64 rows a tile), 97 (64x64); 512 rows 285 and 160; 2048 rows 618
+// (64x64), 527 (128x256).
+struct Choice {
+  int rows, cols;               // tile
+  double start, lone, busy;     // us, us per element of the reduction
+  double rate;                  // bytes of weights per us
+};
+constexpr int kFewChoices = 3;  // of each list: the few-row kernel with 1, 2 and 4 row blocks
+constexpr Choice kBf16Nk[] = {{16, 16, 3.0, .0015, .0020, 4.8e6}, {32, 16, 3.0, .0018, .0029, 4.0e6},
+                              {64, 16, 3.0, .0024, .0050, 3.4e6}, {64, 128, 4.5, .0048, .0074, 4.2e6},
+                              {64, 256, 4.9, .0070, .0121, 5.4e6}, {128, 128, 6.0, .0059, .0104, 4.2e6},
+                              {128, 256, 6.9, .0100, .0181, 5.5e6}, {256, 128, 6.8, .0092, .0164, 4.1e6},
+                              {256, 256, 10.0, .0166, .0281, 5.0e6}};
+constexpr Choice kBf16Kn[] = {{16, 64, 3.0, .0027, .0049, 5.0e6}, {32, 64, 3.0, .0030, .0053, 5.1e6},
+                              {64, 64, 3.0, .0037, .0095, 5.0e6}, {64, 128, 5.0, .0048, .0076, 4.8e6},
+                              {64, 256, 5.5, .0073, .0121, 5.2e6}, {128, 128, 6.0, .0063, .0106, 4.8e6},
+                              {128, 256, 7.0, .0104, .0186, 5.2e6}, {256, 128, 6.8, .0095, .0162, 4.2e6},
+                              {256, 256, 10.0, .0175, .0286, 4.6e6}};
+constexpr Choice kF32Nk[] = {{16, 16, 3.0, .0040, .0034, 4.2e6}, {32, 16, 3.0, .0049, .0052, 4.0e6},
+                             {64, 16, 3.0, .0076, .0087, 3.0e6}, {64, 64, 3.5, .0231, .0185, 4.0e6},
+                             {64, 128, 3.7, .0389, .0353, 4.0e6}, {64, 256, 4.0, .0686, .0708, 4.0e6},
+                             {128, 128, 3.8, .0675, .0647, 4.0e6}, {128, 256, 4.1, .1247, .1285, 4.0e6},
+                             {256, 256, 5.0, .2350, .2500, 4.0e6}};
+constexpr Choice kF32Kn[] = {{16, 64, 3.0, .0080, .0094, 5.2e6}, {32, 64, 3.0, .0118, .0111, 5.0e6},
+                             {64, 64, 3.0, .0190, .0206, 3.0e6}, {64, 64, 3.5, .0231, .0185, 4.5e6},
+                             {64, 128, 3.7, .0389, .0353, 4.5e6}, {64, 256, 4.0, .0686, .0708, 4.5e6},
+                             {128, 128, 3.8, .0675, .0647, 4.5e6}, {128, 256, 4.1, .1247, .1285, 4.5e6},
+                             {256, 256, 5.0, .2350, .2500, 4.5e6}};
+constexpr Choice kW4A16[] = {{16, 16, 3.5, .0010, .0013, 2.1e6}, {32, 16, 3.5, .0012, .0022, 1.8e6},
+                             {64, 16, 3.5, .0017, .0042, 1.3e6}, {64, 128, 4.8, .0046, .0081, 2.3e6},
+                             {64, 256, 5.8, .0062, .0115, 3.1e6}, {128, 128, 5.2, .0069, .0100, 2.2e6},
+                             {128, 256, 7.1, .0101, .0155, 2.6e6}, {256, 128, 6.9, .0098, .0160, 1.5e6},
+                             {256, 256, 10.1, .0170, .0270, 1.8e6}};
+constexpr Choice kW4A4[] = {{16, 16, 3.2, .0006, .0009, 2.6e6}, {32, 16, 3.2, .0007, .0013, 2.6e6},
+                            {64, 16, 3.2, .0010, .0023, 2.0e6}, {64, 128, 4.1, .0020, .0030, 4.5e6},
+                            {64, 256, 4.2, .0029, .0045, 5.4e6}, {128, 128, 4.2, .0024, .0039, 4.4e6},
+                            {128, 256, 5.4, .0037, .0069, 5.0e6}, {256, 256, 8.0, .0055, .0121, 3.7e6}};
+
+template <int N>
+int choose(const Choice (&list)[N], const ExpertArgs& a, double weight_bytes) {
+  const double experts = a.offsets ? (a.n_experts < a.rows ? a.n_experts : a.rows) : 1;
+  const double mean = a.rows / experts;
+  int best = 0;
+  double best_us = 0;
+  for (int i = 0; i < N; ++i) {
+    const Choice& c = list[i];
+    double tiles = experts == 1 ? (a.rows + c.rows - 1) / c.rows : mean / c.rows + 0.5;
+    if (tiles < 1) tiles = 1;
+    const double rounds = experts * tiles * ((a.N + c.cols - 1) / c.cols) / kCus;
+    const double lone = c.lone * (double)(int64_t)(rounds + 0.999), busy = c.busy * rounds;
+    double us = c.start + a.K * (lone > busy ? lone : busy);
+    const double read = c.start + experts * weight_bytes / c.rate;
+    if (read > us) us = read;
+    if (i == 0 || us < best_us) {
+      best = i;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
+template <int AL, int BL, int N>
+void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weight_bytes, const ExpertArgs& a,
+               hipStream_t s) {
+  const int i = choose(list, a, weight_bytes);
+  if (i < kFewChoices) return launch_expert_few(form, b_kc, list[i].rows / 16, a, s);
+  const int r = list[i].rows, c = list[i].cols;
+  if (r == 64 && c == 128) return rows_pipe<AL, BL, 1, 2>(a, s);
+  if (r == 64) return rows_pipe<AL, BL, 1, 4>(a, s);
+  if (r == 128 && c == 128) return rows_pipe<AL, BL, 2, 2>(a, s);
+  if (r == 128) return rows_pipe<AL, BL, 2, 4>(a, s);
+  if constexpr (AL == KC)
+    if (c == 128) return rows_pipe<AL, BL, 4, 2>(a, s);
+  rows_pipe<AL, BL, 4, 4>(a, s);
+}
+template <int BL, int N>
+void rows_f32(const Choice (&list)[N], bool b_kc, const ExpertArgs& a, hipStream_t s) {
+  const int i = choose(list, a, 4.0 * a.K * a.N);
+  if (i < kFewChoices) return launch_expert_few(ExpertForm::kF32, b_kc, list[i].rows / 16, a, s);
+  const int r = list[i].rows, c = list[i].cols;
+  if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
+  if (r == 64 && c == 128) return rows_f32_tile<BL, 1, 2>(a, s);
+  if (r == 64) return rows_f32_tile<BL, 1, 4>(a, s);
+  if (r == 128 && c == 128) return rows_f32_tile<BL, 2, 2>(a, s);
+  if (r == 128) return rows_f32_tile<BL, 2, 4>(a, s);
+  rows_f32_tile<BL, 4, 4>(a, s);
 }
 
 }  // namespace
 
 void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStream_t s) {
   if (a.rows <= 0) return;
-  const int64_t mean = a.rows / (a.offsets ? a.n_experts : 1);
-  if (mean <= 32) return launch_expert_few(form, b_kc, mean <= 16 ? 1 : 2, a, s);
+  const double elems = (double)a.K * a.N;
   switch (form) {
     case ExpertForm::kBf16:
-      if (b_kc) rows_size<KC, KC>(a, s);
-      else rows_size<KC, NC>(a, s);
+      if (b_kc) rows_bf16<KC, KC>(form, true, kBf16Nk, 2 * elems, a, s);
+      else rows_bf16<KC, NC>(form, false, kBf16Kn, 2 * elems, a, s);
       break;
     case ExpertForm::kF32:
-      if (b_kc) rows_f32<KC>(a, s);
-      else rows_f32<NC>(a, s);
+      if (b_kc) rows_f32<KC>(kF32Nk, true, a, s);
+      else rows_f32<NC>(kF32Kn, false, a, s);
       break;
-    case ExpertForm::kW4A16: rows_size<KC, F4>(a, s); break;
+    case ExpertForm::kW4A16: rows_bf16<KC, F4>(form, true, kW4A16, elems * 17 / 32, a, s); break;
     case ExpertForm::kW4A4:
-      if (a.K % 512 == 0) rows_size<X4, X4>(a, s);
-      else rows_size<X4D, X4D>(a, s);
+      if (a.K % 512 == 0) rows_bf16<X4, X4>(form, true, kW4A4, elems * 17 / 32, a, s);
+      else rows_bf16<X4D, X4D>(form, true, kW4A4, elems * 17 / 32, a, s);
       break;
   }
 }
 
+namespace {
+
+template <int BM>
+int64_t dw_grid(const ExpertArgs& a) {
+  const int64_t E = a.offsets ? a.n_experts : 1;
+  return 8 * E * (((int64_t)((a.M + BM - 1) / BM) * ((a.N + BM - 1) / BM) + 7) / 8);
+}
+template <int FI>
+void dw_pipe(const ExpertArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)dw_grid<64 * FI>(a));
+  if (a.ma.by_order || a.mb.by_order)
+    hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, false>), grid, dim3(256), 0, s, a);
+}
+template <int FI>
+void dw_f32(const ExpertArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_expert_f32<NC, NC, FI, FI, true>), dim3((unsigned)dw_grid<64 * FI>(a)), dim3(256), 0, s, a);
+}
+
+}  // namespace
+
+// dW tiles: 256 x 256, or smaller ones while those leave CUs idle.  Measured
+// (microseconds, experts x d_in x d_out, 100 rows each): bf16 8 x 512 x 1024
+// (64 tiles of 256 x 256) 17.0 against 9.6 with 128 x 128, 32 x 512 x 1024 (256
+// tiles) 22.6 against 34.0; fp32 8 x 512 x 1024 45 (256), 18.1 (128), 17.6 (64),
+// with 1000 rows each 266, 90 and 94; 32 x 512 x 1024 51, 52 and 55.
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
-  const int64_t grid = 8 * E * (((a.M + 255) / 256 * ((a.N + 255) / 256) + 7) / 8);
-  const dim3 dg((unsigned)grid);
-  if (f32) hipLaunchKernelGGL((k_expert_f32<NC, NC, 4, true>), dg, dim3(256), 0, s, a);
-  else if (a.ma.by_order || a.mb.by_order)
-    hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, 4, true, true>), dg, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, 4, 4, true, false>), dg, dim3(256), 0, s, a);
+  const int64_t tiles = E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (f32) {
+    if (tiles >= 192) dw_f32<4>(a, s);
+    else if (tiles >= 48 && a.rows / E >= 400) dw_f32<2>(a, s);
+    else dw_f32<1>(a, s);
+  } else {
+    if (tiles >= 160) dw_pipe<4>(a, s);
+    else dw_pipe<2>(a, s);
+  }
 }
 
 }  // namespace mlora
