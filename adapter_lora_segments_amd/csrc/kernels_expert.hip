@@ -945,7 +945,7 @@ template <int AL, int BL, int N>
 void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weight_bytes, const ExpertArgs& a,
                hipStream_t s) {
   const int i = choose(list, a, weight_bytes);
-  if (i < kFewChoices) return launch_expert_few(form, b_kc, list[i].rows / 16, a, s);
+  if (i < kFewChoices) return launch_expert_few(form, b_kc, list[i].rows, list[i].cols, a, s);
   const int r = list[i].rows, c = list[i].cols;
   if (r == 64 && c == 128) return rows_pipe<AL, BL, 1, 2>(a, s);
   if (r == 64) return rows_pipe<AL, BL, 1, 4>(a, s);
@@ -958,7 +958,7 @@ void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weigh
 template <int BL, int N>
 void rows_f32(const Choice (&list)[N], bool b_kc, const ExpertArgs& a, hipStream_t s) {
   const int i = choose(list, a, 4.0 * a.K * a.N);
-  if (i < kFewChoices) return launch_expert_few(ExpertForm::kF32, b_kc, list[i].rows / 16, a, s);
+  if (i < kFewChoices) return launch_expert_few(ExpertForm::kF32, b_kc, list[i].rows, list[i].cols, a, s);
   const int r = list[i].rows, c = list[i].cols;
   if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
   if (r == 64 && c == 128) return rows_f32_tile<BL, 1, 2>(a, s);
