@@ -86,9 +86,8 @@ enum class ExpertForm { kBf16, kF32, kW4A16, kW4A4 };
 // rows form; b_kc: B_e(k, n) at B[n * ldb + k], else at B[k * ldb + n]
 // (MXFP4 weights are always k-contiguous).
 void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStream_t s);
-// The same for few rows per group: tiles of `rows` rows (16, 32 or 64) and
-// `cols` columns (64 where the weights are n-contiguous; else 16, 32, or with
-// up to 32 rows 64).
+// The same for few rows per group, in one of the tiles of rows x cols that
+// kernels_expert.hip chooses from.
 void launch_expert_few(ExpertForm form, bool b_kc, int rows, int cols, const ExpertArgs& a, hipStream_t s);
 // dW form, bf16 or fp32 operands, both n-contiguous.
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s);

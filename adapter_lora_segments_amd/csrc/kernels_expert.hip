@@ -869,84 +869,97 @@ void rows_f32_tile(const ExpertArgs& a, hipStream_t s) {
 namespace {
 
 // Which kernel and tile a product takes.  Its time is predicted for each as
-//   start + K max(lone * ceil(rounds), busy * rounds),   at least the weights' bytes at `rate`
-// with rounds = tiles / 256 CUs: `lone` is a tile's time per element of the
-// reduction while it has its CU and the caches to itself, `busy` the same when
-// the chip is full (clocks drop and the L2s are shared).  The groups' sizes
-// are not known here, so row tiles are estimated from the mean group: one
-// partial tile per group more than the rows fill, half full on average.
-// Measured with groups of equal size (microseconds, K = N = 4096 unless
-// said): bf16 weights [d_out][d_in], one expert: 8 rows 10 with the few-row
-// kernel, 24 with 64x128 tiles, 78 with 256x256; 160 rows 57 (few-row), 25
-// (64x128), 80 (256x256); 2048 rows 104 (64x128), 64 (256x128), 89 (256x256);
-// eight experts of 2048 rows 969, 538 and 462.  fp32, one expert: 48 rows 37
-// (few-row, 64 rows a tile), 97 (64x64); 512 rows 285 and 160; 2048 rows 618
-// (64x64), 527 (128x256).
+//   start + K max(lone * ceil(rounds), busy * rounds),  at least the time that
+// reading the weights takes, with rounds = tiles / 256 CUs: `lone` is a tile's
+// time per element of the reduction while it has its CU and the caches to
+// itself, `busy` the same when the chip is full (clocks drop, the L2s are
+// shared).  The few-row kernel has several workgroups on a CU: no ceil.  The
+// groups' sizes are not known here: the number of groups with rows is that of
+// rows thrown at the groups evenly, and a group has half a partial tile.
+// Measured with groups of equal size (us; K = 4096): bf16 weights
+// [d_out][d_in], N = 4096: one expert of 4 rows 9.2 with 16x16 few-row tiles,
+// 24 with 64x128 and 78 with 256x256 tiles; of 160 rows 57, 25 and 80; of 2048
+// rows 104 (64x128), 64 (256x128), 89 (256x256); eight of 2048 rows 969, 538,
+// 462.  MXFP4 weights, bf16 activations, N = 14336: 4 rows 17.1 (16x16), 13.8
+// (16x32), 12.4 (16x64), 27 (64x128); eight experts of 32 rows 152 (16x64), 88
+// (64x256).  fp32, N = 4096: 48 rows 37 (64x16 few-row), 97 (64x64); 512 rows
+// 285 and 160; 2048 rows 618 (64x64), 527 (128x256).
 struct Choice {
+  bool few;
   int rows, cols;               // tile
   double start, lone, busy;     // us, us per element of the reduction
   double rate;                  // bytes of weights per us
 };
-constexpr int kFewChoices = 3;  // of each list: the few-row kernel with 1, 2 and 4 row blocks
-constexpr Choice kBf16Nk[] = {{16, 16, 3.0, .0015, .0020, 4.8e6}, {32, 16, 3.0, .0018, .0029, 4.0e6},
-                              {64, 16, 3.0, .0024, .0050, 3.4e6}, {64, 128, 4.5, .0048, .0074, 4.2e6},
-                              {64, 256, 4.9, .0070, .0121, 5.4e6}, {128, 128, 6.0, .0059, .0104, 4.2e6},
-                              {128, 256, 6.9, .0100, .0181, 5.5e6}, {256, 128, 6.8, .0092, .0164, 4.1e6},
-                              {256, 256, 10.0, .0166, .0281, 5.0e6}};
-constexpr Choice kBf16Kn[] = {{16, 64, 3.0, .0027, .0049, 5.0e6}, {32, 64, 3.0, .0030, .0053, 5.1e6},
-                              {64, 64, 3.0, .0037, .0095, 5.0e6}, {64, 128, 5.0, .0048, .0076, 4.8e6},
-                              {64, 256, 5.5, .0073, .0121, 5.2e6}, {128, 128, 6.0, .0063, .0106, 4.8e6},
-                              {128, 256, 7.0, .0104, .0186, 5.2e6}, {256, 128, 6.8, .0095, .0162, 4.2e6},
-                              {256, 256, 10.0, .0175, .0286, 4.6e6}};
-constexpr Choice kF32Nk[] = {{16, 16, 3.0, .0040, .0034, 4.2e6}, {32, 16, 3.0, .0049, .0052, 4.0e6},
-                             {64, 16, 3.0, .0076, .0087, 3.0e6}, {64, 64, 3.5, .0231, .0185, 4.0e6},
-                             {64, 128, 3.7, .0389, .0353, 4.0e6}, {64, 256, 4.0, .0686, .0708, 4.0e6},
-                             {128, 128, 3.8, .0675, .0647, 4.0e6}, {128, 256, 4.1, .1247, .1285, 4.0e6},
-                             {256, 256, 5.0, .2350, .2500, 4.0e6}};
-constexpr Choice kF32Kn[] = {{16, 64, 3.0, .0080, .0094, 5.2e6}, {32, 64, 3.0, .0118, .0111, 5.0e6},
-                             {64, 64, 3.0, .0190, .0206, 3.0e6}, {64, 64, 3.5, .0231, .0185, 4.5e6},
-                             {64, 128, 3.7, .0389, .0353, 4.5e6}, {64, 256, 4.0, .0686, .0708, 4.5e6},
-                             {128, 128, 3.8, .0675, .0647, 4.5e6}, {128, 256, 4.1, .1247, .1285, 4.5e6},
-                             {256, 256, 5.0, .2350, .2500, 4.5e6}};
-constexpr Choice kW4A16[] = {{16, 16, 3.5, .0010, .0013, 2.1e6}, {32, 16, 3.5, .0012, .0022, 1.8e6},
-                             {64, 16, 3.5, .0017, .0042, 1.3e6}, {64, 128, 4.8, .0046, .0081, 2.3e6},
-                             {64, 256, 5.8, .0062, .0115, 3.1e6}, {128, 128, 5.2, .0069, .0100, 2.2e6},
-                             {128, 256, 7.1, .0101, .0155, 2.6e6}, {256, 128, 6.9, .0098, .0160, 1.5e6},
-                             {256, 256, 10.1, .0170, .0270, 1.8e6}};
-constexpr Choice kW4A4[] = {{16, 16, 3.2, .0006, .0009, 2.6e6}, {32, 16, 3.2, .0007, .0013, 2.6e6},
-                            {64, 16, 3.2, .0010, .0023, 2.0e6}, {64, 128, 4.1, .0020, .0030, 4.5e6},
-                            {64, 256, 4.2, .0029, .0045, 5.4e6}, {128, 128, 4.2, .0024, .0039, 4.4e6},
-                            {128, 256, 5.4, .0037, .0069, 5.0e6}, {256, 256, 8.0, .0055, .0121, 3.7e6}};
+constexpr Choice kBf16Nk[] = {{true, 16, 16, 3.0, .0015, .0016, 5.2e6},   {true, 16, 32, 3.0, .0024, .0029, 5.0e6},
+                              {true, 32, 16, 3.0, .0028, .0026, 4.3e6},   {true, 32, 32, 3.0, .0036, .0042, 4.6e6},
+                              {true, 32, 64, 3.0, .0054, .0076, 4.6e6},   {true, 64, 32, 3.0, .0055, .0061, 3.8e6},
+                              {false, 64, 128, 4.5, .0048, .0074, 4.2e6}, {false, 64, 256, 4.9, .0070, .0121, 5.4e6},
+                              {false, 128, 128, 6.0, .0059, .0104, 4.2e6}, {false, 128, 256, 6.9, .0100, .0181, 5.5e6},
+                              {false, 256, 128, 6.8, .0092, .0164, 4.1e6}, {false, 256, 256, 10.0, .0166, .0281, 5.0e6}};
+constexpr Choice kBf16Kn[] = {{true, 16, 64, 3.0, .0027, .0049, 5.0e6},   {true, 32, 64, 3.0, .0030, .0053, 5.1e6},
+                              {true, 64, 64, 3.0, .0037, .0095, 5.0e6},   {false, 64, 128, 5.0, .0048, .0076, 4.8e6},
+                              {false, 64, 256, 5.5, .0073, .0121, 5.2e6}, {false, 128, 128, 6.0, .0063, .0106, 4.8e6},
+                              {false, 128, 256, 7.0, .0104, .0186, 5.2e6}, {false, 256, 128, 6.8, .0095, .0162, 4.2e6},
+                              {false, 256, 256, 10.0, .0175, .0286, 4.6e6}};
+constexpr Choice kF32Nk[] = {{true, 16, 16, 3.0, .0040, .0048, 4.7e6},   {true, 16, 32, 3.0, .0052, .0078, 5.2e6},
+                             {true, 32, 16, 3.0, .0058, .0063, 4.3e6},   {true, 32, 32, 3.0, .0080, .0098, 4.8e6},
+                             {true, 64, 32, 3.0, .0130, .0134, 3.2e6},   {false, 64, 64, 3.5, .0231, .0185, 4.0e6},
+                             {false, 64, 128, 3.7, .0389, .0353, 4.0e6}, {false, 64, 256, 4.0, .0686, .0708, 4.0e6},
+                             {false, 128, 128, 3.8, .0675, .0647, 4.0e6}, {false, 128, 256, 4.1, .1247, .1285, 4.0e6},
+                             {false, 256, 256, 5.0, .2350, .2500, 4.0e6}};
+constexpr Choice kF32Kn[] = {{true, 16, 64, 3.0, .0080, .0094, 5.2e6},   {true, 32, 64, 3.0, .0118, .0111, 5.0e6},
+                             {true, 64, 64, 3.0, .0190, .0206, 3.0e6},   {false, 64, 64, 3.5, .0231, .0185, 4.5e6},
+                             {false, 64, 128, 3.7, .0389, .0353, 4.5e6}, {false, 64, 256, 4.0, .0686, .0708, 4.5e6},
+                             {false, 128, 128, 3.8, .0675, .0647, 4.5e6}, {false, 128, 256, 4.1, .1247, .1285, 4.5e6},
+                             {false, 256, 256, 5.0, .2350, .2500, 4.5e6}};
+constexpr Choice kW4A16[] = {{true, 16, 16, 3.2, .0011, .0013, 2.6e6},   {true, 16, 32, 3.2, .0016, .0018, 3.3e6},
+                             {true, 16, 64, 3.2, .0024, .0029, 3.7e6},   {true, 32, 32, 3.2, .0026, .0029, 2.8e6},
+                             {true, 32, 64, 3.2, .0036, .0044, 2.9e6},   {false, 64, 128, 4.8, .0046, .0081, 2.3e6},
+                             {false, 64, 256, 5.8, .0062, .0115, 3.1e6}, {false, 128, 128, 5.2, .0069, .0100, 2.2e6},
+                             {false, 128, 256, 7.1, .0101, .0155, 2.6e6}, {false, 256, 128, 6.9, .0098, .0160, 1.5e6},
+                             {false, 256, 256, 10.1, .0170, .0270, 1.8e6}};
+constexpr Choice kW4A4[] = {{true, 16, 16, 3.2, .0007, .0010, 2.9e6},   {true, 16, 32, 3.2, .0011, .0013, 3.8e6},
+                            {true, 16, 64, 3.2, .0021, .0025, 3.4e6},   {true, 32, 32, 3.2, .0017, .0019, 3.4e6},
+                            {true, 32, 64, 3.2, .0026, .0033, 3.2e6},   {false, 64, 128, 4.1, .0020, .0030, 4.6e6},
+                            {false, 64, 256, 4.2, .0029, .0045, 5.6e6}, {false, 128, 128, 4.2, .0024, .0039, 4.4e6},
+                            {false, 128, 256, 5.4, .0037, .0069, 5.0e6}, {false, 256, 256, 8.0, .0055, .0121, 3.7e6}};
 
 template <int N>
-int choose(const Choice (&list)[N], const ExpertArgs& a, double weight_bytes) {
-  const double experts = a.offsets ? (a.n_experts < a.rows ? a.n_experts : a.rows) : 1;
-  const double mean = a.rows / experts;
+const Choice& choose(const Choice (&list)[N], const ExpertArgs& a, double weight_bytes) {
+  double groups = 1;
+  if (a.offsets && a.n_experts > 1) {
+    double empty = 1;           // chance that a group gets none of the rows
+    for (double p = 1.0 - 1.0 / a.n_experts, n = a.rows; n >= 1 && empty > 1e-3; n -= 1) empty *= p;
+    groups = a.n_experts * (1 - empty);
+  }
+  const double mean = a.rows / groups;
   int best = 0;
   double best_us = 0;
   for (int i = 0; i < N; ++i) {
     const Choice& c = list[i];
-    double tiles = experts == 1 ? (a.rows + c.rows - 1) / c.rows : mean / c.rows + 0.5;
+    double tiles = groups == 1 ? (a.rows + c.rows - 1) / c.rows : mean / c.rows + 0.5;
     if (tiles < 1) tiles = 1;
-    const double rounds = experts * tiles * ((a.N + c.cols - 1) / c.cols) / kCus;
-    const double lone = c.lone * (double)(int64_t)(rounds + 0.999), busy = c.busy * rounds;
+    const double rounds = groups * tiles * ((a.N + c.cols - 1) / c.cols) / kCus;
+    const double lone = c.few ? c.lone : c.lone * (double)(int64_t)(rounds + 0.999), busy = c.busy * rounds;
     double us = c.start + a.K * (lone > busy ? lone : busy);
-    const double read = c.start + experts * weight_bytes / c.rate;
+    // fewer workgroups than CUs do not reach the full rate
+    const double fill = 0.5 + 0.75 * rounds;
+    const double read = c.start + groups * weight_bytes / (c.rate * (fill < 1 ? fill : 1));
     if (read > us) us = read;
     if (i == 0 || us < best_us) {
       best = i;
       best_us = us;
     }
   }
-  return best;
+  return list[best];
 }
 
 template <int AL, int BL, int N>
 void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weight_bytes, const ExpertArgs& a,
                hipStream_t s) {
-  const int i = choose(list, a, weight_bytes);
-  if (i < kFewChoices) return launch_expert_few(form, b_kc, list[i].rows, list[i].cols, a, s);
-  const int r = list[i].rows, c = list[i].cols;
+  const Choice& t = choose(list, a, weight_bytes);
+  const int r = t.rows, c = t.cols;
+  if (t.few) return launch_expert_few(form, b_kc, r, c, a, s);
   if (r == 64 && c == 128) return rows_pipe<AL, BL, 1, 2>(a, s);
   if (r == 64) return rows_pipe<AL, BL, 1, 4>(a, s);
   if (r == 128 && c == 128) return rows_pipe<AL, BL, 2, 2>(a, s);
@@ -957,9 +970,9 @@ void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weigh
 }
 template <int BL, int N>
 void rows_f32(const Choice (&list)[N], bool b_kc, const ExpertArgs& a, hipStream_t s) {
-  const int i = choose(list, a, 4.0 * a.K * a.N);
-  if (i < kFewChoices) return launch_expert_few(ExpertForm::kF32, b_kc, list[i].rows, list[i].cols, a, s);
-  const int r = list[i].rows, c = list[i].cols;
+  const Choice& t = choose(list, a, 4.0 * a.K * a.N);
+  const int r = t.rows, c = t.cols;
+  if (t.few) return launch_expert_few(ExpertForm::kF32, b_kc, r, c, a, s);
   if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
   if (r == 64 && c == 128) return rows_f32_tile<BL, 1, 2>(a, s);
   if (r == 64) return rows_f32_tile<BL, 1, 4>(a, s);

@@ -291,21 +291,24 @@ void few(const ExpertArgs& a, hipStream_t s) {
 }
 template <int FORM>
 void few_of(int rows, int cols, const ExpertArgs& a, hipStream_t s) {
-  if constexpr (FORM == W16_NC || FORM == W32_NC) {
-    if (rows == 16) few<FORM, 1, 1>(a, s);
-    else if (rows == 32) few<FORM, 2, 1>(a, s);
-    else few<FORM, 4, 1>(a, s);
-  } else if (cols == 16) {
-    if (rows == 16) few<FORM, 1, 1>(a, s);
-    else if (rows == 32) few<FORM, 2, 1>(a, s);
-    else few<FORM, 4, 1>(a, s);
-  } else if (cols == 32) {
-    if (rows == 16) few<FORM, 1, 2>(a, s);
-    else if (rows == 32) few<FORM, 2, 2>(a, s);
-    else few<FORM, 4, 2>(a, s);
+  constexpr bool wide = FORM == W16_NC || FORM == W32_NC, f4 = FORM == W4_A16 || FORM == W4_A4;
+  if constexpr (wide) {
+    if (rows == 16) return few<FORM, 1, 1>(a, s);
+    if (rows == 32) return few<FORM, 2, 1>(a, s);
+    few<FORM, 4, 1>(a, s);
   } else {
-    if (rows == 16) few<FORM, 1, 4>(a, s);
-    else few<FORM, 2, 4>(a, s);
+    if (rows == 16 && cols == 16) return few<FORM, 1, 1>(a, s);
+    if (rows == 16 && cols == 32) return few<FORM, 1, 2>(a, s);
+    if (rows == 32 && cols == 32) return few<FORM, 2, 2>(a, s);
+    if constexpr (f4) {
+      if (rows == 16) return few<FORM, 1, 4>(a, s);
+      few<FORM, 2, 4>(a, s);
+    } else {
+      if (rows == 32 && cols == 16) return few<FORM, 2, 1>(a, s);
+      if constexpr (FORM == W16_KC)
+        if (rows == 32) return few<FORM, 2, 4>(a, s);
+      few<FORM, 4, 2>(a, s);
+    }
   }
 }
 
