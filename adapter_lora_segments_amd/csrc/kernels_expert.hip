@@ -367,7 +367,10 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   // Ring: five units (RING5), four units (RING4: the scales take the rest), or
   // NR whole steps; D: steps ahead that a step copies.
   constexpr bool RING5 = UA + UB == 65536 && !S4, RING4 = UA + UB == 65536 && S4;
-  constexpr int SCL = S4 ? 16384 : 0, FIT = (160 * 1024 - SCL) / (UA + UB);
+  constexpr int SCL = !S4 ? 0 : NJ < 4 ? 32768 : 16384, FIT = (160 * 1024 - SCL) / (UA + UB);
+  // Small tiles (few MFMAs a slice) read a whole step's fragments ahead (those
+  // of 64 x 256 with both operands' scales would not fit the registers).
+  constexpr bool SMALL = !DW && NS <= 4 && !(S4 && NJ == 4);
   constexpr int NR = RING5 || RING4 ? 2 : FIT > 6 ? 6 : FIT;
   constexpr int D = RING5 || RING4 ? 2 : NR - 1;
   constexpr int CA = UA / 4096, CB = UB / 4096;          // 1 KiB copies per wave and unit
@@ -463,7 +466,10 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
   const uint32_t lds_a = lds0 + 1024u * (uint32_t)(CA * w), lds_b = lds0 + 1024u * (uint32_t)(CB * w);
-  auto slot = [](int u) -> uint32_t {
+  // (readfirstlane: the compiler may count steps in a vector register, and an
+  // LDS address of a copy has to be scalar)
+  auto slot = [](int v) -> uint32_t {
+    const int u = __builtin_amdgcn_readfirstlane(v);
     if constexpr (RING5) return (uint32_t)(u % 5) * UA;
     else if constexpr (RING4) return (uint32_t)(u & 3) * UA;
     else return (uint32_t)((u >> 1) % NR) * (UA + UB) + ((u & 1) ? UA : 0);
@@ -525,9 +531,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   // X4 scale codes: 8 bytes per row and step.  A copy of dwords touches a row
   // per lane, four times the addresses of a copy of codes, so where a row's 16
   // bytes are aligned (S16: K a multiple of 512) two steps' codes are copied at
-  // once: [chunk & 1][operand][row] of 16 bytes; else [step & 3][dword]
-  // [operand][row] of 4.  (The waits below count neither: they are stricter
-  // by what is in flight.)
+  // once: [chunk][operand][row] of 16 bytes; else [step][dword][operand][row]
+  // of 4.  A ring of NCH chunks (2 NCH steps): a chunk's copy, D + 1 steps
+  // ahead at most, meets the place of one whose reads are over.  (The waits
+  // below count neither: they are stricter by what is in flight.)
+  constexpr int NCH = SCL > 0 ? SCL / 8192 : 1;
+  static_assert(!S4 || (NCH == 2 ? D <= 2 : D <= 4), "the ring of scales covers the steps in flight");
   auto copy_scales = [&](int t, auto check) {
     if constexpr (BL == F4) {
       dma4_at(!check.value || t * KD < klen ? sp + 4 * (t >> 1) : zero,
@@ -536,11 +545,12 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       if constexpr (S16) {
         // even steps: A's codes of the two steps from t on; odd steps: B's of
         // the two after t, so every step has one copy and no branch
-        const int odd = t & 1, c = (t + 1) >> 1;
+        const int odd = __builtin_amdgcn_readfirstlane(t & 1), c = __builtin_amdgcn_readfirstlane((t + 1) >> 1);
         dma16_at(c * 512 < klen ? (odd ? sp : sq) + 16 * c : zero,
-                 lds0 + RING + 8192u * (c & 1) + 4096u * odd + 1024u * (uint32_t)w);
+                 lds0 + RING + 8192u * (c % NCH) + 4096u * odd + 1024u * (uint32_t)w);
       } else {
-        const uint32_t at = lds0 + RING + 4096u * (t & 3) + 256u * (uint32_t)w;
+        const uint32_t at =
+            lds0 + RING + 4096u * (uint32_t)__builtin_amdgcn_readfirstlane(t % (2 * NCH)) + 256u * (uint32_t)w;
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           const bool on = t * KD + 128 * d < klen;
@@ -593,7 +603,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       }
     }
     if constexpr (S4) {
-      const uint32_t at = RING + (S16 ? 8192u * ((s >> 1) & 1) + 8u * (s & 1) : 4096u * (s & 3));
+      const uint32_t at = RING + (S16 ? 8192u * ((s >> 1) % NCH) + 8u * (s & 1) : 4096u * (s % (2 * NCH)));
       bs.sa = at + (S16 ? 16u : 4u) * (uint32_t)(wrow + l32);
       bs.sb = at + (S16 ? 4096u : 1024u) + (S16 ? 16u : 4u) * (uint32_t)(wcol + l32);
       asm volatile("" : "+v"(bs.sa), "+v"(bs.sb));
@@ -729,6 +739,82 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     }
   };
 
+  // SMALL: a step's MFMAs are too few to hide an LDS read, so step s reads all
+  // of step s + 1's fragments (set 1 - P) while its MFMAs take their own (set
+  // P).  At its barrier step s + 1 has landed and every wave holds step s in
+  // registers; the copies of step s + D go to the slot of step s - 1.
+  constexpr int SET = SMALL ? 2 : 1;
+  u32x4 ga[SET][4][FIW], gb[SET][BL == F4 ? 1 : 4][FJW];   // F4: the codes of the step
+  float gc[SET][FJW];
+  int gsa[SET][2][FIW], gsb[SET][2][FJW];
+  auto read_ahead = [&](const Bases& bs, int t, int set, int r) {
+    if constexpr (BL == F4) {
+      if (r < FJW) {
+        read_codes(bs, t, r);
+        gb[set][0][r] = cw[r];
+        gc[set][r] = cs[r];
+      } else if (r < FJW + 4 * FIW) {
+        const int ks = (r - FJW) / FIW, f = (r - FJW) % FIW;
+        ga[set][ks][f] = *(const MLORA_LDS u32x4*)(base + bs.a[ks] + 4096 * f);
+      }
+    } else if (r < 4 * (FIW + FJW)) {
+      const int ks = r / (FIW + FJW), f = r % (FIW + FJW);
+      if (f < FIW) {
+        if constexpr (AK) ga[set][ks][f] = *(const MLORA_LDS u32x4*)(base + bs.a[ks] + 4096 * f);
+        if (S4 && (ks & 1) == 0) gsa[set][ks >> 1][f] = read_scale(bs.sa, ks >> 1, f);
+      } else {
+        const int j = f - FIW;
+        if constexpr (BK) gb[set][ks][j] = *(const MLORA_LDS u32x4*)(base + bs.b[ks] + 4096 * j);
+        else gb[set][ks][j] = read_tr(bs.b[j], CPRB, ks);
+        if (S4 && (ks & 1) == 0) gsb[set][ks >> 1][j] = read_scale(bs.sb, ks >> 1, j);
+      }
+    }
+  };
+  auto small_step = [&](int s, auto par, auto kind) {
+    constexpr int P = decltype(par)::value, KIND = decltype(kind)::value;
+    constexpr bool COPY = KIND < 2;
+    const std::integral_constant<bool, KIND != 0> check{};
+    constexpr int SLOTS = 4 * NS, READS = BL == F4 ? FJW + 4 * FIW : 4 * (FIW + FJW);
+    constexpr int RPQ = (READS + SLOTS - 1) / SLOTS, NC = CA + CB + (BL == F4 || S4 ? 1 : 0);
+    constexpr int CPQ = (NC + SLOTS - 1) / SLOTS;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    wait_vm_barrier<COPY ? (D - 2) * (CA + CBW) : 0>();
+    Bases nxt;
+    step_bases(s + 1, nxt, 0, 3);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      const int ks = q / NS, fi = q % NS / FJW, fj = q % FJW;
+#pragma unroll
+      for (int j = 0; j < RPQ; ++j) read_ahead(nxt, s + 1, 1 - P, RPQ * q + j);
+      if constexpr (S4) {
+        const i32x8 b8 =
+            __builtin_bit_cast(i32x8, __builtin_shufflevector(gb[P][ks][fj], zero4(), 0, 1, 2, 3, 4, 5, 6, 7));
+        const i32x8 a8 =
+            __builtin_bit_cast(i32x8, __builtin_shufflevector(ga[P][ks][fi], zero4(), 0, 1, 2, 3, 4, 5, 6, 7));
+        const int sbv = gsb[P][ks >> 1][fj], sav = gsa[P][ks >> 1][fi];
+        if (ks & 1)
+          acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[fi][fj], 4, 4, 2, sbv, 2, sav);
+        else
+          acc[fi][fj] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b8, a8, acc[fi][fj], 4, 4, 0, sbv, 0, sav);
+      } else if constexpr (BL == F4) {
+        acc[fi][fj] = mfma32(bf16_of_e2m1(gb[P][0][fj][ks], gc[P][fj]), ga[P][ks][fi], acc[fi][fj]);
+      } else {
+        acc[fi][fj] = mfma32(gb[P][ks][fj], ga[P][ks][fi], acc[fi][fj]);
+      }
+      if (COPY) {
+#pragma unroll
+        for (int j = 0; j < CPQ; ++j) {
+          const int c = CPQ * q + j;
+          if (c < CA) copy_a(s + D, c, check);
+          else if (c < CA + CB) copy_b(s + D, c - CA, check);
+          else if (c < NC) copy_scales(s + D, check);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
   // The first D steps of a tile.
   auto prologue = [&]() {
     const std::integral_constant<bool, true> check{};
@@ -752,9 +838,40 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       for (int b = 0; b < FJW; ++b)
 #pragma unroll
         for (int x = 0; x < 16; ++x) acc[a][b][x] = 0.f;
-    // step 0's first slice once every wave's copies of it have landed
+    // step 0's first reads once every wave's copies of it have landed
     wait_vm_barrier<RING4 ? CB : (D - 1) * (CA + CBW)>();
     Bases b0;
+    if constexpr (SMALL) {
+      step_bases(0, b0, 0, 3);
+#pragma unroll
+      for (int r = 0; r < 4 * (FIW + FJW); ++r) read_ahead(b0, 0, 0, r);
+      const std::integral_constant<int, 0> even{};
+      const std::integral_constant<int, 1> odd{};
+      int s = 0;
+      for (; (s + D + 2) * KD <= klen; s += 2) {
+        small_step(s, even, std::integral_constant<int, 0>());
+        small_step(s + 1, odd, std::integral_constant<int, 0>());
+      }
+      for (; s + 1 + D < nsteps; s += 2) {
+        small_step(s, even, std::integral_constant<int, 1>());
+        small_step(s + 1, odd, std::integral_constant<int, 1>());
+      }
+      if (s + D < nsteps) {
+        small_step(s, even, std::integral_constant<int, 1>());
+        ++s;
+        for (; s < nsteps; s += 2) {
+          small_step(s, odd, std::integral_constant<int, 2>());
+          if (s + 1 < nsteps) small_step(s + 1, even, std::integral_constant<int, 2>());
+        }
+      } else {
+        for (; s < nsteps; s += 2) {
+          small_step(s, even, std::integral_constant<int, 2>());
+          if (s + 1 < nsteps) small_step(s + 1, odd, std::integral_constant<int, 2>());
+        }
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      return;
+    }
     step_bases(0, b0, 0, 0);
 #pragma unroll
     for (int f = 0; f < FJW; ++f) read_codes(b0, 0, f);

@@ -264,6 +264,24 @@ def test_mxfp4_forward(sizes, dims, act):
     check(y[owned], want[owned], S[owned], dims[0], "bf16", "Y")
 
 
+@pytest.mark.parametrize("per,experts,do", [(3, 2, 40), (40, 4, 264), (64, 16, 1032), (130, 8, 520), (200, 3, 136),
+                                            (600, 2, 264)])
+@pytest.mark.parametrize("di", [2048, 2176, 3328])
+@pytest.mark.parametrize("form", ["bf16", "w4 bf16", "w4 mxfp4"])
+def test_long_reductions(per, experts, do, di, form):
+    """Reductions of many steps, past every ring's depth, whole and with a
+    partial last step."""
+    say(f"long {per} x {experts} {di} -> {do} {form}")
+    w4 = form.startswith("w4")
+    act = form.split()[-1]
+    c = Case([per, 0, per + 5, per - 2] if experts < 4 else [per + e % 3 for e in range(experts)], di, do, layout="nk",
+             y_order=True, w4=w4)
+    Y = c.layer(**(dict(w_format="mxfp4", act_format=act) if w4 else {})).forward(c.X, c.d_off, c.d_order)
+    X = ox.decode(*ox.quantize(c.Xh)) if act == "mxfp4" else c.Xh
+    want, S, _ = ox.forward(X, c.Wm, c.off, c.order, c.rows, **c.kw)
+    check(Y, want, S, di, "bf16", "Y")
+
+
 @pytest.mark.parametrize("sizes", ["few", "sixty", "big"])
 def test_mxfp4_dx(sizes):
     import torch
