@@ -74,15 +74,18 @@ const char* shape_error(const mlora_expert_shape& s, mlora_status* st) {
 
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
-// Workspace bytes of a forward (quantized activations) and of a backward
-// (the decoded MXFP4 weight).
+// Workspace bytes of a forward (quantized activations) and of a backward's dX
+// (the decoded MXFP4 weight) and dW (partial sums of long groups).
 int64_t forward_ws(const mlora_expert_shape& s) {
   if (s.act_format != MLORA_ACT_MXFP4) return 0;
   const int64_t t = s.x_by_order ? s.rows / s.top_k : s.rows;
   return round16(t * s.d_in / 2) + round16(t * s.d_in / 32);
 }
-int64_t backward_ws(const mlora_expert_shape& s) {
+int64_t dx_ws(const mlora_expert_shape& s) {
   return s.w_format == MLORA_W0_MXFP4 ? 2 * (int64_t)s.n_experts * s.d_in * s.d_out : 0;
+}
+int64_t dw_ws(const mlora_expert_shape& s) {
+  return s.w_format == MLORA_W0_MXFP4 ? 0 : mlora::dw_part_bytes(s.rows, s.n_experts, s.d_in, s.d_out);
 }
 
 mlora_status check_call(const mlora_expert_shape* s, const int32_t* offsets, const int32_t* order, void* ws,
@@ -148,7 +151,8 @@ mlora_status mlora_expert_workspace(const mlora_expert_shape* shape, int64_t* by
   if (!shape || !bytes) return fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
   mlora_status st;
   if (const char* msg = shape_error(*shape, &st)) return fail(st, msg);
-  const int64_t f = forward_ws(*shape), b = backward_ws(*shape);
+  // a weight is quantized (dX only) or has a dW
+  const int64_t f = forward_ws(*shape), b = dx_ws(*shape) + dw_ws(*shape);
   *bytes = f > b ? f : b;
   return MLORA_OK;
 }
@@ -213,7 +217,7 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
   if (const char* msg = shape_error(s, &st)) return fail(st, msg);
   const bool w4 = s.w_format == MLORA_W0_MXFP4;
   const bool want_dx = dX != nullptr && s.rows > 0;
-  st = check_call(shape, offsets, order, workspace, ws_bytes, want_dx ? backward_ws(s) : 0);
+  st = check_call(shape, offsets, order, workspace, ws_bytes, (want_dx ? dx_ws(s) : 0) + (dW ? dw_ws(s) : 0));
   if (st != MLORA_OK) return st;
   if (w4 && dW) return fail(MLORA_ERR_UNSUPPORTED, "expert backward: an MXFP4 weight is frozen, dW must be NULL");
   if ((s.rows > 0 && !dY) || (want_dx && !W) || (dW && s.rows > 0 && !X))
@@ -266,6 +270,8 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
     a.C = dW;
     a.c_expert = wn;
     a.accumulate = s.grad_accumulate;
+    a.chunk = (int32_t)mlora::dw_chunk(s.rows, s.n_experts, s.d_in, s.d_out);
+    a.part = static_cast<float*>(workspace);
     mlora::launch_expert_dw(f32, a, cs);
     st = launched();
     if (st != MLORA_OK) return st;

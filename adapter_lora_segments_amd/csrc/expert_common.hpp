@@ -115,6 +115,84 @@ struct RowTiles {
   }
 };
 
+// The chunks of C rows that the groups' rows are cut into (one at least, so a
+// group without rows gets its zeros), and where a chunk's sums go: straight to
+// the group's dW when it has one chunk, else to a slot of its own.
+struct DwChunk {
+  int e, row0, rows, slot;  // slot -1: the only chunk; rows < 0: past the last chunk
+};
+struct DwChunks {
+  int E, C, total, room;  // room: slots there are, for offsets that are not ordered
+
+  __device__ __forceinline__ void group(const ExpertArgs& a, int c, int& lo, int& hi, int& n, int& sum, int& slots) const {
+    const int lane = threadIdx.x & 63;
+    lo = hi = n = 0;
+    if (c + lane < E) {
+      group_rows(a, c + lane, lo, hi);
+      n = max(1, (hi - lo + C - 1) / C);
+    }
+    sum = n;
+    slots = n > 1 ? n : 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(sum, d), v = __shfl_up(slots, d);
+      if (lane >= d) {
+        sum += u;
+        slots += v;
+      }
+    }
+  }
+  __device__ __forceinline__ explicit DwChunks(const ExpertArgs& a) {
+    E = a.offsets ? a.n_experts : 1;
+    C = a.chunk;
+    total = 0;
+    room = (int)(2 * (int64_t)a.rows / C);
+    for (int c = 0; c < E; c += 64) {
+      int lo, hi, n, sum, slots;
+      group(a, c, lo, hi, n, sum, slots);
+      total += __builtin_amdgcn_readlane(sum, 63);
+    }
+  }
+  __device__ __forceinline__ DwChunk at(const ExpertArgs& a, int i) const {
+    DwChunk r{0, 0, -1, -1};
+    if (i >= total) return r;
+    for (int c = 0, before = 0, used = 0; c < E; c += 64) {
+      int lo, hi, n, sum, slots;
+      group(a, c, lo, hi, n, sum, slots);
+      const uint64_t past = __ballot(before + sum > i);
+      if (past != 0) {
+        const int l = __builtin_ctzll(past);
+        const int k = i - before - __builtin_amdgcn_readlane(sum - n, l);    // chunk of the group
+        const int many = __builtin_amdgcn_readlane(n, l);
+        r.e = c + l;
+        r.row0 = __builtin_amdgcn_readlane(lo, l) + k * C;
+        r.rows = min(C, __builtin_amdgcn_readlane(hi, l) - r.row0);
+        r.slot = many > 1 ? used + __builtin_amdgcn_readlane(slots, l) - many + k : -1;
+        if (r.slot >= room) r.rows = -1;
+        break;
+      }
+      before += __builtin_amdgcn_readlane(sum, 63);
+      used += __builtin_amdgcn_readlane(slots, 63);
+    }
+    return r;
+  }
+  // Chunks of group e and the first one's slot (if it has several).
+  __device__ __forceinline__ void of_group(const ExpertArgs& a, int e, int& many, int& first) const {
+    many = first = 0;
+    for (int c = 0, used = 0; c < E; c += 64) {
+      int lo, hi, n, sum, slots;
+      group(a, c, lo, hi, n, sum, slots);
+      if (e < c + 64) {
+        many = __builtin_amdgcn_readlane(n, e - c);
+        first = used + __builtin_amdgcn_readlane(slots, e - c) - many;
+        if (first + many > room) many = 0;
+        break;
+      }
+      used += __builtin_amdgcn_readlane(slots, 63);
+    }
+  }
+};
+
 // Eight E2M1 codes (one word) times 2^(x - 127) -> eight bf16, exact.
 __device__ __forceinline__ u32x4 bf16_of_e2m1(uint32_t w, float scale) {
   u32x4 o;

@@ -79,7 +79,29 @@ struct ExpertArgs {
   const uint8_t* a_scale;       // MXFP4 scale codes of A [..][K / 32], B [N][K / 32] per expert
   const uint8_t* b_scale;
   int32_t accumulate;           // dW form: add to C
+  int32_t chunk;                // dW form: rows of a group summed by one workgroup, 0: all
+  float* part;                  // sums of the chunks of groups that have several, [slot][M][N]
 };
+
+// Rows a dW chunk takes, 0 for no chunks: where the tiles of all experts
+// leave CUs idle, the rows are cut into pieces that give about 1024 tiles of
+// 128 x 128, of at least 256 rows (a piece's partial sums are written and read
+// once, 2 x 64 KiB a tile, against 4 KiB of operands per row).
+inline int64_t dw_tiles128(int64_t m, int64_t n) { return ((m + 127) / 128) * ((n + 127) / 128); }
+inline int64_t dw_chunk(int64_t rows, int64_t experts, int64_t m, int64_t n) {
+  const int64_t t = dw_tiles128(m, n);
+  if (experts * t >= 1024) return 0;
+  const int64_t even = ((rows * t + 1023) / 1024 + 63) / 64 * 64, c = even > 256 ? even : 256;
+  return rows > c ? c : 0;
+}
+// Bytes of the partial sums of at most `rows` rows: a group of more than one
+// chunk of c rows has at most 2 / c chunks a row.
+inline int64_t dw_part_bytes(int64_t rows, int64_t experts, int64_t m, int64_t n) {
+  const int64_t t = dw_tiles128(m, n);
+  if (experts * t >= 1024 || rows <= 256) return 0;
+  const int64_t a = rows / 128, b = 2048 / t + 1;
+  return (a < b ? a : b) * m * n * 4;
+}
 
 enum class ExpertForm { kBf16, kF32, kW4A16, kW4A4 };
 
@@ -89,7 +111,8 @@ void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStre
 // The same for few rows per group, in one of the tiles of rows x cols that
 // kernels_expert.hip chooses from.
 void launch_expert_few(ExpertForm form, bool b_kc, int rows, int cols, const ExpertArgs& a, hipStream_t s);
-// dW form, bf16 or fp32 operands, both n-contiguous.
+// dW form, bf16 or fp32 operands, both n-contiguous; with a.chunk a second
+// kernel adds the chunks of a group in order.
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s);
 
 }  // namespace mlora

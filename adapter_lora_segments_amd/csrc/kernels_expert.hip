@@ -67,43 +67,66 @@ struct Tile {
   int e, row0, mrows;   // grouped rows [row0, row0 + mrows); dW: row0 is the group's first row, mrows the tile's
   int m0, n0;           // first row of dW_e (else 0) and first column
   int klen;             // length of the reduction
+  int slot;             // dW: partial sums' slot, or -1: dW itself
 };
+// dW: where the tile's sums go, and whether they are added to what is there.
+__device__ __forceinline__ float* dw_out(const ExpertArgs& g, const Tile& t) {
+  return t.slot < 0 ? static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert : g.part + (int64_t)t.slot * g.c_expert;
+}
+__device__ __forceinline__ bool dw_adds(const ExpertArgs& g, const Tile& t) { return g.accumulate && t.slot < 0; }
 template <int BM, int BN, bool DW>
 __device__ __forceinline__ Tile find_tile(const ExpertArgs& g) {
   const int nN = (g.N + BN - 1) / BN;
   Tile t;
   if constexpr (DW) {
-    // Experts have reductions of different lengths: every expert's tiles are
-    // spread over all XCDs, and up to 64 experts run longest first, so the
-    // launch does not end on one XCD's long tiles.
-    const int nM = (g.M + BM - 1) / BM, TT = nM * nN, share = (TT + 7) / 8;
+    const int nM = (g.M + BM - 1) / BM, TT = nM * nN;
     const int xcd = blockIdx.x & 7, q = blockIdx.x >> 3;
-    int i = xcd * share + q % share;
-    t.e = q / share;
-    if (g.offsets && g.n_experts <= 64) {
-      const int lane = threadIdx.x & 63;
-      int lo = 0, hi = -1;
-      if (lane < g.n_experts) group_rows(g, lane, lo, hi);
-      const int n = hi - lo;
-      int rank = 0;
-      for (int j = 0; j < g.n_experts; ++j) {
-        const int nj = __builtin_amdgcn_readlane(n, j);
-        rank += nj > n || (nj == n && j < lane) ? 1 : 0;
+    int i;
+    t.slot = -1;
+    if (g.chunk > 0) {
+      // Chunks of equal length: a contiguous run of tiles for each XCD.
+      const DwChunks chunks(g);
+      const int T = chunks.total * TT, per = T >> 3, rem = T & 7;
+      const int L = xcd * per + min(xcd, rem) + q;
+      const bool on = q < per + (xcd < rem ? 1 : 0);
+      const DwChunk c = chunks.at(g, on ? L / TT : chunks.total);
+      i = c.rows >= 0 ? L % TT : TT;
+      t.e = c.e;
+      t.row0 = c.row0;
+      t.klen = max(c.rows, 0);
+      t.slot = c.slot;
+    } else {
+      // Experts have reductions of different lengths: every expert's tiles are
+      // spread over all XCDs, and up to 64 experts run longest first, so the
+      // launch does not end on one XCD's long tiles.
+      const int share = (TT + 7) / 8;
+      i = xcd * share + q % share;
+      t.e = q / share;
+      if (g.offsets && g.n_experts <= 64) {
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = -1;
+        if (lane < g.n_experts) group_rows(g, lane, lo, hi);
+        const int n = hi - lo;
+        int rank = 0;
+        for (int j = 0; j < g.n_experts; ++j) {
+          const int nj = __builtin_amdgcn_readlane(n, j);
+          rank += nj > n || (nj == n && j < lane) ? 1 : 0;
+        }
+        t.e = __builtin_ctzll(__ballot(lane < g.n_experts && rank == t.e));
       }
-      t.e = __builtin_ctzll(__ballot(lane < g.n_experts && rank == t.e));
+      int hi;
+      group_rows(g, t.e, t.row0, hi);
+      t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+      t.klen = __builtin_amdgcn_readfirstlane(hi) - t.row0;
     }
     constexpr int GM = 4;
-    const int fm = i / (GM * nN) * GM, gm = min(GM, nM - fm), within = i - fm * nN;
+    const int fm = i / (GM * nN) * GM, gm = max(1, min(GM, nM - fm)), within = i - fm * nN;
     t.m0 = (fm + within % gm) * BM;
     t.n0 = within / gm * BN;
-    int hi;
-    group_rows(g, t.e, t.row0, hi);
-    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-    t.klen = __builtin_amdgcn_readfirstlane(hi) - t.row0;
     t.mrows = i < TT ? min(BM, g.M - t.m0) : 0;
   } else {
     const RowTile r = RowTiles<BM, 4>(g, nN).at(g, blockIdx.x);
-    t = Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
+    t = Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K, -1};
   }
   return t;
 }
@@ -128,7 +151,7 @@ __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&ac
     const int m = wrow + 32 * fi + l32;
     const int row = DW ? (m < t.mrows ? t.m0 + m : -1) : out_row(g, t, m);
     if (row < 0) continue;
-    float* crow = static_cast<float*>(g.C) + (DW ? (int64_t)t.e * g.c_expert : 0) + (int64_t)row * g.ldc;
+    float* crow = (DW ? dw_out(g, t) : static_cast<float*>(g.C)) + (int64_t)row * g.ldc;
 #pragma unroll
     for (int fj = 0; fj < FJ; ++fj) {
 #pragma unroll
@@ -137,7 +160,7 @@ __device__ __forceinline__ void store_f32(const ExpertArgs& g, const f32x16 (&ac
         if (n >= g.N) continue;
         f32x4 v = {acc[fi][fj][4 * gg], acc[fi][fj][4 * gg + 1], acc[fi][fj][4 * gg + 2], acc[fi][fj][4 * gg + 3]};
         f32x4* dst = reinterpret_cast<f32x4*>(crow + n);
-        if (DW && g.accumulate) v += *dst;
+        if (DW && dw_adds(g, t)) v += *dst;
         *dst = v;
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -152,7 +175,8 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc
                                          int w, int lane) {
   constexpr int BN = 64 * FJ, GPR = BN / 4, RPI = 64 / GPR;
   const int half = lane >> 5, l32 = lane & 31, wcol = 32 * FJ * (w & 1);
-  float* const c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
+  float* const c = dw_out(g, t);
+  const bool adds = dw_adds(g, t);
   const int n = t.n0 + 4 * (lane % GPR);
   __syncthreads();
 #pragma unroll
@@ -175,7 +199,7 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc
       f32x4 v = *reinterpret_cast<const f32x4*>(buf + mr * (BN * 4) + 16 * ((lane % GPR) ^ (mr & 31)));
       if (m < t.mrows && n < g.N) {
         f32x4* dst = reinterpret_cast<f32x4*>(c + (int64_t)(t.m0 + m) * g.ldc + n);
-        if (g.accumulate) v += *dst;
+        if (adds) v += *dst;
         *dst = v;
       }
     }
@@ -185,9 +209,9 @@ __device__ __forceinline__ void store_dw(const ExpertArgs& g, const f32x16 (&acc
 // dW of a group without rows: zeros (kept when accumulating).
 template <int BN>
 __device__ __forceinline__ void store_zero(const ExpertArgs& g, const Tile& t) {
-  if (g.accumulate) return;
+  if (dw_adds(g, t)) return;
   constexpr int GPR = BN / 4;
-  float* c = static_cast<float*>(g.C) + (int64_t)t.e * g.c_expert;
+  float* c = dw_out(g, t);
   const int n = t.n0 + 4 * (threadIdx.x % GPR);
   if (n >= g.N) return;
   for (int m = threadIdx.x / GPR; m < t.mrows; m += 256 / GPR)
@@ -385,7 +409,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   auto rows_tile = [&](int b) {
     const ExpertArgs& g = kernel_args();
     const RowTile r = tiles.at(g, b);
-    return Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K};
+    return Tile{r.e, r.row0, r.mrows, 0, r.tn * BN, g.K, -1};
   };
   Tile tl;
   if constexpr (DW) tl = find_tile<BM, BN, DW>(kernel_args());
@@ -1122,10 +1146,29 @@ void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStre
 
 namespace {
 
+// dW of the groups with several chunks: their sums added in order.
+__global__ __launch_bounds__(256) void k_expert_dw_sum(ExpertArgs a, int pieces) {
+  const int e = blockIdx.x / pieces, piece = blockIdx.x - e * pieces;
+  int many, first;
+  DwChunks(a).of_group(a, e, many, first);
+  if (many <= 1) return;
+  const int64_t n = a.c_expert / 4;              // vectors of four (M or N is a multiple of 4)
+  const f32x4* part = reinterpret_cast<const f32x4*>(a.part + (int64_t)first * a.c_expert);
+  f32x4* out = reinterpret_cast<f32x4*>(static_cast<float*>(a.C) + (int64_t)e * a.c_expert);
+  for (int64_t i = (int64_t)piece * 1024 + threadIdx.x; i < n && i < (int64_t)(piece + 1) * 1024; i += 256) {
+    f32x4 sum = part[i];
+    for (int c = 1; c < many; ++c) sum += part[c * n + i];
+    if (a.accumulate) sum += out[i];
+    out[i] = sum;
+  }
+}
+
 template <int BM>
 int64_t dw_grid(const ExpertArgs& a) {
   const int64_t E = a.offsets ? a.n_experts : 1;
-  return 8 * E * (((int64_t)((a.M + BM - 1) / BM) * ((a.N + BM - 1) / BM) + 7) / 8);
+  const int64_t tt = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BM - 1) / BM);
+  if (a.chunk > 0) return ((a.rows / a.chunk + E) * tt + 7) / 8 * 8;
+  return 8 * E * ((tt + 7) / 8);
 }
 template <int FI>
 void dw_pipe(const ExpertArgs& a, hipStream_t s) {
@@ -1141,21 +1184,28 @@ void dw_f32(const ExpertArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// dW tiles: 256 x 256, or smaller ones while those leave CUs idle.  Measured
-// (microseconds, experts x d_in x d_out, 100 rows each): bf16 8 x 512 x 1024
-// (64 tiles of 256 x 256) 17.0 against 9.6 with 128 x 128, 32 x 512 x 1024 (256
-// tiles) 22.6 against 34.0; fp32 8 x 512 x 1024 45 (256), 18.1 (128), 17.6 (64),
-// with 1000 rows each 266, 90 and 94; 32 x 512 x 1024 51, 52 and 55.
+// dW tiles: 256 x 256, or smaller ones while those leave CUs idle or are mostly
+// padding.  Measured (us, experts x d_in x d_out, 100 rows each): bf16 8 x 512 x
+// 1024 (64 tiles of 256 x 256) 17.0 against 9.6 with 128 x 128, 32 x 512 x 1024
+// (256 tiles) 22.6 against 34.0; fp32 8 x 512 x 1024 45 (256), 18.1 (128), 17.6
+// (64), with 1000 rows each 266, 90 and 94; 32 x 512 x 1024 51, 52 and 55.
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
-  const int64_t tiles = E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256), t128 = dw_tiles128(a.M, a.N);
+  // groups, or chunks of them
+  const int64_t pieces = a.chunk > 0 ? E + a.rows / a.chunk : E;
+  const bool padded = 4 * t256 * 2 > t128 * 3;
   if (f32) {
-    if (tiles >= 192) dw_f32<4>(a, s);
-    else if (tiles >= 48 && a.rows / E >= 400) dw_f32<2>(a, s);
+    if (pieces * t256 >= 192 && !padded) dw_f32<4>(a, s);
+    else if (pieces * t128 >= 192 && a.rows / pieces >= 400) dw_f32<2>(a, s);
     else dw_f32<1>(a, s);
   } else {
-    if (tiles >= 160) dw_pipe<4>(a, s);
+    if (pieces * t256 >= 160 && !padded) dw_pipe<4>(a, s);
     else dw_pipe<2>(a, s);
+  }
+  if (a.chunk > 0) {
+    const int64_t blocks = (a.c_expert / 4 + 1023) / 1024;
+    hipLaunchKernelGGL(k_expert_dw_sum, dim3((unsigned)(E * blocks)), dim3(256), 0, s, a, (int)blocks);
   }
 }
 

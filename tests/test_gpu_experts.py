@@ -183,6 +183,52 @@ def test_accumulated_gradients(dt):
     assert not L.dW.any()
 
 
+CHUNKS = {"skewed": [0, 700, 1, 300, 257, 2000, 256, 0],
+          "one": [3000],
+          "wide": [5 if e % 9 else 600 for e in range(80)]}
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("order", [False, True])
+@pytest.mark.parametrize("sizes", list(CHUNKS))
+def test_gradients_summed_in_chunks(sizes, order, dt):
+    """Groups cut into pieces of 256 rows whose sums are added by a second
+    kernel: dW, its accumulation, the same bits twice, a captured one, and
+    offsets out of order, which stay in the workspace."""
+    import torch
+    say(f"chunks {sizes} {order} {dt}")
+    c = Case(CHUNKS[sizes], 72, 136, dt, "nk", x_order=order, y_order=order, dropped=3)
+    L = c.layer()
+    assert L.shape.workspace_bytes >= 4 * 72 * 136 * 2
+    L.backward(c.dY, c.X, c.d_off, c.d_order, want_dx=False)
+    _, _, _, dW, SW = ox.backward(c.dYh, c.Xh, c.Wm, c.off, c.order, c.rows, **c.kw)
+    check(L.dW, c.wdw(dW), c.wdw(SW), max(CHUNKS[sizes]), "fp32", "dW")
+    first = L.dW.clone()
+    A = c.layer(grad_accumulate=True)
+    A.dW.copy_(first)
+    A.backward(c.dY, c.X, c.d_off, c.d_order, want_dx=False)
+    assert torch.equal(A.dW, first + first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.backward(c.dY, c.X, c.d_off, c.d_order, want_dx=False)
+    for _ in range(3):
+        L.dW.fill_(9.0)
+        A.ws.fill_(255)
+        A.backward(c.dY, c.X, c.d_off, c.d_order, want_dx=False)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(L.dW, first)
+    # every group is all rows: far more chunks than the workspace has room for
+    n = L.ws.numel()
+    pad = torch.full((n + 2 ** 20,), 7, dtype=torch.uint8, device="cuda")
+    L.ws = pad[2 ** 19:2 ** 19 + n]
+    off = c.d_off.clone()
+    off[::2], off[1::2] = -4, 2 ** 31 - 1
+    L.backward(c.dY, c.X, off, c.d_order, want_dx=False)
+    assert (pad[:2 ** 19] == 7).all() and (pad[2 ** 19 + n:] == 7).all()
+
+
 def test_single_expert_without_offsets():
     import torch
     c = Case([333], 136, 72)
