@@ -17,9 +17,9 @@ __device__ __forceinline__ const ExpertArgs& kernel_args() {
   return *(const ExpertArgs*)p;
 }
 
-// n / d for 0 <= n < 2^31 (div_by).
+// n / d for 0 <= n < 2^31 (div_by; mul is 0 for d = 1).
 __device__ __forceinline__ uint32_t div_fast(uint32_t n, const DivBy& d) {
-  return d.mul ? __umulhi(n, d.mul) >> d.shift : n;
+  return (__umulhi(n, d.mul) >> d.shift) + (d.mul ? 0u : n);
 }
 
 // Order entry `v` as a row to read: an entry that names no row reads row 0.

@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_f32(ExpertArgs g) {
 // by four conversions while the slice before is computed, so the weights
 // cross LDS at 4 bits and no decoded copy exists.
 // ---------------------------------------------------------------------------
-template <int AL, int BL, int FI, int NJ, bool DW, bool GATHER>
+template <int AL, int BL, int FI, int NJ, bool DW, int GATHER>
 __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   constexpr bool S4 = AL >= X4, S16 = AL == X4;          // both operands E2M1; their scales' alignment
   constexpr bool AK = AL != NC, BK = BL == KC || S4;     // k-contiguous 128-byte rows
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       } else {
         ac[i] = RPCA * (CA * w + i) + lane / CPRA;
         const int col = min(t.m0 + 8 * ((lane % CPRA) ^ nx16(ac[i])), g.M - 8);
-        ao[i] = (uint32_t)((GATHER ? 0 : ac[i] * arow) + col * 2);
+        ao[i] = (uint32_t)((GATHER & 1 ? 0 : ac[i] * arow) + col * 2);
       }
     }
 #pragma unroll
@@ -473,7 +473,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       } else if constexpr (BL == NC) {
         bc[i] = RPCB * (CB * w + i) + lane / CPRB;
         const int col = min(t.n0 + 8 * ((lane % CPRB) ^ nx16(bc[i])), g.N - 8);
-        bo[i] = (uint32_t)(GATHER ? col * 2 : bc[i] * brow + (col - t.n0) * 2);
+        bo[i] = (uint32_t)(GATHER & 2 ? col * 2 : bc[i] * brow + (col - t.n0) * 2);
       } else {
         const int r = 32 * (CB * w + i) + (lane >> 1);
         bc[i] = 0;
@@ -484,8 +484,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
       sp = g.b_scale + ((int64_t)t.e * g.N + min(t.n0 + 64 * w + lane, g.N - 1)) * (g.ldb / 32);
     if constexpr (S4) sq = g.a_scale + source_row(g, g.ma, t.row0 + min(64 * w + lane, t.mrows - 1)) * (g.lda / 32);
     const uint8_t* Be = DW ? g.B : g.B + (int64_t)t.e * g.b_expert;
-    baseA = AL == NC && !GATHER ? g.A + t.row0 * arow : g.A;
-    baseB = BL != NC ? Be + t.n0 * brow : (GATHER ? Be : Be + (DW ? t.row0 * brow : 0) + t.n0 * 2);
+    baseA = AL == NC && !(GATHER & 1) ? g.A + t.row0 * arow : g.A;
+    baseB = BL != NC ? Be + t.n0 * brow : (GATHER & 2 ? Be : Be + (DW ? t.row0 * brow : 0) + t.n0 * 2);
   };
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(MLORA_LDS void*)&ring[0]);
@@ -499,30 +499,37 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     else return (uint32_t)((u >> 1) % NR) * (UA + UB) + ((u & 1) ? UA : 0);
   };
   // Order entries of this wave's 16 k-rows of a step, by scalar loads (they
-  // wait on lgkmcnt, not on the counter that tracks the copies in flight), and
-  // the row that copy i of either operand reads: k-row 16 w + RPC i + lane / CPR.
+  // wait on lgkmcnt, not on the counter that tracks the copies in flight).
+  // Copy i of either operand reads k-rows 16 w + RPC i + lane / CPR: the lane's
+  // entry is selected first, so the row behind it is computed once per copy
+  // and lane and not in scalar registers for every row.
   static_assert(!GATHER || (AL == NC && BL == NC && BM == BN), "both operands copy the same k-rows");
   int oidx[GATHER ? 16 : 1];
   const int32_t* const order = GATHER ? kernel_args().order : nullptr;
-  const RowMap ma = kernel_args().ma, mb = kernel_args().mb;   // GATHER only
+  const DivBy diva = kernel_args().ma.div, divb = kernel_args().mb.div;   // GATHER only
   const int nrows = kernel_args().rows;
-  auto load_order = [&](int t) {
-    if constexpr (GATHER) {
+  auto load_order = [&](int t, auto check) {
+    if constexpr (GATHER != 0 && check.value) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) oidx[j] = ldc(order + tl.row0 + min(t * KD + 16 * w + j, klen - 1));
+    } else if constexpr (GATHER != 0) {
+      typedef int i32x16 __attribute__((ext_vector_type(16), aligned(4)));
+      const i32x16 v = *(const __attribute__((address_space(4))) i32x16*)(order + tl.row0 + t * KD + 16 * w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) oidx[j] = v[j];
     }
   };
-  auto gathered = [&](const uint8_t* from, const RowMap& map, int64_t row_bytes, int i, int t) -> const uint8_t* {
-    const int k = tl.row0 + t * KD + 16 * w + RPCA * i;
-    int64_t at = 0;
-#pragma unroll
-    for (int h = 0; h < RPCA; ++h) {
-      const int64_t row = map.by_order
-                              ? (int64_t)div_fast(read_row(oidx[(RPCA * i + h) % (GATHER ? 16 : 1)], nrows), map.div)
-                              : (int64_t)(k + h);
-      at = lane / CPRA == h ? row * row_bytes : at;
-    }
-    return from + at;
+  static_assert(!GATHER || RPCA == 2 || RPCA == 4, "k-rows of a copy");
+  // masks of the lanes on odd k-rows of a copy and on its rows 2 and 3 (opaque:
+  // of selects by lane the compiler makes one chain over all 16 entries)
+  int odd = GATHER && (lane / CPRA & 1) ? -1 : 0, upper = GATHER && (lane / CPRA & 2) ? -1 : 0;
+  if constexpr (GATHER != 0) asm volatile("" : "+v"(odd), "+v"(upper));
+  auto gathered = [&](const uint8_t* from, const DivBy& div, int64_t row_bytes, int i) -> const uint8_t* {
+    auto entry = [&](int h) { return oidx[(RPCA * i + h) % (GATHER ? 16 : 1)]; };
+    auto pick = [](int mask, int b, int a) { return (mask & b) | (~mask & a); };
+    int v = pick(odd, entry(1), entry(0));
+    if constexpr (RPCA == 4) v = pick(upper, pick(odd, entry(3), entry(2)), v);
+    return from + (uint64_t)div_fast(read_row(v, nrows), div) * (uint32_t)row_bytes;
   };
   // Copy i of step t's A (B) unit.  CHECK: the step may pass the end of the
   // reduction, and what does reads zeros.
@@ -531,8 +538,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     if constexpr (AK) {
       const uint8_t* src = ap[i] + 128 * (int64_t)t;
       dma16_at(!check.value || t * KD + EPC * ac[i] < klen ? src : zero, lds);
-    } else if constexpr (GATHER) {
-      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA, ma, arow, i, t) + ao[i] : zero, lds);
+    } else if constexpr (GATHER & 1) {
+      dma16_at(!check.value || t * KD + ac[i] < klen ? gathered(baseA + ao[i], diva, arow, i) : zero, lds);
     } else if constexpr (check.value) {
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseA + t * stepA));
       dma16_at(t * KD + ac[i] < klen ? at + ao[i] : zero, lds);
@@ -542,8 +549,8 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   };
   auto copy_b = [&](int t, int i, auto check) {
     const uint32_t lds = lds_b + slot(2 * t + 1) + 1024u * i;
-    if constexpr (BL == NC && GATHER) {
-      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB, mb, brow, i, t) + bo[i] : zero, lds);
+    if constexpr (BL == NC && (GATHER & 2) != 0) {
+      dma16_at(!check.value || t * KD + bc[i] < klen ? gathered(baseB + bo[i], divb, brow, i) : zero, lds);
     } else if constexpr (check.value) {
       const bool on = BL == NC ? t * KD + bc[i] < klen : t * KD + EPC * bc[i] < klen;
       const uint8_t* at = reinterpret_cast<const uint8_t*>(uniform64(baseB + t * stepB));
@@ -731,7 +738,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     constexpr bool COPY = KIND < 2, COPY_A = RING4 ? KIND != 2 : COPY;
     const std::integral_constant<bool, KIND != 0> check{};
     Bases cur;
-    if (COPY) load_order(s + D);
+    if (COPY) load_order(s + D, check);
     step_bases(s, cur, 1, 3);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -845,7 +852,7 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
     if constexpr (S16) dma16_at(sp, lds0 + RING + 4096u + 1024u * (uint32_t)w);   // B's scales of steps 0 and 1
 #pragma unroll
     for (int t = 0; t < D; ++t) {
-      load_order(t);
+      load_order(t, check);
       if (!(RING4 && t == 1)) {
 #pragma unroll
         for (int i = 0; i < CA; ++i) copy_a(t, i, check);
@@ -998,7 +1005,7 @@ constexpr int64_t kCus = 256;
 template <int AL, int BL, int FI, int NJ>
 void rows_pipe(const ExpertArgs& a, hipStream_t s) {
   const int64_t most = rows_grid(a, 64 * FI, 64 * NJ), grid = most < kCus ? most : kCus;
-  hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, NJ, false, false>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_expert_pipe<AL, BL, FI, NJ, false, 0>), dim3((unsigned)grid), dim3(256), 0, s, a);
 }
 template <int BL, int FI, int NJ>
 void rows_f32_tile(const ExpertArgs& a, hipStream_t s) {
@@ -1173,9 +1180,12 @@ int64_t dw_grid(const ExpertArgs& a) {
 template <int FI>
 void dw_pipe(const ExpertArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)dw_grid<64 * FI>(a));
-  if (a.ma.by_order || a.mb.by_order)
-    hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, false>), grid, dim3(256), 0, s, a);
+  switch ((a.ma.by_order ? 1 : 0) + (a.mb.by_order ? 2 : 0)) {
+    case 0: hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, 0>), grid, dim3(256), 0, s, a); break;
+    case 1: hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, 1>), grid, dim3(256), 0, s, a); break;
+    case 2: hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, 2>), grid, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_expert_pipe<NC, NC, FI, FI, true, 3>), grid, dim3(256), 0, s, a);
+  }
 }
 template <int FI>
 void dw_f32(const ExpertArgs& a, hipStream_t s) {
