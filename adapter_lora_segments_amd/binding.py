@@ -524,11 +524,13 @@ def _one_device(*tensors):
 def _launch(index, fn, *args):
     """check(fn(*args)) with device ``index`` current."""
     torch = _torch()
-    if index == torch.cuda.current_device():
-        check(fn(*args))
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args)
     else:
         with torch.cuda.device(index):
-            check(fn(*args))
+            status = fn(*args)
+    if status:
+        check(status)
 
 
 def group_rows_workspace(rows: int, n_groups: int) -> int:
@@ -605,6 +607,10 @@ class ExpertShape:
             self.w_shape = (microscale_bytes(self.n_experts * self.d_out, self.d_in),)
         else:
             self.w_shape = (self.n_experts,) + ((self.d_in, self.d_out) if w_layout == "kn" else (self.d_out, self.d_in))
+        # torch's dtypes of the activations and of the weight
+        torch = _torch()
+        self.t_dtype = _dt(self)
+        self.t_w_dtype = torch.uint8 if w_format == "mxfp4" else self.t_dtype
 
     def struct(self, rows: int):
         """The C structure for a call of ``rows`` rows (never changed once made:
@@ -625,8 +631,7 @@ class ExpertShape:
 
 
 def _check_weight(shape: ExpertShape, W):
-    torch = _torch()
-    _need(W, "W", shape.w_shape, torch.uint8 if shape.w_format == "mxfp4" else _dt(shape))
+    _need(W, "W", shape.w_shape, shape.t_w_dtype)
 
 
 def _check_tables(shape: ExpertShape, rows: int, offsets, order, ws):
@@ -645,7 +650,7 @@ def mlora_expert_forward(shape: ExpertShape, X, W, offsets, order, Y, ws=None, s
     """Y[y(s)] = X[x(s)] W_e for every expert e and its grouped rows s (rows
     of Y that belong to no group are left as they were)."""
     rows = Y.shape[0]
-    dt = _dt(shape)
+    dt = shape.t_dtype
     _need(X, "X", (shape.src_rows(rows), shape.d_in), dt)
     _need(Y, "Y", (rows, shape.d_out), dt)
     _check_weight(shape, W)
@@ -661,7 +666,7 @@ def mlora_expert_backward(shape: ExpertShape, dY, X, W, offsets, order, dX, dW, 
     dX or dW may be None to skip it."""
     torch = _torch()
     rows = dY.shape[0]
-    dt = _dt(shape)
+    dt = shape.t_dtype
     _need(dY, "dY", (rows, shape.d_out), dt)
     if X is not None:
         _need(X, "X", (shape.src_rows(rows), shape.d_in), dt)

@@ -1,6 +1,7 @@
 // Grouped expert products for gfx950: one base weight per group of rows,
 // Y = X W_e and dX = dY W_e^T over ragged row groups, dW_e = X^T dY over each
 // group's rows, on matrix instructions with fp32 accumulation.
+#include <cmath>
 #include "expert_common.hpp"
 #include "gemm_common.hpp"
 
@@ -1076,9 +1077,8 @@ template <int N>
 const Choice& choose(const Choice (&list)[N], const ExpertArgs& a, double weight_bytes) {
   double groups = 1;
   if (a.offsets && a.n_experts > 1) {
-    double empty = 1;           // chance that a group gets none of the rows
-    for (double p = 1.0 - 1.0 / a.n_experts, n = a.rows; n >= 1 && empty > 1e-3; n -= 1) empty *= p;
-    groups = a.n_experts * (1 - empty);
+    // less the chance that a group gets none of the rows
+    groups = a.n_experts * (1 - std::pow(1.0 - 1.0 / a.n_experts, a.rows));
   }
   const double mean = a.rows / groups;
   int best = 0;
