@@ -85,7 +85,7 @@ int64_t dx_ws(const mlora_expert_shape& s) {
   return s.w_format == MLORA_W0_MXFP4 ? 2 * (int64_t)s.n_experts * s.d_in * s.d_out : 0;
 }
 int64_t dw_ws(const mlora_expert_shape& s) {
-  return s.w_format == MLORA_W0_MXFP4 ? 0 : mlora::dw_part_bytes(s.rows, s.n_experts, s.d_in, s.d_out);
+  return s.w_format == MLORA_W0_MXFP4 ? 0 : mlora::dw_part_bytes(s.dtype == MLORA_FP32, s.rows, s.n_experts, s.d_in, s.d_out);
 }
 
 mlora_status check_call(const mlora_expert_shape* s, const int32_t* offsets, const int32_t* order, void* ws,
@@ -270,7 +270,7 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
     a.C = dW;
     a.c_expert = wn;
     a.accumulate = s.grad_accumulate;
-    a.chunk = (int32_t)mlora::dw_chunk(s.rows, s.n_experts, s.d_in, s.d_out);
+    a.chunk = (int32_t)mlora::dw_chunk(f32, s.rows, s.n_experts, s.d_in, s.d_out);
     a.part = static_cast<float*>(workspace);
     mlora::launch_expert_dw(f32, a, cs);
     st = launched();

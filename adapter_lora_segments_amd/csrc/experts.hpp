@@ -83,23 +83,29 @@ struct ExpertArgs {
   float* part;                  // sums of the chunks of groups that have several, [slot][M][N]
 };
 
-// Rows a dW chunk takes, 0 for no chunks: where the tiles of all experts
-// leave CUs idle, the rows are cut into pieces that give about 1024 tiles of
-// 128 x 128, of at least 256 rows (a piece's partial sums are written and read
-// once, 2 x 64 KiB a tile, against 4 KiB of operands per row).
+// Rows a dW chunk takes, 0 for no chunks: where the 128 x 128 tiles of all
+// experts do not fill the 256 CUs, long groups are cut into pieces that would,
+// of at least 1024 rows (bf16) or 256 (fp32): a piece's partial sums are
+// written and read once, 2 x 64 KiB a tile, so more or shorter pieces cost more
+// than they spread.  Measured (us, uncut and cut, one expert): bf16 136 x 864,
+// 4000 rows 30 and 17, 16000 rows 100 and 21; 512 x 1024, 16000 rows 100 and
+// 31; 2048 x 2048 (256 tiles), 4000 rows 41 and 78 with pieces of 1024.  fp32
+// 136 x 864, 1000 rows 29 and 15, 16000 rows 404 and 73; 512 x 1024 over 16
+// experts (512 tiles), 8000 skewed rows 116 and 140 with pieces of 256.
 inline int64_t dw_tiles128(int64_t m, int64_t n) { return ((m + 127) / 128) * ((n + 127) / 128); }
-inline int64_t dw_chunk(int64_t rows, int64_t experts, int64_t m, int64_t n) {
+inline int64_t dw_least(bool f32) { return f32 ? 256 : 1024; }
+inline int64_t dw_chunk(bool f32, int64_t rows, int64_t experts, int64_t m, int64_t n) {
   const int64_t t = dw_tiles128(m, n);
-  if (experts * t >= 1024) return 0;
-  const int64_t even = ((rows * t + 1023) / 1024 + 63) / 64 * 64, c = even > 256 ? even : 256;
+  if (experts * t >= 256) return 0;
+  const int64_t even = ((rows * t + 255) / 256 + 63) / 64 * 64, c = even > dw_least(f32) ? even : dw_least(f32);
   return rows > c ? c : 0;
 }
 // Bytes of the partial sums of at most `rows` rows: a group of more than one
 // chunk of c rows has at most 2 / c chunks a row.
-inline int64_t dw_part_bytes(int64_t rows, int64_t experts, int64_t m, int64_t n) {
+inline int64_t dw_part_bytes(bool f32, int64_t rows, int64_t experts, int64_t m, int64_t n) {
   const int64_t t = dw_tiles128(m, n);
-  if (experts * t >= 1024 || rows <= 256) return 0;
-  const int64_t a = rows / 128, b = 2048 / t + 1;
+  if (experts * t >= 256 || rows <= dw_least(f32)) return 0;
+  const int64_t a = 2 * rows / dw_least(f32), b = 512 / t;
   return (a < b ? a : b) * m * n * 4;
 }
 

@@ -1162,12 +1162,17 @@ __global__ __launch_bounds__(256) void k_expert_dw_sum(ExpertArgs a, int pieces)
   const int64_t n = a.c_expert / 4;              // vectors of four (M or N is a multiple of 4)
   const f32x4* part = reinterpret_cast<const f32x4*>(a.part + (int64_t)first * a.c_expert);
   f32x4* out = reinterpret_cast<f32x4*>(static_cast<float*>(a.C) + (int64_t)e * a.c_expert);
-  for (int64_t i = (int64_t)piece * 1024 + threadIdx.x; i < n && i < (int64_t)(piece + 1) * 1024; i += 256) {
-    f32x4 sum = part[i];
-    for (int c = 1; c < many; ++c) sum += part[c * n + i];
-    if (a.accumulate) sum += out[i];
-    out[i] = sum;
+  const int64_t i = (int64_t)piece * 256 + threadIdx.x;
+  if (i >= n) return;
+  f32x4 sum = part[i];
+  int c = 1;
+  for (; c + 3 < many; c += 4) {   // four loads in flight, added in order
+    const f32x4 v0 = part[c * n + i], v1 = part[(c + 1) * n + i], v2 = part[(c + 2) * n + i], v3 = part[(c + 3) * n + i];
+    sum = (((sum + v0) + v1) + v2) + v3;
   }
+  for (; c < many; ++c) sum += part[c * n + i];
+  if (a.accumulate) sum += out[i];
+  out[i] = sum;
 }
 
 template <int BM>
@@ -1194,27 +1199,30 @@ void dw_f32(const ExpertArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// dW tiles: 256 x 256, or smaller ones while those leave CUs idle or are mostly
-// padding.  Measured (us, experts x d_in x d_out, 100 rows each): bf16 8 x 512 x
-// 1024 (64 tiles of 256 x 256) 17.0 against 9.6 with 128 x 128, 32 x 512 x 1024
-// (256 tiles) 22.6 against 34.0; fp32 8 x 512 x 1024 45 (256), 18.1 (128), 17.6
-// (64), with 1000 rows each 266, 90 and 94; 32 x 512 x 1024 51, 52 and 55.
+// dW tiles.  A group's sizes are not known here, and one workgroup sums all of a
+// group's rows: the longest group sets a lower bound, which small tiles keep
+// low.  bf16: 256 x 256 where they fill the chip, one expert has 32 of them and
+// they are not mostly padding, else 128 x 128; fp32: 256 x 256 or 128 x 128
+// where one expert's nearly fill the chip, else 64 x 64.  Measured (us): bf16
+// 8 x 512 x 1024, 100 rows each 17.0 (256) and 9.6 (128); 8 x 2048 x 2048, 1000
+// rows each 82 and 118; 64 x 512 x 1024, 32000 skewed rows 167 and 96 (but 32 x
+// 1000 rows 52 and 77).  fp32 (256, 128, 64): 16 x 832 x 2212, 2000 skewed rows
+// 177, 102, 99; 2048 x 2048, 1000 rows 266, 86, 94; 8 of them 539, 558, 633;
+// 32 x 4096 x 4096, 100 rows each 1423, 1543, 1587.
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
   const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256), t128 = dw_tiles128(a.M, a.N);
-  // groups, or chunks of them
-  const int64_t pieces = a.chunk > 0 ? E + a.rows / a.chunk : E;
-  const bool padded = 4 * t256 * 2 > t128 * 3;
+  const bool padded = 8 * t256 > 3 * t128;      // over 1.5 times the area
   if (f32) {
-    if (pieces * t256 >= 192 && !padded) dw_f32<4>(a, s);
-    else if (pieces * t128 >= 192 && a.rows / pieces >= 400) dw_f32<2>(a, s);
+    if (t256 >= 256 && !padded) dw_f32<4>(a, s);
+    else if (t128 >= 192) dw_f32<2>(a, s);
     else dw_f32<1>(a, s);
   } else {
-    if (pieces * t256 >= 160 && !padded) dw_pipe<4>(a, s);
+    if (E * t256 >= 160 && t256 >= 32 && !padded) dw_pipe<4>(a, s);
     else dw_pipe<2>(a, s);
   }
   if (a.chunk > 0) {
-    const int64_t blocks = (a.c_expert / 4 + 1023) / 1024;
+    const int64_t blocks = (a.c_expert / 4 + 255) / 256;
     hipLaunchKernelGGL(k_expert_dw_sum, dim3((unsigned)(E * blocks)), dim3(256), 0, s, a, (int)blocks);
   }
 }

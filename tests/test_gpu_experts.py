@@ -185,6 +185,7 @@ def test_accumulated_gradients(dt):
 
 CHUNKS = {"skewed": [0, 700, 1, 300, 257, 2000, 256, 0],
           "one": [3000],
+          "long": [5000, 20, 2500],
           "wide": [5 if e % 9 else 600 for e in range(80)]}
 
 
@@ -192,7 +193,7 @@ CHUNKS = {"skewed": [0, 700, 1, 300, 257, 2000, 256, 0],
 @pytest.mark.parametrize("order", [False, True])
 @pytest.mark.parametrize("sizes", list(CHUNKS))
 def test_gradients_summed_in_chunks(sizes, order, dt):
-    """Groups cut into pieces of 256 rows whose sums are added by a second
+    """Groups cut into pieces (of 256 rows, fp32, or 1024, bf16) whose sums are added by a second
     kernel: dW, its accumulation, the same bits twice, a captured one, and
     offsets out of order, which stay in the workspace."""
     import torch
