@@ -34,7 +34,7 @@ mlora_status launched() noexcept {
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+using mlora::kMaxGrid;
 
 // Message of the first thing wrong with a shape, or NULL.
 const char* shape_error(const mlora_expert_shape& s, mlora_status* st) {
@@ -62,12 +62,15 @@ const char* shape_error(const mlora_expert_shape& s, mlora_status* st) {
     return "expert: MXFP4 weights need bf16, the NK layout and d_in a multiple of 128";
   if (s.act_format == MLORA_ACT_MXFP4 && s.w_format != MLORA_W0_MXFP4)
     return "expert: MXFP4 activations need MXFP4 weights";
-  // launch bounds, at the smallest tiles any form takes (16 rows, 16 columns;
-  // 256 x 256 for dW)
-  const int64_t d = s.d_in > s.d_out ? s.d_in : s.d_out;
-  const int64_t tiles = s.rows / 16 + (s.n_experts < s.rows ? s.n_experts : s.rows);
-  const int64_t dw = (int64_t)s.n_experts * ((s.d_in + 255) / 256) * ((s.d_out + 255) / 256);
-  if (tiles > kMaxGrid / ((d + 15) / 16) || dw > kMaxGrid) return "expert: too many tiles for one launch";
+  // launch bounds at 256 x 256 tiles (smaller ones are taken where they fit),
+  // and those of the MXFP4 conversions, a thread per 8 activations or 32 weights
+  const int64_t d = (s.d_in > s.d_out ? s.d_in : s.d_out) + 255;
+  const int64_t tiles = s.rows / 256 + (s.n_experts < s.rows ? s.n_experts : s.rows);
+  const int64_t dw = (((s.d_in + 255) / 256) * ((s.d_out + 255) / 256) + 7) / 8 * 8;
+  if (tiles > kMaxGrid / (d / 256) || dw > kMaxGrid / s.n_experts ||
+      (s.act_format == MLORA_ACT_MXFP4 && s.rows > kMaxGrid * 256 / (s.d_in / 8)) ||
+      (s.w_format == MLORA_W0_MXFP4 && s.n_experts * s.d_out > kMaxGrid * 256 / (s.d_in / 32)))
+    return "expert: too many tiles for one launch";
   *st = MLORA_OK;
   return nullptr;
 }

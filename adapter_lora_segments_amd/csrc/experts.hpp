@@ -83,6 +83,9 @@ struct ExpertArgs {
   float* part;                  // sums of the chunks of groups that have several, [slot][M][N]
 };
 
+// Workgroups of a launch: their threads (512 each at most) fit 32 bits.
+constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
+
 // Rows a dW chunk takes, 0 for no chunks: where the 128 x 128 tiles of all
 // experts do not fill the 256 CUs, long groups are cut into pieces that would,
 // of at least 1024 rows (bf16) or 256 (fp32): a piece's partial sums are

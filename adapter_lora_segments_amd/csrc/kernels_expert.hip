@@ -1073,18 +1073,21 @@ constexpr Choice kW4A4[] = {{true, 16, 16, 3.2, .0007, .0010, 2.9e6},   {true, 1
                             {false, 64, 256, 4.2, .0029, .0045, 5.6e6}, {false, 128, 128, 4.2, .0024, .0039, 4.4e6},
                             {false, 128, 256, 5.4, .0037, .0069, 5.0e6}, {false, 256, 256, 8.0, .0055, .0121, 3.7e6}};
 
+// (fixed: one workgroup per tile also in the tiled kernel; the last entry's grid
+// always fits a launch.)
 template <int N>
-const Choice& choose(const Choice (&list)[N], const ExpertArgs& a, double weight_bytes) {
+const Choice& choose(const Choice (&list)[N], bool fixed, const ExpertArgs& a, double weight_bytes) {
   double groups = 1;
   if (a.offsets && a.n_experts > 1) {
     // less the chance that a group gets none of the rows
     groups = a.n_experts * (1 - std::pow(1.0 - 1.0 / a.n_experts, a.rows));
   }
   const double mean = a.rows / groups;
-  int best = 0;
+  int best = -1;
   double best_us = 0;
   for (int i = 0; i < N; ++i) {
     const Choice& c = list[i];
+    if ((c.few || fixed) && i + 1 < N && rows_grid(a, c.rows, c.cols) > kMaxGrid) continue;
     double tiles = groups == 1 ? (a.rows + c.rows - 1) / c.rows : mean / c.rows + 0.5;
     if (tiles < 1) tiles = 1;
     const double rounds = groups * tiles * ((a.N + c.cols - 1) / c.cols) / kCus;
@@ -1094,7 +1097,7 @@ const Choice& choose(const Choice (&list)[N], const ExpertArgs& a, double weight
     const double fill = 0.5 + 0.75 * rounds;
     const double read = c.start + groups * weight_bytes / (c.rate * (fill < 1 ? fill : 1));
     if (read > us) us = read;
-    if (i == 0 || us < best_us) {
+    if (best < 0 || us < best_us) {
       best = i;
       best_us = us;
     }
@@ -1105,7 +1108,7 @@ const Choice& choose(const Choice (&list)[N], const ExpertArgs& a, double weight
 template <int AL, int BL, int N>
 void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weight_bytes, const ExpertArgs& a,
                hipStream_t s) {
-  const Choice& t = choose(list, a, weight_bytes);
+  const Choice& t = choose(list, false, a, weight_bytes);
   const int r = t.rows, c = t.cols;
   if (t.few) return launch_expert_few(form, b_kc, r, c, a, s);
   if (r == 64 && c == 128) return rows_pipe<AL, BL, 1, 2>(a, s);
@@ -1118,7 +1121,7 @@ void rows_bf16(ExpertForm form, bool b_kc, const Choice (&list)[N], double weigh
 }
 template <int BL, int N>
 void rows_f32(const Choice (&list)[N], bool b_kc, const ExpertArgs& a, hipStream_t s) {
-  const Choice& t = choose(list, a, 4.0 * a.K * a.N);
+  const Choice& t = choose(list, true, a, 4.0 * a.K * a.N);
   const int r = t.rows, c = t.cols;
   if (t.few) return launch_expert_few(ExpertForm::kF32, b_kc, r, c, a, s);
   if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
@@ -1212,7 +1215,7 @@ void dw_f32(const ExpertArgs& a, hipStream_t s) {
 void launch_expert_dw(bool f32, const ExpertArgs& a, hipStream_t s) {
   const int64_t E = a.offsets ? a.n_experts : 1;
   const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256), t128 = dw_tiles128(a.M, a.N);
-  const bool padded = 8 * t256 > 3 * t128;      // over 1.5 times the area
+  const bool padded = 8 * t256 > 3 * t128 && E * t128 < kMaxGrid / 2;      // over 1.5 times the area
   if (f32) {
     if (t256 >= 256 && !padded) dw_f32<4>(a, s);
     else if (t128 >= 192) dw_f32<2>(a, s);

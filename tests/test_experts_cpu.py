@@ -105,7 +105,9 @@ BAD_SHAPES = [(dict(rows=-1), -1), (dict(rows=1 << 31), -1), (dict(n_experts=0),
               (dict(y_by_order=-1), -1), (dict(grad_accumulate=5), -1), (dict(w_format=1), -1),
               (dict(act_format=1), -1), (dict(d_in=(1 << 20) + 8), -2), (dict(w_format=2, d_in=64), -2),
               (dict(w_format=2, w_layout=0), -2), (dict(w_format=2, dtype=0), -2), (dict(act_format=2), -2),
-              (dict(rows=(1 << 31) - 1, d_out=1 << 20), -2)]
+              (dict(rows=(1 << 31) - 1, d_out=1 << 20), -2), (dict(rows=1 << 28, d_out=4096), -2),
+              (dict(n_experts=4096, d_in=1 << 15, d_out=1 << 15), -2),
+              (dict(w_format=2, act_format=2, rows=1 << 24, d_in=1 << 15, d_out=8), -2)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_SHAPES)
