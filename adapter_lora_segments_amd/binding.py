@@ -690,7 +690,9 @@ class ExpertLinear:
     [n_experts][d_out][d_in] for "nk", the packed buffer of
     ``mlora_microscale_quantize`` for "mxfp4").  ``forward`` and ``backward``
     take up to ``max_rows`` grouped rows; ``dW`` holds the fp32 gradients of
-    the last backward (with grad_accumulate, their sum since it was zeroed)."""
+    the last backward (with grad_accumulate, their sum since it was zeroed).
+    The calls share the workspace ``ws``: those that may overlap, on two streams
+    or in graphs that run at once, need an ExpertLinear each (over one W)."""
 
     def __init__(self, W, n_experts: int, d_in: int, d_out: int, max_rows: int, **options):
         torch = _torch()

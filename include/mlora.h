@@ -536,7 +536,8 @@ mlora_status mlora_group_rows(const int32_t *ids, int64_t rows, int32_t n_groups
  * experts in one buffer, [n_experts][d_in][d_out] (MLORA_W0_KN) or
  * [n_experts][d_out][d_in] (MLORA_W0_NK); dW has W's layout.  Rows are dense.
  * d_in and d_out: multiples of 8 (bf16) or 4 (fp32), at most
- * MLORA_MAX_EXPERT_DIM.
+ * MLORA_MAX_EXPERT_DIM.  A launch takes up to 2^23 - 1 tiles of 256 x 256 of
+ * any product (Y, dX, all dW_e); larger shapes are MLORA_ERR_UNSUPPORTED.
  *
  * w_format MLORA_W0_MXFP4 (bf16, MLORA_W0_NK, d_in a multiple of 128): W is
  * the packed buffer that mlora_microscale_quantize makes of the
@@ -570,7 +571,8 @@ typedef struct {
 } mlora_expert_shape;
 
 /* Workspace of forward and backward for this shape or one with fewer rows (0
- * when none is needed).  Nothing in it has to be kept between calls; calls
+ * when none is needed): X's codes (MLORA_ACT_MXFP4), the decoded weight of an
+ * MXFP4 dX, partial sums of dW where few experts have long groups.  Nothing in it has to be kept between calls; calls
  * that may overlap (streams, replays of captured graphs) need one each. */
 mlora_status mlora_expert_workspace(const mlora_expert_shape *shape, int64_t *bytes);
 

@@ -217,3 +217,24 @@ def test_binding_refusals():
         b.mlora_microscale_quantize(x)
     with pytest.raises(ValueError, match="device tensor"):
         b.mlora_group_rows(torch.zeros(4, dtype=torch.int32), 2, None, None)
+
+
+@pytest.mark.parametrize("dtype,least", [(1, 1024), (0, 256)])
+def test_workspace_of_gradient_chunks(dtype, least):
+    """The partial sums' room: none while no group can be cut, never less for
+    more rows, and never past two slots per `least` rows; none once the tiles
+    of all experts fill the chip."""
+    L, n = _lib.lib(), ctypes.c_int64()
+
+    def need(**kw):
+        assert L.mlora_expert_workspace(ctypes.byref(shape(dtype=dtype, **kw)), ctypes.byref(n)) == 0
+        return n.value
+
+    for experts, di, do in ((1, 136, 864), (4, 72, 136), (7, 512, 1024)):
+        last = 0
+        for rows in list(range(0, 4 * least, 61)) + [10 ** 5, 10 ** 7, 10 ** 8]:
+            v = need(rows=rows, n_experts=experts, d_in=di, d_out=do)
+            assert v >= last and v <= 2 * rows // least * di * do * 4
+            assert (v == 0) == (rows <= least)
+            last = v
+    assert need(rows=10 ** 6, n_experts=64, d_in=512, d_out=1024) == 0
