@@ -164,6 +164,26 @@ def test_backward(sizes, dims, dt, layout):
     assert torch.equal(L.dW, first)
 
 
+@pytest.mark.parametrize("x_order,y_order", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("dt,di,do,sizes", [("bf16", 1032, 2056, [70, 0, 129, 1, 200]),
+                                            ("fp32", 1540, 2052, [70, 1, 0]), ("fp32", 4100, 4100, [33, 0, 70])])
+def test_gradients_of_wide_weights(dt, di, do, sizes, x_order, y_order):
+    """dW in the tiles that wide weights take (256 x 256, fp32 128 x 128), with
+    either operand's rows by order, and dX beside it; accumulated once more."""
+    import torch
+    say(f"wide {dt} {di}x{do} {x_order} {y_order}")
+    c = Case(sizes, di, do, dt, "nk" if x_order else "kn", top_k=2 if x_order and y_order else 1, x_order=x_order,
+             y_order=y_order, dropped=5)
+    A = c.layer(grad_accumulate=True)
+    dX = A.backward(c.dY, c.X, c.d_off, c.d_order)
+    want, SX, owned, dW, SW = ox.backward(c.dYh, c.Xh, c.Wm, c.off, c.order, c.rows, **c.kw)
+    check(dX.double().cpu().numpy()[owned], want[owned], SX[owned], do, dt, "dX")
+    check(A.dW, c.wdw(dW), c.wdw(SW), max(sizes), "fp32", "dW")
+    one = A.dW.clone()
+    A.backward(c.dY, c.X, c.d_off, c.d_order, want_dx=False)
+    assert torch.equal(A.dW, one + one)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_accumulated_gradients(dt):
     """Two backwards into one dW: bit for bit the fp32 sums of two separate ones."""
@@ -596,3 +616,46 @@ def test_offsets_past_32_bits():
     for lo, hi, e in ((0, 10, 0), (T - 1000, T, E - 1), (262000, 262300, E - 1)):
         x, w = X[lo:hi].double().cpu().numpy(), W[e].double().cpu().numpy()
         check(Y[lo:hi], x @ w, np.abs(x) @ np.abs(w), di, "bf16", f"rows {lo}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gradient_rows_past_32_bits(dt):
+    """dW and dX whose rows lie behind the 4 GiB mark of X, dY and dX."""
+    import torch
+    from adapter_lora_segments_amd import ExpertLinear
+    say(f"gradient rows past 32 bits {dt}")
+    di, do, T = (4096, 8, 600000) if dt == "bf16" else (4096, 8, 300000)
+    X = torch.zeros(T, di, device="cuda", dtype=_t(dt))
+    dY = torch.zeros(T, do, device="cuda", dtype=_t(dt))
+    rows = torch.cat([torch.arange(T - 90, T), torch.arange(5), torch.arange(T - 300, T - 100)]).int()
+    for t in (X, dY):
+        t[rows.cuda().long()] = torch.randn(rows.numel(), t.shape[1], device="cuda").to(t.dtype)
+    W = torch.randn(2, di, do, device="cuda").to(_t(dt))
+    order = torch.full((T,), -1, dtype=torch.int32)
+    order[:rows.numel()] = rows
+    off = torch.tensor([0, 95, rows.numel()], dtype=torch.int32).cuda()
+    L = ExpertLinear(W, 2, di, do, T, dtype=dt, x_order=True, y_order=True)
+    dX = L.backward(dY, X, off, order.cuda())                                        # 4.9 GB each
+    for e, (lo, hi) in enumerate(((0, 95), (95, rows.numel()))):
+        at = rows[lo:hi].cuda().long()
+        x, dy, w = (t.double().cpu().numpy() for t in (X[at], dY[at], W[e]))
+        check(L.dW[e], x.T @ dy, np.abs(x).T @ np.abs(dy), hi - lo, "fp32", "dW")
+        check(dX[at], dy @ w.T, np.abs(dy) @ np.abs(w).T, do, dt, "dX")
+
+
+def test_as_many_experts_as_there_may_be():
+    """4096 experts, most of them empty: forward, dX and dW."""
+    rng = np.random.default_rng(3)
+    sizes = [0] * 4096
+    for e in rng.integers(0, 4096, size=37):
+        sizes[e] += 3
+    sizes[4095] += 1
+    c = Case(sizes, 16, 8, x_order=True, dropped=2)
+    L = c.layer()
+    want, S, _ = ox.forward(c.Xh, c.Wm, c.off, c.order, c.rows, **c.kw)
+    n = int(c.off[-1])
+    check(L.forward(c.X, c.d_off, c.d_order)[:n], want[:n], S[:n], 16, "bf16", "Y")
+    dX = L.backward(c.dY, c.X, c.d_off, c.d_order)
+    want, SX, owned, dW, SW = ox.backward(c.dYh, c.Xh, c.Wm, c.off, c.order, c.rows, **c.kw)
+    check(dX.double().cpu().numpy()[owned], want[owned], SX[owned], 8, "bf16", "dX")
+    check(L.dW, dW, SW, max(sizes), "fp32", "dW")
