@@ -689,8 +689,9 @@ __global__ __launch_bounds__(256, 1) void k_expert_pipe(ExpertArgs) {
   // What MFMA slot q of a slice reads of slice ks (bases bs):
   // fragments in the order the first MFMAs need them, two per slot, or one
   // where a fragment is two transposing reads or four conversions and the
-  // slice has the slots; X4: with the scales of slices ks and ks + 1.
-  constexpr int RPS = (AK && BK) || FI == 1 ? 2 : 1;
+  // slice has a slot for each; X4: with the scales of slices ks and ks + 1.
+  constexpr int RPS = (AK && BK) || FI == 1 || FIW + FJW > NS ? 2 : 1;
+  static_assert(FIW + FJW <= RPS * NS, "a slice's slots read all of the next one's fragments");
   auto reads_at = [&](int q, const Bases& bs, int ks, u32x4 (&ra)[FIW], u32x4 (&rb)[FJW]) {
 #pragma unroll
     for (int j = 0; j < RPS; ++j) {
@@ -1069,7 +1070,7 @@ constexpr Choice kF32Nk[] = {{true, 16, 16, 3.0, .0040, .0048, 4.7e6},   {true, 
                              {false, 128, 128, 3.8, .0675, .0647, 4.0e6}, {false, 128, 256, 4.1, .1247, .1285, 4.0e6},
                              {false, 256, 256, 5.0, .2350, .2500, 4.0e6}};
 constexpr Choice kF32Kn[] = {{true, 16, 64, 3.0, .0080, .0094, 5.2e6},   {true, 32, 64, 3.0, .0118, .0111, 5.0e6},
-                             {true, 64, 64, 3.0, .0190, .0206, 3.0e6},   {false, 64, 64, 3.5, .0231, .0185, 4.5e6},
+                             {true, 64, 64, 3.0, .0190, .0206, 3.0e6},
                              {false, 64, 128, 3.7, .0389, .0353, 4.5e6}, {false, 64, 256, 4.0, .0686, .0708, 4.5e6},
                              {false, 128, 128, 3.8, .0675, .0647, 4.5e6}, {false, 128, 256, 4.1, .1247, .1285, 4.5e6},
                              {false, 256, 256, 5.0, .2350, .2500, 4.5e6}};
@@ -1136,7 +1137,8 @@ void rows_f32(const Choice (&list)[N], bool b_kc, const ExpertArgs& a, hipStream
   const Choice& t = choose(list, true, a, 4.0 * a.K * a.N);
   const int r = t.rows, c = t.cols;
   if (t.few) return launch_expert_few(ExpertForm::kF32, b_kc, r, c, a, s);
-  if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
+  if constexpr (BL == KC)     // (n-contiguous weights: the few-row kernel is faster wherever this tile would do)
+    if (r == 64 && c == 64) return rows_f32_tile<BL, 1, 1>(a, s);
   if (r == 64 && c == 128) return rows_f32_tile<BL, 1, 2>(a, s);
   if (r == 64) return rows_f32_tile<BL, 1, 4>(a, s);
   if (r == 128 && c == 128) return rows_f32_tile<BL, 2, 2>(a, s);

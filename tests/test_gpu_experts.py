@@ -134,6 +134,95 @@ def test_forward(sizes, dims, dt, layout):
     check(y[owned], want[owned], S[owned], di, dt, "Y")
 
 
+# Products (rows, experts, d_in, d_out), the smallest of a grid of sizes that
+# between them take every few-row and tile form of each type and layout, over a
+# short reduction and a long one.
+FORMS = {
+    "bf16 nk": [(1, 1, 128, 72), (1, 1, 1152, 72), (48, 32, 128, 264), (48, 32, 1152, 264), (384, 16, 128, 520),
+                (384, 16, 1152, 520), (1024, 3, 256, 14336), (1024, 64, 1152, 264), (1536, 1, 128, 72),
+                (1536, 1, 1152, 72), (1536, 64, 128, 72), (1536, 64, 1152, 72), (1536, 64, 1152, 136),
+                (3000, 2, 256, 14336), (3000, 64, 128, 72), (3000, 64, 128, 520), (3000, 64, 1152, 72),
+                (4096, 64, 256, 136), (8192, 1, 1152, 136), (16384, 1, 1152, 136), (16384, 8, 256, 264),
+                (16384, 64, 1152, 136), (32768, 1, 128, 264), (32768, 64, 1152, 136)],
+    "bf16 kn": [(1, 1, 128, 72), (1, 1, 1152, 72), (8, 3, 128, 2056), (8, 3, 1152, 2056), (768, 2, 1152, 14336),
+                (1536, 64, 1280, 520), (2048, 8, 128, 14336), (3000, 1, 128, 72), (3000, 1, 1152, 72),
+                (3000, 8, 256, 14336), (4096, 64, 1152, 72), (8192, 1, 1152, 136), (8192, 64, 256, 136),
+                (16384, 1, 1152, 136), (16384, 64, 1152, 136), (32768, 1, 128, 72), (32768, 1, 128, 264),
+                (32768, 1, 256, 72)],
+    "fp32 nk": [(1, 1, 128, 72), (1, 1, 1152, 72), (48, 2, 1152, 14336), (64, 2, 128, 14336), (96, 3, 1152, 14336),
+                (128, 2, 1152, 14336), (128, 3, 128, 14336), (128, 3, 1152, 4104), (128, 64, 128, 72),
+                (128, 64, 1152, 72), (384, 2, 128, 14336), (384, 3, 256, 2056), (384, 16, 128, 264),
+                (384, 16, 1152, 264), (768, 32, 128, 72), (768, 32, 1152, 72), (3000, 1, 128, 4104),
+                (3000, 1, 1152, 4104), (3000, 64, 128, 72), (3000, 64, 1152, 72), (32768, 1, 128, 72),
+                (32768, 1, 1152, 136)],
+    "fp32 kn": [(1, 1, 128, 72), (1, 1, 1152, 72), (200, 2, 1152, 14336), (384, 2, 1152, 14336), (3000, 1, 128, 72),
+                (3000, 1, 1152, 72), (3000, 1, 1152, 4104), (3000, 3, 128, 4104), (3000, 8, 128, 2056),
+                (3000, 16, 128, 2056), (8192, 1, 128, 72), (8192, 1, 1152, 72), (16384, 1, 1152, 72),
+                (32768, 1, 128, 72), (32768, 1, 1152, 72)],
+    "w4 bf16": [(1, 1, 128, 72), (1, 1, 128, 14336), (1, 1, 1152, 72), (1, 1, 1152, 14336), (128, 8, 1152, 4104),
+                (256, 8, 128, 14336), (384, 64, 128, 72), (384, 64, 1152, 72), (1536, 8, 128, 14336),
+                (1536, 32, 128, 136), (1536, 32, 1152, 136), (2048, 1, 128, 72), (2048, 1, 1152, 72),
+                (3000, 64, 1152, 136), (4096, 32, 1152, 264), (8192, 1, 128, 4104), (8192, 1, 128, 14336),
+                (8192, 64, 1152, 264), (16384, 1, 128, 136), (16384, 1, 256, 72), (16384, 2, 1152, 136),
+                (32768, 64, 1152, 136)],
+    "w4 mxfp4": [(1, 1, 128, 72), (1, 1, 128, 14336), (1, 1, 1152, 72), (1, 1, 1152, 14336), (1, 1, 2048, 72),
+                 (1, 1, 2048, 14336), (48, 32, 2048, 1032), (96, 64, 1152, 520), (128, 32, 1280, 520),
+                 (128, 64, 2048, 264), (160, 64, 128, 72), (160, 64, 256, 1032), (160, 64, 1152, 72),
+                 (160, 64, 2048, 72), (768, 32, 128, 264), (768, 32, 1152, 264), (1536, 1, 1280, 14336),
+                 (1536, 32, 128, 72), (1536, 32, 1152, 72), (1536, 32, 2048, 72), (3000, 1, 256, 14336),
+                 (3000, 1, 2048, 4104), (4096, 16, 1152, 264), (4096, 16, 2048, 264), (16384, 1, 128, 72),
+                 (16384, 1, 128, 14336), (16384, 2, 128, 72), (16384, 2, 1152, 136), (16384, 2, 2048, 136)],
+}
+
+
+@pytest.mark.parametrize("form,size", [(f, s) for f in FORMS for s in FORMS[f]])
+def test_every_form(form, size):
+    """Ragged groups, rows by order in half of the cases, against float64
+    products on the device."""
+    import torch
+    from adapter_lora_segments_amd import ExpertLinear, mlora_microscale_quantize
+    say(f"form {form} {size}")
+    rows, E, di, do = size
+    kind, how = form.split()
+    dt = "fp32" if kind == "fp32" else "bf16"
+    rng = np.random.default_rng(rows + E + di + do)
+    p = 1.0 / (1 + np.arange(E))
+    if E > 2:
+        p[E // 2] = 0.0                                     # an expert without rows
+    sizes = rng.permutation(rng.multinomial(rows, p / p.sum()))
+    c = np.concatenate([[0], np.cumsum(sizes)])
+    off = torch.from_numpy(c.astype(np.int32)).cuda()
+    by = (rows + di) % 3 != 0
+    order = torch.from_numpy(rng.permutation(rows).astype(np.int32)).cuda() if by else None
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    X = torch.randn(rows, di, generator=g, device="cuda").to(_t(dt))
+    opts = dict(dtype=dt, x_order=by, y_order=by)
+    if kind == "w4":
+        codes = rng.integers(0, 16, size=(E * do, di), dtype=np.uint8)
+        scales = rng.integers(115, 126, size=(E * do, di // 32), dtype=np.uint8)
+        W = torch.from_numpy(ox.pack(codes, scales)).cuda()
+        Wd = torch.from_numpy(ox.decode(codes, scales).reshape(E, do, di)).cuda().transpose(1, 2)
+        opts.update(w_layout="nk", w_format="mxfp4", act_format=how)
+    else:
+        W = torch.randn(*((E, do, di) if how == "nk" else (E, di, do)), generator=g, device="cuda").to(_t(dt))
+        Wd = W.double().transpose(1, 2) if how == "nk" else W.double()
+        opts.update(w_layout=how)
+    Y = ExpertLinear(W, E, di, do, rows, **opts).forward(X, off, order)
+    V = X
+    if how == "mxfp4":
+        V = torch.empty_like(X)
+        mlora_microscale_quantize(X, values=V)
+    V = V.double()
+    for e in range(E):
+        at = slice(int(c[e]), int(c[e + 1]))
+        at = order[at].long() if by else at
+        x, w = V[at], Wd[e].contiguous()
+        want, S = x @ w, x.abs() @ w.abs()
+        bound = HALF[dt] * want.abs() + (di + 2) * 2.0 ** -23 * S * (1 + 2.0 ** -8)
+        ok = (Y[at].double() - want).abs() <= bound          # NaN fails
+        assert ok.all(), f"expert {e}: {int((~ok).sum())} of {ok.numel()} past the bound"
+
+
 @pytest.mark.parametrize("sizes", ["few", "sixty", "hundreds", "big"])
 @pytest.mark.parametrize("dims", DIMS)
 @pytest.mark.parametrize("dt,layout", [("bf16", "kn"), ("bf16", "nk"), ("fp32", "kn"), ("fp32", "nk")])
@@ -165,14 +254,15 @@ def test_backward(sizes, dims, dt, layout):
 
 
 @pytest.mark.parametrize("x_order,y_order", [(False, False), (True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
 @pytest.mark.parametrize("dt,di,do,sizes", [("bf16", 1032, 2056, [70, 0, 129, 1, 200]),
                                             ("fp32", 1540, 2052, [70, 1, 0]), ("fp32", 4100, 4100, [33, 0, 70])])
-def test_gradients_of_wide_weights(dt, di, do, sizes, x_order, y_order):
+def test_gradients_of_wide_weights(dt, di, do, sizes, layout, x_order, y_order):
     """dW in the tiles that wide weights take (256 x 256, fp32 128 x 128), with
     either operand's rows by order, and dX beside it; accumulated once more."""
     import torch
-    say(f"wide {dt} {di}x{do} {x_order} {y_order}")
-    c = Case(sizes, di, do, dt, "nk" if x_order else "kn", top_k=2 if x_order and y_order else 1, x_order=x_order,
+    say(f"wide {dt} {di}x{do} {layout} {x_order} {y_order}")
+    c = Case(sizes, di, do, dt, layout, top_k=2 if x_order and y_order else 1, x_order=x_order,
              y_order=y_order, dropped=5)
     A = c.layer(grad_accumulate=True)
     dX = A.backward(c.dY, c.X, c.d_off, c.d_order)
