@@ -218,6 +218,15 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _made(stream, make, shape, dtype, device):
+    """make(shape) on ``stream`` (None: the current stream): memory that a call
+    hands to its kernels, and its fill, have to be ordered with them."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _torch().cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _dt(plan):
     torch = _torch()
     return torch.bfloat16 if plan.dtype == "bf16" else torch.float32
@@ -692,7 +701,10 @@ class ExpertLinear:
     take up to ``max_rows`` grouped rows; ``dW`` holds the fp32 gradients of
     the last backward (with grad_accumulate, their sum since it was zeroed).
     The calls share the workspace ``ws``: those that may overlap, on two streams
-    or in graphs that run at once, need an ExpertLinear each (over one W)."""
+    or in graphs that run at once, need an ExpertLinear each (over one W).
+    A call given a ``stream`` runs there, and what it makes (Y, dX, the first
+    ``dW``) is made there: the stream has to wait for the inputs and for what
+    the constructor filled, and a reader on another stream for the results."""
 
     def __init__(self, W, n_experts: int, d_in: int, d_out: int, max_rows: int, **options):
         torch = _torch()
@@ -712,7 +724,7 @@ class ExpertLinear:
         if Y is None:
             rows = X.shape[0] * sh.top_k if sh.x_order else X.shape[0]
             make = torch.zeros if sh.y_order else torch.empty
-            Y = make((rows, sh.d_out), dtype=X.dtype, device=X.device)
+            Y = _made(stream, make, (rows, sh.d_out), X.dtype, X.device)
         return mlora_expert_forward(sh, X, self.W, offsets, order, Y, self.ws, stream)
 
     def backward(self, dY, X, offsets=None, order=None, dX=None, want_dx=True, want_dw=True, stream=None):
@@ -723,10 +735,10 @@ class ExpertLinear:
         sh = self.shape
         if want_dx and dX is None:
             make = torch.zeros if sh.x_order else torch.empty
-            dX = make((dY.shape[0], sh.d_in), dtype=dY.dtype, device=dY.device)
+            dX = _made(stream, make, (dY.shape[0], sh.d_in), dY.dtype, dY.device)
         want_dw = want_dw and sh.w_format == "bf16"
         if want_dw and self.dW is None:
-            self.dW = torch.empty(sh.w_shape, dtype=torch.float32, device=self.W.device)
+            self.dW = _made(stream, torch.empty, sh.w_shape, torch.float32, self.W.device)
         mlora_expert_backward(sh, dY, X, self.W, offsets, order, dX if want_dx else None,
                               self.dW if want_dw else None, self.ws, stream)
         return dX if want_dx else None
@@ -739,7 +751,7 @@ def microscale_bytes(rows: int, cols: int) -> int:
 
 def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", stream=None):
     """X [rows][cols] (bf16 or fp32, rows contiguous) to MXFP4: q, the packed
-    buffer of codes and scales, made if None.  along: "cols", blocks of 32
+    buffer of codes and scales, made if None (on ``stream`` if one is given).  along: "cols", blocks of 32
     along a row (a [d_out][d_in] weight or activations), or "rows", blocks down
     a column (a [d_in][d_out] weight).  values: None or a dense tensor like X
     for the decoded elements."""
@@ -755,7 +767,7 @@ def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", strea
         raise ValueError("X's rows must be contiguous")
     n = microscale_bytes(rows, cols)
     if q is None:
-        q = torch.empty(n, dtype=torch.uint8, device=X.device)
+        q = _made(stream, torch.empty, n, torch.uint8, X.device)
     _need(q, "q", (n,), torch.uint8)
     if values is not None:
         _need(values, "values", (rows, cols), X.dtype)

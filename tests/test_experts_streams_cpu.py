@@ -1,0 +1,75 @@
+"""Tensors that a call makes for itself (outputs not given, the first dW, the
+quantizer's buffer) are made on the stream that the call's kernels run on, so
+neither their fill nor the last use of their memory can meet the kernels.
+Shown without a GPU: torch's makers are watched and no kernel is launched."""
+import contextlib
+
+import pytest
+
+from adapter_lora_segments_amd import binding as b
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """[(maker, stream it ran on)] of the torch.zeros and torch.empty calls."""
+    seen, at = [], [None]
+
+    @contextlib.contextmanager
+    def stream(s):
+        was, at[0] = at[0], s
+        yield
+        at[0] = was
+
+    def watch(name):
+        make = getattr(torch, name)
+
+        def run(*a, **k):
+            seen.append((name, at[0]))
+            return make(*a, **k)
+        monkeypatch.setattr(torch, name, run)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    watch("zeros")
+    watch("empty")
+    return seen
+
+
+def layer(**opts):
+    L = b.ExpertLinear.__new__(b.ExpertLinear)
+    L.shape = b.ExpertShape(8, 2, 64, 64, **opts)
+    L.W, L.ws, L.dW = torch.ones(2, 64, 64, dtype=torch.bfloat16), None, None
+    return L
+
+
+@pytest.mark.parametrize("given", [None, "side"])
+@pytest.mark.parametrize("order", [False, True])
+def test_outputs_are_made_on_the_calls_stream(made, monkeypatch, order, given):
+    calls = []
+    monkeypatch.setattr(b, "mlora_expert_forward", lambda *a: calls.append(a[-1]))
+    monkeypatch.setattr(b, "mlora_expert_backward", lambda *a: calls.append(a[-1]))
+    L = layer(x_order=order, y_order=order)
+    x = torch.ones(8, 64, dtype=torch.bfloat16)
+    del made[:]
+    L.forward(x, stream=given)
+    L.backward(x, x, stream=given)
+    fill = "zeros" if order else "empty"
+    assert calls == [given, given]
+    assert made == [(fill, given), (fill, given), ("empty", given)]
+
+
+@pytest.mark.parametrize("given", [None, "side"])
+def test_quantizer_buffer_is_made_on_the_calls_stream(made, monkeypatch, given):
+    class Matrix:
+        dtype, is_cuda, shape, device = torch.bfloat16, True, (4, 64), torch.device("cpu")
+        dim = staticmethod(lambda: 2)
+        stride = staticmethod(lambda i: (64, 1)[i])
+        data_ptr = staticmethod(lambda: 0)
+
+    monkeypatch.setattr(b, "_need", lambda *a: None)
+    monkeypatch.setattr(b, "_one_device", lambda *a: 0)
+    monkeypatch.setattr(b, "_raw_stream", lambda *a: 0)
+    monkeypatch.setattr(b, "_launch", lambda *a: None)
+    b.mlora_microscale_quantize(Matrix(), stream=given)
+    assert made == [("empty", given)]
