@@ -263,9 +263,10 @@ def base_both(W0_kn, stream=None):
     the weight, then its transpose [d_out][d_in] built by the library."""
     torch = _torch()
     d_in, d_out = W0_kn.shape
-    buf = torch.empty(2 * d_in * d_out, dtype=W0_kn.dtype, device=W0_kn.device)
-    buf[: d_in * d_out].view(d_in, d_out).copy_(W0_kn)
-    mlora_base_transpose(W0_kn.contiguous(), buf[d_in * d_out:], stream)
+    with torch.cuda.stream(stream):     # (None: the current one) the copies too
+        buf = torch.empty(2 * d_in * d_out, dtype=W0_kn.dtype, device=W0_kn.device)
+        buf[: d_in * d_out].view(d_in, d_out).copy_(W0_kn)
+        mlora_base_transpose(W0_kn.contiguous(), buf[d_in * d_out:], stream)
     return buf
 
 
@@ -437,7 +438,7 @@ class PackedLoRALinear:
     def forward(self, X, Y=None, stream=None):
         torch = _torch()
         if Y is None:
-            Y = torch.empty((self.plan.info["T"], self.plan.info["d_out"]), dtype=X.dtype, device=X.device)
+            Y = _made(stream, torch.empty, (self.plan.info["T"], self.plan.info["d_out"]), X.dtype, X.device)
         mlora_forward(self.plan, X, self.W0, self.A_ptrs, self.B_ptrs, self.scales, Y, self.Z,
                       self.ws, stream)
         return Y
@@ -445,7 +446,7 @@ class PackedLoRALinear:
     def backward(self, dY, X, dX=None, want_dx=True, stream=None):
         torch = _torch()
         if want_dx and dX is None:
-            dX = torch.empty((self.plan.info["T"], self.plan.info["d_in"]), dtype=X.dtype, device=X.device)
+            dX = _made(stream, torch.empty, (self.plan.info["T"], self.plan.info["d_in"]), X.dtype, X.device)
         mlora_backward(self.plan, dY, X, self.W0, self.A_ptrs, self.B_ptrs, self.scales, self.Z,
                        dX if want_dx else None, self.dA_ptrs, self.dB_ptrs, self.ws, stream)
         return dX
@@ -483,8 +484,9 @@ class AdamW:
         weight_decay, step, optionally max_grad_norm), or a device array
         from ``adamw_hparams``; clip_grads applies each adapter's
         max_grad_norm."""
-        hp = hparams if hasattr(hparams, "data_ptr") else adamw_hparams(hparams, self.layer.ws.device)
         L = self.layer
+        with _torch().cuda.stream(stream):  # (None: the current one) a table made here belongs to the call
+            hp = hparams if hasattr(hparams, "data_ptr") else adamw_hparams(hparams, L.ws.device)
         mlora_adamw_step(L.plan, hp, self.A_ptrs, self.B_ptrs, L.dA_ptrs, L.dB_ptrs, self.mA_ptrs,
                          self.vA_ptrs, self.mB_ptrs, self.vB_ptrs, self.copies[0], self.copies[1],
                          L.ws, stream, clip_grads)

@@ -30,6 +30,7 @@ def made(monkeypatch):
             return make(*a, **k)
         monkeypatch.setattr(torch, name, run)
 
+    stream.at = lambda: at[0]
     monkeypatch.setattr(torch.cuda, "stream", stream)
     watch("zeros")
     watch("empty")
@@ -73,3 +74,40 @@ def test_quantizer_buffer_is_made_on_the_calls_stream(made, monkeypatch, given):
     monkeypatch.setattr(b, "_launch", lambda *a: None)
     b.mlora_microscale_quantize(Matrix(), stream=given)
     assert made == [("empty", given)]
+
+
+@pytest.mark.parametrize("given", [None, "side"])
+def test_packed_layer_outputs_are_made_on_the_calls_stream(made, monkeypatch, given):
+    monkeypatch.setattr(b, "mlora_forward", lambda *a: None)
+    monkeypatch.setattr(b, "mlora_backward", lambda *a: None)
+    L = b.PackedLoRALinear.__new__(b.PackedLoRALinear)
+    L.plan = type("Plan", (), dict(info=dict(T=8, d_in=64, d_out=64)))
+    L.W0 = L.A_ptrs = L.B_ptrs = L.scales = L.Z = L.ws = L.dA_ptrs = L.dB_ptrs = None
+    x = torch.ones(8, 64, dtype=torch.bfloat16)
+    L.forward(x, stream=given)
+    L.backward(x, x, stream=given)
+    assert made == [("empty", given)] * 2
+
+
+def test_two_layout_base_is_copied_on_the_calls_stream(made, monkeypatch):
+    """The copy beside the transpose kernel runs where the buffer is made."""
+    at = []
+    monkeypatch.setattr(b, "mlora_base_transpose", lambda W, out, stream: at.append(stream))
+    copy = torch.Tensor.copy_
+    monkeypatch.setattr(torch.Tensor, "copy_", lambda t, o: (made.append(("copy", torch.cuda.stream.at())), copy(t, o))[1])
+    buf = b.base_both(torch.arange(64 * 64, dtype=torch.float32).view(64, 64), "side")
+    assert buf.numel() == 2 * 64 * 64 and at == ["side"]
+    assert made == [("empty", "side"), ("copy", "side")]
+
+
+@pytest.mark.parametrize("given", [None, "side"])
+def test_optimizer_table_is_made_on_the_calls_stream(made, monkeypatch, given):
+    monkeypatch.setattr(b, "adamw_hparams", lambda *a: made.append(("table", torch.cuda.stream.at())))
+    monkeypatch.setattr(b, "mlora_adamw_step", lambda *a: None)
+    opt = b.AdamW.__new__(b.AdamW)
+    opt.layer = type("Layer", (), dict(plan=None, dA_ptrs=None, dB_ptrs=None, ws=torch.empty(0)))
+    opt.A_ptrs = opt.B_ptrs = opt.mA_ptrs = opt.vA_ptrs = opt.mB_ptrs = opt.vB_ptrs = None
+    opt.copies = (None, None)
+    del made[:]
+    opt.step([{}], stream=given)
+    assert made == [("table", given)]
