@@ -64,7 +64,7 @@ struct RowTiles {
     const int lane = threadIdx.x & 63;
     l = h = 0;
     if (c + lane < E) group_rows(a, c + lane, l, h);
-    n = (h - l + BM - 1) / BM;
+    n = pieces_of(h - l, BM);
     sum = n;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -129,7 +129,7 @@ struct DwChunks {
     lo = hi = n = 0;
     if (c + lane < E) {
       group_rows(a, c + lane, lo, hi);
-      n = max(1, (hi - lo + C - 1) / C);
+      n = max(1, pieces_of(hi - lo, C));
     }
     sum = n;
     slots = n > 1 ? n : 0;

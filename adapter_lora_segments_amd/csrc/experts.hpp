@@ -83,6 +83,10 @@ struct ExpertArgs {
   float* part;                  // sums of the chunks of groups that have several, [slot][M][N]
 };
 
+// Pieces of at most c > 0 rows that n >= 0 rows make.  (n + c - 1) / c would
+// wrap: a dW chunk takes up to 2^23 of up to 2^31 - 257 rows.
+constexpr int pieces_of(int n, int c) { return n > 0 ? (n - 1) / c + 1 : 0; }
+
 // Workgroups of a launch: their threads (512 each at most) fit 32 bits.
 constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
 
