@@ -203,10 +203,4 @@ __device__ __forceinline__ u32x4 bf16_of_e2m1(uint32_t w, float scale) {
   return o;
 }
 
-// Largest number of row tiles that `rows` rows in at most `experts` groups
-// can make.
-inline int64_t max_row_tiles(int64_t rows, int64_t experts, int bm) {
-  return rows / bm + (experts < rows ? experts : rows);
-}
-
 }  // namespace mlora

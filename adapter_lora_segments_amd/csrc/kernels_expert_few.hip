@@ -10,6 +10,7 @@
 // 4096 x 4096 bf16 28 us (176 MB of chosen weights, 6 TB/s with what the
 // last-level cache holds); by latency below that: 4 rows, 4096 -> 14336, MXFP4
 // codes (31 MB) 12.5 us.
+#include "expert_choice.hpp"
 #include "expert_common.hpp"
 
 namespace mlora {
