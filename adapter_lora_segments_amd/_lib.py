@@ -32,7 +32,7 @@ EXPORTS = ["mlora_plan", "mlora_plan_from_ids", "mlora_plan_multi", "mlora_plan_
            "mlora_plan_upload", "mlora_forward", "mlora_backward", "mlora_adamw_step", "mlora_profile_enable",
            "mlora_profile_read", "mlora_device_check", "mlora_status_string", "mlora_last_error",
            "mlora_version", "mlora_base_transpose", "mlora_forward_noalloc", "mlora_group_rows_workspace",
-           "mlora_group_rows", "mlora_expert_workspace", "mlora_expert_forward", "mlora_expert_backward",
+           "mlora_group_rows", "mlora_expert_workspace", "mlora_expert_forward_workspace", "mlora_expert_forward", "mlora_expert_backward",
            "mlora_microscale_quantize"]
 
 
@@ -133,6 +133,8 @@ def lib() -> ctypes.CDLL:
     L.mlora_group_rows.restype = i32
     L.mlora_expert_workspace.argtypes = [ctypes.POINTER(ExpertShape), ctypes.POINTER(i64)]
     L.mlora_expert_workspace.restype = i32
+    L.mlora_expert_forward_workspace.argtypes = L.mlora_expert_workspace.argtypes
+    L.mlora_expert_forward_workspace.restype = i32
     L.mlora_expert_forward.argtypes = [ctypes.POINTER(ExpertShape), vp, vp, vp, vp, vp, vp, sz, vp]
     L.mlora_expert_forward.restype = i32
     L.mlora_expert_backward.argtypes = [ctypes.POINTER(ExpertShape), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]

@@ -613,6 +613,8 @@ class ExpertShape:
         n = ctypes.c_int64()
         check(lib().mlora_expert_workspace(ctypes.byref(self.struct(self.rows)), ctypes.byref(n)))
         self.workspace_bytes = n.value
+        check(lib().mlora_expert_forward_workspace(ctypes.byref(self._c), ctypes.byref(n)))
+        self.forward_workspace_bytes = n.value
         # shape of all experts' weights (MXFP4: of the packed buffer)
         if w_format == "mxfp4":
             self.w_shape = (microscale_bytes(self.n_experts * self.d_out, self.d_in),)
@@ -702,6 +704,8 @@ class ExpertLinear:
     ``mlora_microscale_quantize`` for "mxfp4").  ``forward`` and ``backward``
     take up to ``max_rows`` grouped rows; ``dW`` holds the fp32 gradients of
     the last backward (with grad_accumulate, their sum since it was zeroed).
+    An MXFP4 layer keeps the forward's workspace only: a dX decodes the weight
+    into memory of torch's allocator (2 bytes per weight) for the call.
     The calls share the workspace ``ws``: those that may overlap, on two streams
     or in graphs that run at once, need an ExpertLinear each (over one W).
     A call given a ``stream`` runs there, and what it makes (Y, dX, the first
@@ -713,7 +717,8 @@ class ExpertLinear:
         self.shape = ExpertShape(max_rows, n_experts, d_in, d_out, **options)
         _check_weight(self.shape, W)
         self.W = W
-        self.ws = self.shape.alloc_workspace(W.device)
+        keep = self.shape.forward_workspace_bytes if self.shape.w_format == "mxfp4" else self.shape.workspace_bytes
+        self.ws = torch.empty(keep, dtype=torch.uint8, device=W.device) if keep else None
         self.dW = None
         if self.shape.grad_accumulate and self.shape.w_format == "bf16":
             self.dW = torch.zeros(self.shape.w_shape, dtype=torch.float32, device=W.device)
@@ -741,8 +746,11 @@ class ExpertLinear:
         want_dw = want_dw and sh.w_format == "bf16"
         if want_dw and self.dW is None:
             self.dW = _made(stream, torch.empty, sh.w_shape, torch.float32, self.W.device)
+        ws = self.ws
+        if want_dx and sh.w_format == "mxfp4" and dY.shape[0] > 0:
+            ws = _made(stream, torch.empty, sh.workspace_bytes, torch.uint8, self.W.device)
         mlora_expert_backward(sh, dY, X, self.W, offsets, order, dX if want_dx else None,
-                              self.dW if want_dw else None, self.ws, stream)
+                              self.dW if want_dw else None, ws, stream)
         return dX if want_dx else None
 
 

@@ -160,6 +160,14 @@ mlora_status mlora_expert_workspace(const mlora_expert_shape* shape, int64_t* by
   return MLORA_OK;
 }
 
+mlora_status mlora_expert_forward_workspace(const mlora_expert_shape* shape, int64_t* bytes) {
+  if (!shape || !bytes) return fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
+  mlora_status st;
+  if (const char* msg = shape_error(*shape, &st)) return fail(st, msg);
+  *bytes = forward_ws(*shape);
+  return MLORA_OK;
+}
+
 mlora_status mlora_expert_forward(const mlora_expert_shape* shape, const void* X, const void* W,
                                   const int32_t* offsets, const int32_t* order, void* Y, void* workspace,
                                   size_t ws_bytes, void* stream) {

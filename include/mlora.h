@@ -572,9 +572,13 @@ typedef struct {
 
 /* Workspace of forward and backward for this shape or one with fewer rows (0
  * when none is needed): X's codes (MLORA_ACT_MXFP4), the decoded weight of an
- * MXFP4 dX, partial sums of dW where few experts have long groups.  Nothing in it has to be kept between calls; calls
- * that may overlap (streams, replays of captured graphs) need one each. */
+ * MXFP4 dX (2 bytes per weight of all experts), partial sums of dW where few
+ * experts have long groups.  mlora_expert_forward_workspace: that of the
+ * forward alone, X's codes.  Each call checks for its own share.  Nothing in
+ * it has to be kept between calls; calls that may overlap (streams, replays of
+ * captured graphs) need one each. */
 mlora_status mlora_expert_workspace(const mlora_expert_shape *shape, int64_t *bytes);
+mlora_status mlora_expert_forward_workspace(const mlora_expert_shape *shape, int64_t *bytes);
 
 /* Y per the formulas above.  Pointers 16-byte aligned (offsets and order:
  * 4-byte).  Enqueued on `stream`, kernels only, so the call can be captured
