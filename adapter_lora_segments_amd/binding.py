@@ -706,8 +706,9 @@ class ExpertLinear:
     the last backward (with grad_accumulate, their sum since it was zeroed).
     An MXFP4 layer keeps the forward's workspace only: a dX decodes the weight
     into memory of torch's allocator (2 bytes per weight) for the call.
-    The calls share the workspace ``ws``: those that may overlap, on two streams
-    or in graphs that run at once, need an ExpertLinear each (over one W).
+    The calls share the workspace ``ws``: those that may overlap, on two streams,
+    from two threads or in graphs that run at once, need an ExpertLinear each
+    (over one W).
     A call given a ``stream`` runs there, and what it makes (Y, dX, the first
     ``dW``) is made there: the stream has to wait for the inputs and for what
     the constructor filled, and a reader on another stream for the results."""
@@ -761,10 +762,10 @@ def microscale_bytes(rows: int, cols: int) -> int:
 
 def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", stream=None):
     """X [rows][cols] (bf16 or fp32, rows contiguous) to MXFP4: q, the packed
-    buffer of codes and scales, made if None (on ``stream`` if one is given).  along: "cols", blocks of 32
-    along a row (a [d_out][d_in] weight or activations), or "rows", blocks down
-    a column (a [d_in][d_out] weight).  values: None or a dense tensor like X
-    for the decoded elements."""
+    buffer of codes and scales, made if None (on ``stream`` if one is given).
+    along: "cols", blocks of 32 along a row (a [d_out][d_in] weight or
+    activations), or "rows", blocks down a column (a [d_in][d_out] weight).
+    values: None or a dense tensor like X for the decoded elements."""
     torch = _torch()
     if along not in ("cols", "rows"):
         raise ValueError(f"along must be 'cols' or 'rows', got {along!r}")

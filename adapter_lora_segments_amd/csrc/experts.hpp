@@ -122,7 +122,7 @@ enum class ExpertForm { kBf16, kF32, kW4A16, kW4A4 };
 // (MXFP4 weights are always k-contiguous).
 void launch_expert_rows(ExpertForm form, bool b_kc, const ExpertArgs& a, hipStream_t s);
 // The same for few rows per group, in one of the tiles of rows x cols that
-// kernels_expert.hip chooses from.
+// expert_choice.hpp chooses from.
 void launch_expert_few(ExpertForm form, bool b_kc, int rows, int cols, const ExpertArgs& a, hipStream_t s);
 // dW form, bf16 or fp32 operands, both n-contiguous; with a.chunk a second
 // kernel adds the chunks of a group in order.

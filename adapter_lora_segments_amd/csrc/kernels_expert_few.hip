@@ -7,9 +7,10 @@
 // wave order.  A wave's activations serve its NB column blocks, so more blocks
 // mean fewer loads per weight byte and fewer workgroups.
 // Bound by HBM when enough workgroups are in flight: 8 rows over 8 experts of
-// 4096 x 4096 bf16 28 us (176 MB of chosen weights, 6 TB/s with what the
-// last-level cache holds); by latency below that: 4 rows, 4096 -> 14336, MXFP4
-// codes (31 MB) 12.5 us.
+// 4096 x 4096 bf16, twelve sets of weights in turn 38 us (190 MB of chosen
+// weights a call, 5.0 TB/s), one set over and over 28 us (168 MB, 6.0 TB/s, part
+// of it from the last-level cache); by latency below that: 4 rows, 4096 ->
+// 14336, MXFP4 codes (31 MB) 12.4 us, 224 workgroups of 128 KB of codes each.
 #include "expert_choice.hpp"
 #include "expert_common.hpp"
 

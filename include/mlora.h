@@ -544,7 +544,9 @@ mlora_status mlora_group_rows(const int32_t *ids, int64_t rows, int32_t n_groups
  * [n_experts * d_out][d_in] weights, and is read as codes: no decoded copy
  * is made in the forward.  Such a weight is frozen (dW must be NULL); dX
  * decodes it into the workspace first.  act_format MLORA_ACT_BF16: X as it
- * is, the weights' bf16 values (exact: two significant bits).
+ * is, the weights' bf16 values (exact: two significant bits; past bf16's
+ * range, which scale codes 253 and 254 reach, infinite; the quantizer writes
+ * none above 252 but 255, NaN).
  * MLORA_ACT_MXFP4: X is quantized along d_in into the workspace by the
  * conversion of mlora_microscale_quantize, and both operands go through the
  * 4-bit matrix cores, Y = Q(X) W; the backward's dX = dY W^T is the
@@ -575,8 +577,8 @@ typedef struct {
  * MXFP4 dX (2 bytes per weight of all experts), partial sums of dW where few
  * experts have long groups.  mlora_expert_forward_workspace: that of the
  * forward alone, X's codes.  Each call checks for its own share.  Nothing in
- * it has to be kept between calls; calls that may overlap (streams, replays of
- * captured graphs) need one each. */
+ * it has to be kept between calls; calls that may overlap (streams, host
+ * threads, replays of captured graphs) need one each. */
 mlora_status mlora_expert_workspace(const mlora_expert_shape *shape, int64_t *bytes);
 mlora_status mlora_expert_forward_workspace(const mlora_expert_shape *shape, int64_t *bytes);
 
