@@ -218,13 +218,19 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _made(stream, make, shape, dtype, device):
+def _made(stream, make, shape, dtype, device, returned=True):
     """make(shape) on ``stream`` (None: the current stream): memory that a call
-    hands to its kernels, and its fill, have to be ordered with them."""
+    hands to its kernels, and its fill, have to be ordered with them.  What is
+    returned to the caller also waits, once freed, for what the caller's
+    stream has queued by then."""
     if stream is None:
         return make(shape, dtype=dtype, device=device)
-    with _torch().cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _dt(plan):
@@ -263,8 +269,8 @@ def base_both(W0_kn, stream=None):
     the weight, then its transpose [d_out][d_in] built by the library."""
     torch = _torch()
     d_in, d_out = W0_kn.shape
+    buf = _made(stream, torch.empty, 2 * d_in * d_out, W0_kn.dtype, W0_kn.device)
     with torch.cuda.stream(stream):     # (None: the current one) the copies too
-        buf = torch.empty(2 * d_in * d_out, dtype=W0_kn.dtype, device=W0_kn.device)
         buf[: d_in * d_out].view(d_in, d_out).copy_(W0_kn)
         mlora_base_transpose(W0_kn.contiguous(), buf[d_in * d_out:], stream)
     return buf
@@ -749,7 +755,7 @@ class ExpertLinear:
             self.dW = _made(stream, torch.empty, sh.w_shape, torch.float32, self.W.device)
         ws = self.ws
         if want_dx and sh.w_format == "mxfp4" and dY.shape[0] > 0:
-            ws = _made(stream, torch.empty, sh.workspace_bytes, torch.uint8, self.W.device)
+            ws = _made(stream, torch.empty, sh.workspace_bytes, torch.uint8, self.W.device, returned=False)
         mlora_expert_backward(sh, dY, X, self.W, offsets, order, dX if want_dx else None,
                               self.dW if want_dw else None, ws, stream)
         return dX if want_dx else None

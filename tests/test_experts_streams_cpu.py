@@ -31,6 +31,9 @@ def made(monkeypatch):
         monkeypatch.setattr(torch, name, run)
 
     stream.at = lambda: at[0]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: ("current", at[0]))
+    # (only what was made on another stream is recorded, with the caller's)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.append(("record", s)))
     monkeypatch.setattr(torch.cuda, "stream", stream)
     watch("zeros")
     watch("empty")
@@ -57,7 +60,8 @@ def test_outputs_are_made_on_the_calls_stream(made, monkeypatch, order, given):
     L.backward(x, x, stream=given)
     fill = "zeros" if order else "empty"
     assert calls == [given, given]
-    assert made == [(fill, given), (fill, given), ("empty", given)]
+    kept = [("record", ("current", None))] if given else []
+    assert made == [(fill, given)] + kept + [(fill, given)] + kept + [("empty", given)] + kept
 
 
 @pytest.mark.parametrize("given", [None, "side"])
@@ -73,7 +77,7 @@ def test_quantizer_buffer_is_made_on_the_calls_stream(made, monkeypatch, given):
     monkeypatch.setattr(b, "_raw_stream", lambda *a: 0)
     monkeypatch.setattr(b, "_launch", lambda *a: None)
     b.mlora_microscale_quantize(Matrix(), stream=given)
-    assert made == [("empty", given)]
+    assert made == [("empty", given)] + ([("record", ("current", None))] if given else [])
 
 
 @pytest.mark.parametrize("given", [None, "side"])
@@ -86,7 +90,8 @@ def test_packed_layer_outputs_are_made_on_the_calls_stream(made, monkeypatch, gi
     x = torch.ones(8, 64, dtype=torch.bfloat16)
     L.forward(x, stream=given)
     L.backward(x, x, stream=given)
-    assert made == [("empty", given)] * 2
+    assert [m for m in made if m[0] != "record"] == [("empty", given)] * 2
+    assert len(made) == (4 if given else 2)
 
 
 def test_two_layout_base_is_copied_on_the_calls_stream(made, monkeypatch):
@@ -97,7 +102,7 @@ def test_two_layout_base_is_copied_on_the_calls_stream(made, monkeypatch):
     monkeypatch.setattr(torch.Tensor, "copy_", lambda t, o: (made.append(("copy", torch.cuda.stream.at())), copy(t, o))[1])
     buf = b.base_both(torch.arange(64 * 64, dtype=torch.float32).view(64, 64), "side")
     assert buf.numel() == 2 * 64 * 64 and at == ["side"]
-    assert made == [("empty", "side"), ("copy", "side")]
+    assert made == [("empty", "side"), ("record", ("current", None)), ("copy", "side")]
 
 
 @pytest.mark.parametrize("given", [None, "side"])

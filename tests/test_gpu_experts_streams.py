@@ -64,3 +64,26 @@ def test_outputs_do_not_take_memory_still_in_use():
         call()
         torch.cuda.synchronize()
         assert (out == 7).all(), name
+
+
+def test_outputs_freed_while_read_are_not_reused():
+    """An output of a call on another stream that the current stream still has to
+    read when it is freed: the next call there makes its own elsewhere."""
+    import torch
+    c = Case([300], 256, 264, layout="nk")
+    L = c.layer()
+    want = L.forward(c.X)
+    other = (c.X * 0.5).contiguous()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y = L.forward(c.X, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        out = torch.empty_like(want)
+        torch.cuda._sleep(SPIN)
+        out.copy_(y)
+        del y
+        L.forward(other, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
