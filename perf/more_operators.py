@@ -195,8 +195,8 @@ def prepare(case, seed):
         x *= torch.exp2(_rand(g, (case["rows"], 1), torch.float32, 1.5))      # rows of different sizes
         s["x"] = x.to(DT[case["dtype"]])
         if own:
-            from adapter_lora_segments_amd import int4_bytes
-            s["q"] = torch.empty(int4_bytes(case["rows"], case["cols"], case["group"]), dtype=torch.uint8,
+            from adapter_lora_segments_amd import affine_bytes
+            s["q"] = torch.empty(affine_bytes(case["rows"], case["cols"], case["group"]), dtype=torch.uint8,
                                  device="cuda")
             s["values"] = torch.empty_like(s["x"])
         return s
@@ -208,8 +208,8 @@ def prepare(case, seed):
     else:
         s["dy"] = _rand(g, (R, do), torch.bfloat16)
     if own:
-        from adapter_lora_segments_amd import Int4Linear
-        s["layer"] = Int4Linear(s["w"], E, di, do, R, group=case["group"], top_k=case["top_k"],
+        from adapter_lora_segments_amd import AffineLinear
+        s["layer"] = AffineLinear(s["w"], E, di, do, R, group=case["group"], top_k=case["top_k"],
                                 x_order=case["x_order"], y_order=case["y_order"])
     return s
 
@@ -405,7 +405,7 @@ def _run_own(s):
         dy, dw = m.mlora_combine_backward(s["dout"], s["y"], c["top_k"], s["ids"], s["weights"])
         return {"dy": dy} if dw is None else {"dy": dy, "dweights": dw}
     if op == "int4_quantize":
-        m.mlora_int4_quantize(s["x"], s["q"], values=s["values"], group=c["group"], symmetric=c["symmetric"])
+        m.mlora_affine_quantize(s["x"], s["q"], values=s["values"], group=c["group"], symmetric=c["symmetric"])
         return {"values": s["values"]}
     if op == "int4_backward":
         return {"dx": s["layer"].backward(s["dy"], s["offsets"], s["order"])}
