@@ -10,5 +10,7 @@ from .binding import (Plan, PackedLoRALinear, AdamW, mlora_plan, mlora_forward, 
                       base_both, mlora_base_transpose, mlora_forward_noalloc,
                       mlora_group_rows, group_rows_workspace, RowGroups, ExpertShape, ExpertLinear,
                       mlora_expert_forward, mlora_expert_backward, mlora_microscale_quantize,
-                      microscale_bytes)
+                      microscale_bytes, Router, mlora_route, mlora_route_backward, mlora_combine,
+                      mlora_combine_backward, affine_bytes, affine_pack, mlora_affine_quantize, AffineShape, AffineLinear,
+                      mlora_affine_forward, mlora_affine_backward)
 from ._lib import MloraError, lib  # noqa: F401

@@ -15,6 +15,8 @@ W0_LAYOUTS = {"kn": 0, "nk": 1, "both": 2}
 W0_FORMATS = {"bf16": 0, "mxfp8": 1, "mxfp4": 2}
 ACT_FORMATS = {"bf16": 0, "mxfp8": 1}
 EXPERT_ACT_FORMATS = {"bf16": 0, "mxfp4": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 WG_OVERLAP = {"auto": 0, "side": 1, "after": 2}
 
 TABLES = ["rpad", "zoff", "roff", "group_first_adapter", "nb", "nb_start", "chunks", "chunk_start",
@@ -33,7 +35,9 @@ EXPORTS = ["mlora_plan", "mlora_plan_from_ids", "mlora_plan_multi", "mlora_plan_
            "mlora_profile_read", "mlora_device_check", "mlora_status_string", "mlora_last_error",
            "mlora_version", "mlora_base_transpose", "mlora_forward_noalloc", "mlora_group_rows_workspace",
            "mlora_group_rows", "mlora_expert_workspace", "mlora_expert_forward_workspace", "mlora_expert_forward", "mlora_expert_backward",
-           "mlora_microscale_quantize"]
+           "mlora_microscale_quantize", "mlora_route", "mlora_route_backward", "mlora_combine",
+           "mlora_combine_backward", "mlora_affine_bytes", "mlora_affine_quantize", "mlora_affine_workspace",
+           "mlora_affine_forward", "mlora_affine_backward"]
 
 
 class PlanOpts(ctypes.Structure):
@@ -70,6 +74,18 @@ class ExpertShape(ctypes.Structure):
                 ("w_format", ctypes.c_int32), ("act_format", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("x_by_order", ctypes.c_int32), ("y_by_order", ctypes.c_int32),
                 ("grad_accumulate", ctypes.c_int32)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("expert_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class AffineShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int64), ("d_out", ctypes.c_int64),
+                ("n_experts", ctypes.c_int32), ("group", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("x_by_order", ctypes.c_int32), ("y_by_order", ctypes.c_int32)]
 
 
 class MloraError(RuntimeError):
@@ -141,6 +157,24 @@ def lib() -> ctypes.CDLL:
     L.mlora_expert_backward.restype = i32
     L.mlora_microscale_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp]
     L.mlora_microscale_quantize.restype = i32
+    L.mlora_route.argtypes = [ctypes.POINTER(Router), vp, i32, i64, i64, vp, vp, vp, vp]
+    L.mlora_route.restype = i32
+    L.mlora_route_backward.argtypes = [ctypes.POINTER(Router), vp, i32, i64, i64, vp, vp, vp, vp]
+    L.mlora_route_backward.restype = i32
+    L.mlora_combine.argtypes = [vp, i32, i64, i32, i64, vp, i32, vp, vp, vp, vp]
+    L.mlora_combine.restype = i32
+    L.mlora_combine_backward.argtypes = [vp, vp, i32, i64, i32, i64, vp, i32, vp, vp, vp, vp]
+    L.mlora_combine_backward.restype = i32
+    L.mlora_affine_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
+    L.mlora_affine_bytes.restype = i32
+    L.mlora_affine_quantize.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp]
+    L.mlora_affine_quantize.restype = i32
+    L.mlora_affine_workspace.argtypes = [ctypes.POINTER(AffineShape), ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    L.mlora_affine_workspace.restype = i32
+    L.mlora_affine_forward.argtypes = [ctypes.POINTER(AffineShape), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mlora_affine_forward.restype = i32
+    L.mlora_affine_backward.argtypes = [ctypes.POINTER(AffineShape), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mlora_affine_backward.restype = i32
     L.mlora_profile_enable.argtypes = [vp, i32]
     L.mlora_profile_enable.restype = i32
     L.mlora_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]

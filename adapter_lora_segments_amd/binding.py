@@ -793,3 +793,324 @@ def mlora_microscale_quantize(X, q=None, values=None, along: str = "cols", strea
             X.stride(0) if rows > 1 else cols, 1 if along == "rows" else 0, q.data_ptr(), _ptr(values),
             _raw_stream(stream, i))
     return q
+
+
+# ---- routing, combining, 4-bit weights with group scales ----
+
+def _logits_of(logits, n_experts):
+    """(rows, ld, dtype number) of a router's logits, rows of contiguous elements."""
+    torch = _torch()
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be a 2-d bf16 or fp32 tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    rows, cols = logits.shape
+    if cols != n_experts:
+        raise ValueError(f"logits must have {n_experts} columns, got {cols}")
+    if logits.stride(1) != 1 and cols > 1:
+        raise ValueError("logits' rows must be contiguous")
+    return rows, logits.stride(0) if rows > 1 else cols, 1 if logits.dtype == torch.bfloat16 else 0
+
+
+class Router:
+    """How rows choose experts (``mlora_router``): score "softmax" or
+    "sigmoid"; with top_groups < expert_groups only the experts of the
+    top_groups best groups, by their "max" score or the sum of their two
+    largest ("top2"); renormalize: the weights of a row sum to ``scale``."""
+
+    def __init__(self, n_experts: int, top_k: int, score: str = "softmax", expert_groups: int = 1,
+                 top_groups: int = 1, group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+        if score not in _lib.SCORES:
+            raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+        if group_score not in _lib.GROUP_SCORES:
+            raise ValueError(f"group_score must be 'max' or 'top2', got {group_score!r}")
+        self.n_experts, self.top_k = int(n_experts), int(top_k)
+        self._c = _lib.Router(self.n_experts, self.top_k, _lib.SCORES[score], int(expert_groups), int(top_groups),
+                              _lib.GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
+        # the library's own checks, on no rows
+        check(lib().mlora_route(ctypes.byref(self._c), None, 1, 0, self.n_experts, None, None, None, None))
+
+    def route(self, logits, bias=None, ids=None, weights=None, stream=None):
+        """ids [rows][top_k] int32 (-1: no expert left) and weights fp32 of
+        logits [rows][n_experts]; bias [n_experts] fp32 enters the choice only.
+        What is not given is made here, on ``stream`` if one is given."""
+        torch = _torch()
+        shape = (logits.shape[0], self.top_k)
+        if ids is None:
+            ids = _made(stream, torch.empty, shape, torch.int32, logits.device)
+        if weights is None:
+            weights = _made(stream, torch.empty, shape, torch.float32, logits.device)
+        return mlora_route(self, logits, bias, ids, weights, stream)
+
+    def backward(self, logits, ids, dweights, dlogits=None, stream=None):
+        """dlogits [rows][n_experts] of the logits' type from the weights'
+        gradients and the ids that ``route`` gave."""
+        torch = _torch()
+        if dlogits is None:
+            dlogits = _made(stream, torch.empty, tuple(logits.shape), logits.dtype, logits.device)
+        return mlora_route_backward(self, logits, ids, dweights, dlogits, stream)
+
+
+def mlora_route(router: Router, logits, bias, ids, weights, stream=None):
+    """A row's top_k experts and their weights (bias may be None)."""
+    torch = _torch()
+    rows, ld, dt = _logits_of(logits, router.n_experts)
+    if bias is not None:
+        _need(bias, "bias", (router.n_experts,), torch.float32)
+    _need(ids, "ids", (rows, router.top_k), torch.int32)
+    _need(weights, "weights", (rows, router.top_k), torch.float32)
+    i = _one_device(logits, bias, ids, weights)
+    _launch(i, lib().mlora_route, ctypes.byref(router._c), logits.data_ptr(), dt, rows, ld, _ptr(bias), ids.data_ptr(),
+            weights.data_ptr(), _raw_stream(stream, i))
+    return ids, weights
+
+
+def mlora_route_backward(router: Router, logits, ids, dweights, dlogits, stream=None):
+    """dlogits (dense) of the weights' gradients; it may be the logits' own memory."""
+    torch = _torch()
+    rows, ld, dt = _logits_of(logits, router.n_experts)
+    _need(ids, "ids", (rows, router.top_k), torch.int32)
+    _need(dweights, "dweights", (rows, router.top_k), torch.float32)
+    _need(dlogits, "dlogits", (rows, router.n_experts), logits.dtype)
+    i = _one_device(logits, ids, dweights, dlogits)
+    _launch(i, lib().mlora_route_backward, ctypes.byref(router._c), logits.data_ptr(), dt, rows, ld, ids.data_ptr(),
+            dweights.data_ptr(), dlogits.data_ptr(), _raw_stream(stream, i))
+    return dlogits
+
+
+def _combine_sizes(Y, top_k, ids, weights):
+    torch = _torch()
+    if Y.dim() != 2 or Y.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("Y must be a 2-d bf16 or fp32 tensor")
+    rows, d = Y.shape
+    if top_k < 1 or rows % top_k:
+        raise ValueError(f"{rows} rows are no multiple of top_k = {top_k}")
+    tokens = rows // top_k
+    _need(Y, "Y", (rows, d), Y.dtype)
+    if ids is not None:
+        _need(ids, "ids", (tokens, top_k), torch.int32)
+    if weights is not None:
+        _need(weights, "weights", (tokens, top_k), torch.float32)
+    return tokens, d, 1 if Y.dtype == torch.bfloat16 else 0
+
+
+def mlora_combine(Y, top_k: int, ids=None, weights=None, add=None, out=None, n_experts: int = 0, stream=None):
+    """out [tokens][d] = add + the sum of a token's top_k rows of Y times their
+    weights (None: ones), over the slots whose id [tokens][top_k] is not
+    negative (and below n_experts, if one is given); rows of other slots are
+    not read.  out may be add; made here, on ``stream`` if one is given, if
+    None."""
+    torch = _torch()
+    tokens, d, dt = _combine_sizes(Y, top_k, ids, weights)
+    if add is not None:
+        _need(add, "add", (tokens, d), Y.dtype)
+    if out is None:
+        out = _made(stream, torch.empty, (tokens, d), Y.dtype, Y.device)
+    _need(out, "out", (tokens, d), Y.dtype)
+    i = _one_device(Y, ids, weights, add, out)
+    _launch(i, lib().mlora_combine, Y.data_ptr(), dt, tokens, top_k, d, _ptr(ids), n_experts, _ptr(weights), _ptr(add),
+            out.data_ptr(), _raw_stream(stream, i))
+    return out
+
+
+def mlora_combine_backward(dout, Y, top_k: int, ids=None, weights=None, dY=None, dweights=None, want_dy=True,
+                           want_dweights=None, n_experts: int = 0, stream=None):
+    """(dY, dweights) of mlora_combine, either None if not wanted (dweights is
+    by default where weights are given); Y may be None without dweights."""
+    torch = _torch()
+    if want_dweights is None:
+        want_dweights = weights is not None
+    if Y is None and want_dweights:
+        raise ValueError("dweights needs Y")
+    if dout.dim() != 2 or dout.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dout must be a 2-d bf16 or fp32 tensor")
+    tokens, d = dout.shape
+    dt = dout.dtype
+    if top_k < 1:
+        raise ValueError(f"top_k must be positive, got {top_k}")
+    _need(dout, "dout", (tokens, d), dt)
+    if Y is not None:
+        _need(Y, "Y", (tokens * top_k, d), dt)
+    if ids is not None:
+        _need(ids, "ids", (tokens, top_k), torch.int32)
+    if weights is not None:
+        _need(weights, "weights", (tokens, top_k), torch.float32)
+    if not want_dy:
+        dY = None
+    elif dY is None:
+        dY = _made(stream, torch.empty, (tokens * top_k, d), dt, dout.device)
+    if not want_dweights:
+        dweights = None
+    elif dweights is None:
+        dweights = _made(stream, torch.empty, (tokens, top_k), torch.float32, dout.device)
+    if dY is not None:
+        _need(dY, "dY", (tokens * top_k, d), dt)
+    if dweights is not None:
+        _need(dweights, "dweights", (tokens, top_k), torch.float32)
+    i = _one_device(dout, Y, ids, weights, dY, dweights)
+    _launch(i, lib().mlora_combine_backward, dout.data_ptr(), _ptr(Y), 1 if dt == torch.bfloat16 else 0, tokens, top_k, d,
+            _ptr(ids), n_experts, _ptr(weights), _ptr(dY), _ptr(dweights), _raw_stream(stream, i))
+    return dY, dweights
+
+
+def affine_bytes(rows: int, cols: int, group: int = 128) -> int:
+    """Bytes of the packed buffer of a [rows][cols] matrix in 4-bit codes."""
+    n = ctypes.c_int64()
+    check(lib().mlora_affine_bytes(rows, cols, group, ctypes.byref(n)))
+    return n.value
+
+
+def affine_pack(codes, scales, zeros=None):
+    """The packed buffer of codes [rows][cols] (0 .. 15, any integer type),
+    scales and zero points [rows][cols / group] (zeros None: 8), rounded to
+    bf16; group is 32, 64 or 128.  For weights that another program quantized;
+    checks the codes' range, so it waits for the device."""
+    torch = _torch()
+    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0] or scales.shape[1] < 1:
+        raise ValueError("codes must be [rows][cols] and scales [rows][cols / group]")
+    rows, cols = codes.shape
+    if cols % scales.shape[1] or cols // scales.shape[1] not in (32, 64, 128):
+        raise ValueError(f"{cols} columns and {scales.shape[1]} scales a row make no group of 32, 64 or 128")
+    zeros = torch.full_like(scales, 8.0) if zeros is None else zeros
+    if zeros.shape != scales.shape:
+        raise ValueError(f"zeros must have shape {tuple(scales.shape)}, got {tuple(zeros.shape)}")
+    if codes.is_floating_point() or rows and (int(codes.min()) < 0 or int(codes.max()) > 15):
+        raise ValueError("codes must be integers from 0 to 15")
+    c = codes.to(torch.uint8)
+    pairs = (c[:, 0::2] | (c[:, 1::2] << 4)).reshape(-1)
+    params = torch.stack([zeros.to(torch.bfloat16), scales.to(torch.bfloat16)], dim=-1).contiguous()
+    return torch.cat([pairs, params.view(torch.uint8).reshape(-1)])
+
+
+def mlora_affine_quantize(X, q=None, values=None, group: int = 128, symmetric: bool = False, stream=None):
+    """X [rows][cols] (bf16 or fp32, rows contiguous) to 4-bit codes with a
+    scale and a zero point per ``group`` elements of a row: q, the packed
+    buffer, made if None (on ``stream`` if one is given).  values: None or a
+    dense tensor like X for the decoded elements."""
+    torch = _torch()
+    if X.dim() != 2 or X.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("X must be a 2-d bf16 or fp32 tensor")
+    if not X.is_cuda:
+        raise ValueError("X must be a device tensor")
+    rows, cols = X.shape
+    if X.stride(1) != 1 and cols > 1:
+        raise ValueError("X's rows must be contiguous")
+    n = affine_bytes(rows, cols, group)
+    if q is None:
+        q = _made(stream, torch.empty, n, torch.uint8, X.device)
+    _need(q, "q", (n,), torch.uint8)
+    if values is not None:
+        _need(values, "values", (rows, cols), X.dtype)
+    i = _one_device(X, q, values)
+    _launch(i, lib().mlora_affine_quantize, X.data_ptr(), 1 if X.dtype == torch.bfloat16 else 0, rows, cols,
+            X.stride(0) if rows > 1 else cols, group, 1 if symmetric else 0, q.data_ptr(), _ptr(values),
+            _raw_stream(stream, i))
+    return q
+
+
+class AffineShape:
+    """Sizes and layouts of a product with 4-bit weights (``mlora_affine_shape``).
+    ``rows`` is the most rows of a call."""
+
+    def __init__(self, rows: int, n_experts: int, d_in: int, d_out: int, group: int = 128, top_k: int = 1,
+                 x_order: bool = False, y_order: bool = False):
+        self.rows, self.n_experts, self.d_in, self.d_out = int(rows), int(n_experts), int(d_in), int(d_out)
+        self.group, self.top_k, self.x_order, self.y_order = int(group), int(top_k), bool(x_order), bool(y_order)
+        self._c = _lib.AffineShape(self.rows, self.d_in, self.d_out, self.n_experts, self.group, self.top_k,
+                                 int(self.x_order), int(self.y_order))
+        f, b = ctypes.c_int64(), ctypes.c_int64()
+        check(lib().mlora_affine_workspace(ctypes.byref(self._c), ctypes.byref(f), ctypes.byref(b)))
+        self.forward_workspace_bytes, self.backward_workspace_bytes = f.value, b.value
+        self.q_shape = (affine_bytes(self.n_experts * self.d_out, self.d_in, self.group),)
+
+    def struct(self, rows: int):
+        """The C structure for a call of ``rows`` rows (never changed once made:
+        a call on another thread may be reading it)."""
+        c = self._c
+        if c.rows != rows:
+            c = _lib.AffineShape.from_buffer_copy(c)
+            c.rows = rows
+            self._c = c
+        return c
+
+    def src_rows(self, rows: int) -> int:
+        return rows // self.top_k if self.x_order else rows
+
+
+def mlora_affine_forward(shape: AffineShape, X, q, offsets, order, Y, ws=None, stream=None):
+    """Y[y(s)] = X[x(s)] W_e^T for every expert e and its grouped rows s (rows
+    of Y that belong to no group are left as they were)."""
+    torch = _torch()
+    rows = Y.shape[0]
+    _need(X, "X", (shape.src_rows(rows), shape.d_in), torch.bfloat16)
+    _need(Y, "Y", (rows, shape.d_out), torch.bfloat16)
+    _need(q, "q", shape.q_shape, torch.uint8)
+    _check_tables(shape, rows, offsets, order, ws)
+    i = _one_device(X, q, offsets, order, Y, ws)
+    _launch(i, lib().mlora_affine_forward, ctypes.byref(shape.struct(rows)), X.data_ptr(), q.data_ptr(), _ptr(offsets),
+            _ptr(order), Y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, i))
+    return Y
+
+
+def mlora_affine_backward(shape: AffineShape, dY, q, offsets, order, dX, ws=None, stream=None):
+    """dX[p(s)] = dY[y(s)] W_e (the weight is frozen)."""
+    torch = _torch()
+    rows = dY.shape[0]
+    _need(dY, "dY", (rows, shape.d_out), torch.bfloat16)
+    _need(dX, "dX", (rows, shape.d_in), torch.bfloat16)
+    _need(q, "q", shape.q_shape, torch.uint8)
+    _check_tables(shape, rows, offsets, order, ws)
+    i = _one_device(dY, q, offsets, order, dX, ws)
+    _launch(i, lib().mlora_affine_backward, ctypes.byref(shape.struct(rows)), dY.data_ptr(), q.data_ptr(), _ptr(offsets),
+            _ptr(order), dX.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, i))
+    return dX
+
+
+class AffineLinear:
+    """A frozen 4-bit weight, or one per expert: ``q`` is the packed buffer of
+    [n_experts * d_out][d_in] (``mlora_affine_quantize``, ``affine_pack``).
+    ``forward`` and ``backward`` take up to ``max_rows`` grouped rows, as those
+    of ``ExpertLinear``.  Nothing is kept beside ``q``: workspaces (a decoded
+    weight, 2 bytes each) come from torch's allocator for the call, so calls may
+    overlap.  A call given a ``stream`` runs there, and what it makes is made
+    there: the stream has to wait for the inputs, and a reader on another stream
+    for the results."""
+
+    def __init__(self, q, n_experts: int, d_in: int, d_out: int, max_rows: int, **options):
+        torch = _torch()
+        self.shape = AffineShape(max_rows, n_experts, d_in, d_out, **options)
+        _need(q, "q", self.shape.q_shape, torch.uint8)
+        self.q = q
+
+    def _workspace(self, need, stream):
+        torch = _torch()
+        return _made(stream, torch.empty, need, torch.uint8, self.q.device, returned=False) if need else None
+
+    def _need_of(self, rows, which):
+        """Workspace bytes of a call of ``rows`` rows."""
+        f, b = ctypes.c_int64(), ctypes.c_int64()
+        check(lib().mlora_affine_workspace(ctypes.byref(self.shape.struct(rows)), ctypes.byref(f), ctypes.byref(b)))
+        return (f, b)[which].value
+
+    def forward(self, X, offsets=None, order=None, Y=None, stream=None):
+        """Y [rows][d_out]; a Y made here is zero in rows of no group when an
+        order names the rows."""
+        torch = _torch()
+        sh = self.shape
+        if Y is None:
+            rows = X.shape[0] * sh.top_k if sh.x_order else X.shape[0]
+            make = torch.zeros if sh.y_order else torch.empty
+            Y = _made(stream, make, (rows, sh.d_out), X.dtype, X.device)
+        need = self._need_of(Y.shape[0], 0) if sh.forward_workspace_bytes else 0
+        return mlora_affine_forward(sh, X, self.q, offsets, order, Y, self._workspace(need, stream), stream)
+
+    def backward(self, dY, offsets=None, order=None, dX=None, stream=None):
+        """dX [rows][d_in]; a dX made here is zero in rows of no group when an
+        order names the rows."""
+        torch = _torch()
+        sh = self.shape
+        if dX is None:
+            make = torch.zeros if sh.x_order else torch.empty
+            dX = _made(stream, make, (dY.shape[0], sh.d_in), dY.dtype, dY.device)
+        ws = self._workspace(sh.backward_workspace_bytes if dY.shape[0] > 0 else 0, stream)
+        return mlora_affine_backward(sh, dY, self.q, offsets, order, dX, ws, stream)

@@ -621,6 +621,155 @@ mlora_status mlora_expert_backward(const mlora_expert_shape *shape, const void *
 mlora_status mlora_microscale_quantize(const void *X, mlora_dtype dtype, int64_t rows, int64_t cols,
                                        int64_t ld, int32_t down, void *q, void *values, void *stream);
 
+/*
+ * Routing: which experts a row goes to, from its router logits.
+ *
+ * Per row, over the experts e:
+ *   s_e = softmax(logits)_e or 1 / (1 + e^-logit_e), computed in 64 bits and
+ *         rounded to fp32;  c_e = s_e + bias_e in fp32 (bias NULL: c_e = s_e)
+ * With top_groups < expert_groups the experts, in expert_groups equal runs,
+ * are first narrowed to the top_groups groups of the highest group score:
+ * the largest c of the group (MLORA_GROUP_MAX) or the sum of its two largest
+ * (MLORA_GROUP_TOP2; the largest alone if one expert only can be chosen),
+ * equal scores to the lowest group.  ids [rows][top_k]: the experts of the
+ * largest c, falling, equal values to the lowest expert.  weights [rows]
+ * [top_k] fp32: scale s, or with renormalize scale s / (sum of the chosen s)
+ * (from the 64-bit scores; a sum of 0 divides by 1).  The bias enters the
+ * choice only.
+ *
+ * An expert whose logit or c is -infinity is never chosen (a mask, a row of
+ * padding); slots with no expert left have id -1 and weight 0, which
+ * mlora_group_rows and mlora_combine drop.  A NaN is chosen first, so that it
+ * reaches the weights; a NaN or +infinity among softmax logits makes all of
+ * the row's scores NaN.
+ */
+typedef enum { MLORA_SCORE_SOFTMAX = 0, MLORA_SCORE_SIGMOID = 1 } mlora_score;
+typedef enum { MLORA_GROUP_MAX = 0, MLORA_GROUP_TOP2 = 1 } mlora_group_score;
+typedef struct {
+  int32_t n_experts;     /* 1 .. MLORA_MAX_EXPERTS */
+  int32_t top_k;         /* 1 .. 64, at most the experts of top_groups groups */
+  int32_t score;         /* mlora_score */
+  int32_t expert_groups; /* 1 .. 64, a divisor of n_experts */
+  int32_t top_groups;    /* 1 .. expert_groups */
+  int32_t group_score;   /* mlora_group_score */
+  int32_t renormalize;   /* 0 or 1 */
+  float scale;
+} mlora_router;
+
+/* logits: bf16 or fp32, row r starting at element r * ld (ld >= n_experts),
+ * aligned to an element.  0 <= rows < 2^31; MLORA_ERR_UNSUPPORTED for more
+ * rows than a launch takes (2^26 - 4; 2^24 - 1 over 1024 experts).  One kernel
+ * on `stream`; with rows = 0 nothing is launched.  Results do not depend on
+ * the other rows of a call. */
+mlora_status mlora_route(const mlora_router *router, const void *logits, mlora_dtype dtype, int64_t rows,
+                         int64_t ld, const float *bias, int32_t *ids, float *weights, void *stream);
+
+/* dlogits [rows][n_experts], dense, of the logits' type: the gradient of the
+ * weights of the experts in ids, dweights [rows][top_k].  The choice has no
+ * gradient, and neither has the bias.  With u_j the score of slot j:
+ *   du_j = scale dweights_j, or renormalized scale (dweights_j - sum_m
+ *          dweights_m u_m / S) / S, S = sum_m u_m
+ *   softmax: dlogit_e = s_e (du_e - sum_j du_j u_j)
+ *   sigmoid: dlogit_e = s_e (1 - s_e) du_e
+ * where du_e is the sum over the slots of e.  Slots whose id names no expert
+ * have no part.  An expert at -infinity gets 0.  dlogits may be the logits
+ * themselves when ld = n_experts. */
+mlora_status mlora_route_backward(const mlora_router *router, const void *logits, mlora_dtype dtype,
+                                  int64_t rows, int64_t ld, const int32_t *ids, const float *dweights,
+                                  void *dlogits, void *stream);
+
+/*
+ * mlora_combine -- the expert rows of a token summed into its row:
+ *   out_t = add_t + sum_j weights_tj Y[t top_k + j]
+ * over the slots j whose id counts.  Y [tokens * top_k][d], rows in the order
+ * of the ids (an expert product with y_by_order writes it); ids [tokens]
+ * [top_k] or NULL (every slot counts); a slot counts if its id is in [0,
+ * n_experts), or with n_experts = 0 if it is not negative.  The row of a slot
+ * that does not count is not read.  weights [tokens][top_k] fp32 or NULL
+ * (ones: the sum of a token's gradients dX).  add [tokens][d] or NULL; it may
+ * be out.  bf16 or fp32, sums in fp32 in slot order, then add, one rounding.
+ * d: a multiple of 8 (bf16) or 4 (fp32), at most MLORA_MAX_EXPERT_DIM;
+ * 1 <= top_k <= 64; tokens * top_k < 2^31, and MLORA_ERR_UNSUPPORTED for more
+ * tokens than a launch takes (2^24 - 1 pieces of 2048 (bf16) or 1024 (fp32)
+ * columns).  Y, add, out 16-byte aligned; out must not overlap Y.
+ *
+ * mlora_combine_backward -- its gradients: dY [tokens * top_k][d] = weights_tj
+ * dout_t (zero in slots that do not count) and dweights_tj = <dout_t,
+ * Y[t top_k + j]> in fp32, a fixed order (0 in those slots); either may be
+ * NULL.  Y may be NULL without dweights.  The gradient of add is dout itself.
+ */
+mlora_status mlora_combine(const void *Y, mlora_dtype dtype, int64_t tokens, int32_t top_k, int64_t d,
+                           const int32_t *ids, int32_t n_experts, const float *weights, const void *add,
+                           void *out, void *stream);
+mlora_status mlora_combine_backward(const void *dout, const void *Y, mlora_dtype dtype, int64_t tokens,
+                                    int32_t top_k, int64_t d, const int32_t *ids, int32_t n_experts,
+                                    const float *weights, void *dY, float *dweights, void *stream);
+
+/*
+ * 4-bit weights with a scale and a zero point per group of inputs.
+ *
+ * A [rows][cols] matrix (a [d_out][d_in] weight, all experts' one after the
+ * other) as one buffer of mlora_affine_bytes bytes: rows * cols / 2 code bytes
+ * [rows][cols / 2], two codes of 0 .. 15 a byte along a row, the even element
+ * in the low four bits; then [rows][cols / group] pairs of bf16, the zero
+ * point z and the scale s of `group` (32, 64 or 128) consecutive elements of a
+ * row.  An element is s (c - z).  Any z and s are taken (z whole or not), so
+ * symmetric codes (z = 8) and those of other quantizers can be packed as well.
+ *
+ * mlora_affine_quantize -- X [rows][cols], bf16 or fp32, row r starting at
+ * element r * ld, to such a buffer, by rounding to nearest, ties to even, in
+ * fp32 steps.  With lo = min(0, the group's smallest) and hi = max(0, its
+ * largest): s = bf16(hi / 15 - lo / 15), z = round(-lo / s) clamped to 0 .. 15;
+ * symmetric = 1: s = bf16(max|x| / 7), z = 8.  c = round(x / s) + z clamped to
+ * 0 .. 15.  Where s is 0 all values are 0.  A group that holds a NaN or an
+ * infinity gets s = NaN, z = 0, c = 0.  values: NULL or [rows][cols] dense of
+ * X's type, s (c - z) (exact in fp32, rounded in bf16).  q and values must not
+ * overlap X or each other; X, q, values 16-byte aligned, ld a multiple of 8
+ * (bf16) or 4 (fp32), cols of group.  One kernel.
+ */
+mlora_status mlora_affine_bytes(int64_t rows, int64_t cols, int32_t group, int64_t *bytes);
+mlora_status mlora_affine_quantize(const void *X, mlora_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 int32_t group, int32_t symmetric, void *q, void *values, void *stream);
+
+/*
+ * Products over such weights, bf16 activations, one weight or one per expert:
+ *   forward :  Y[y(s)]  = X[x(s)] W_e^T      W_e [d_out][d_in]
+ *   backward:  dX[p(s)] = dY[y(s)] W_e       (the weight is frozen)
+ * offsets, order, x_by_order, y_by_order and top_k as in mlora_expert_shape,
+ * also in which rows are left as they were.  Sums in fp32, one rounding at the
+ * end.  Over few rows a group the codes are multiplied as they are, the scales
+ * in fp32: the weights are not rounded (activations whose sums over a group
+ * pass fp32's range, or that are not finite, make NaN).  Over more rows and in
+ * the backward the weights are rounded to bf16 first, as the matrix cores take
+ * them.
+ */
+typedef struct {
+  int64_t rows;            /* grouped rows, 0 <= rows < 2^31, a multiple of top_k */
+  int64_t d_in, d_out;     /* multiples of group and of 8, at most MLORA_MAX_EXPERT_DIM */
+  int32_t n_experts;       /* 1 .. MLORA_MAX_EXPERTS */
+  int32_t group;           /* 32, 64 or 128 */
+  int32_t top_k;           /* 1 .. 64 */
+  int32_t x_by_order;
+  int32_t y_by_order;
+} mlora_affine_shape;
+
+/* Workspaces of forward and backward for this shape or one with fewer rows
+ * (either pointer may be NULL).  Nothing in them has to be kept between calls;
+ * calls that may overlap (streams, host threads, replays of captured graphs)
+ * need one each. */
+mlora_status mlora_affine_workspace(const mlora_affine_shape *shape, int64_t *forward, int64_t *backward);
+
+/* Pointers 16-byte aligned (offsets and order: 4-byte); offsets may be NULL
+ * with one expert, order without x_by_order and y_by_order.  Kernels only, on
+ * `stream`: a call can be captured into a graph.  With rows = 0 nothing is
+ * launched. */
+mlora_status mlora_affine_forward(const mlora_affine_shape *shape, const void *X, const void *q,
+                                const int32_t *offsets, const int32_t *order, void *Y, void *workspace,
+                                size_t ws_bytes, void *stream);
+mlora_status mlora_affine_backward(const mlora_affine_shape *shape, const void *dY, const void *q,
+                                 const int32_t *offsets, const int32_t *order, void *dX, void *workspace,
+                                 size_t ws_bytes, void *stream);
+
 /* Per-kernel timing.  Launches of the selected kinds are bracketed by HIP
  * events on the stream they run on; mlora_profile_read waits for them, adds
  * their durations to the totals of kernel `kind` and returns them, then
