@@ -25,7 +25,7 @@ PROBES_LIB = os.path.join(PKG, "libmlora_probes.so")
 SOURCES = ["plan.cpp", "api.cpp", "kernels_bf16.hip", "kernels_gemm.hip", "kernels_gemm_mx.hip", "kernels_fp32.hip", "kernels_adamw.hip",
            "kernels_mx.hip", "scratch.hip", "api_experts.cpp", "kernels_group_rows.hip", "kernels_microscale.hip",
            "kernels_expert.hip", "kernels_expert_few.hip",
-           "api_route.cpp", "kernels_route.hip", "kernels_combine.hip", "api_affine.cpp", "kernels_affine.hip"]
+           "api_route.cpp", "kernels_route.hip", "kernels_combine.hip", "api_affine.cpp", "kernels_affine.hip", "kernels_affine_tile.hip"]
 # measured-ceiling probes (include/mlora_probes.h), a library of their own
 PROBE_SOURCES = ["probes.hip"]
 

@@ -21,8 +21,9 @@ void launch_affine_quantize(bool f32, const void* X, int64_t rows, int64_t cols,
 void launch_affine_decode(const uint8_t* codes, const uint32_t* params, int64_t rows, int64_t cols, int32_t group,
                         uint16_t* out, hipStream_t s);
 
-// Rows form over few rows a group: a.B the codes, a.b_expert their bytes per
-// expert, a.b_scale the parameters.
-void launch_affine_few(const ExpertArgs& a, int32_t group, hipStream_t s);
+// Rows form: a.B the codes, a.b_expert their bytes per expert, a.b_scale the
+// parameters; one of the tiles that affine_choice.hpp chooses from.
+void launch_affine_few(const ExpertArgs& a, int32_t group, int rows, int cols, hipStream_t s);
+void launch_affine_tile(const ExpertArgs& a, int32_t group, int rows, int parts, hipStream_t s);
 
 }  // namespace mlora

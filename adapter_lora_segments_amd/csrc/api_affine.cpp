@@ -34,11 +34,11 @@ const char* shape_error(const mlora_affine_shape* s, mlora_status* st) {
   if (s->top_k > 1 && !s->x_by_order) return "affine: top_k > 1 needs x_by_order";
   *st = MLORA_ERR_UNSUPPORTED;
   if (s->d_in > MLORA_MAX_EXPERT_DIM || s->d_out > MLORA_MAX_EXPERT_DIM) return "affine: d_in and d_out are at most 2^20";
-  // launch bounds: tiles of 256 x 256 of the decoded products, of 16 x 16 over few
-  // rows, a lane per eight decoded weights
-  const int64_t d = (s->d_in > s->d_out ? s->d_in : s->d_out) + 255;
+  // launch bounds: tiles of 128 x 128 (larger ones of the decoded products, smaller
+  // ones where they fit; few rows a group: 32 x 128), a lane per eight decoded weights
+  const int64_t d = (s->d_in > s->d_out ? s->d_in : s->d_out) + 127;
   const int64_t groups = s->n_experts < s->rows ? s->n_experts : s->rows;
-  if (s->rows / 256 + groups > kMaxGrid / (d / 256) || s->n_experts * s->d_out > kMaxGrid * 256 / (s->d_in / 8))
+  if (s->rows / 128 + 2 * groups > kMaxGrid / (d / 128) || s->n_experts * s->d_out > kMaxGrid * 256 / (s->d_in / 8))
     return "affine: too many tiles for one launch";
   *st = MLORA_OK;
   return nullptr;
@@ -67,14 +67,9 @@ mlora::ExpertArgs forward_args(const mlora_affine_shape& s, const int32_t* offse
 
 int64_t weights_of(const mlora_affine_shape& s) { return (int64_t)s.n_experts * s.d_in * s.d_out; }
 
-// Whether a forward takes the codes as they are.  (One expert without offsets
-// counts as one group either way.)
-bool takes_codes(const mlora_affine_shape& s) {
-  mlora::ExpertArgs a = forward_args(s, nullptr, nullptr);
-  const int32_t one = 0;
-  a.offsets = &one;
-  return mlora::affine_few_rows(a) <= mlora::kAffineFew && mlora::rows_grid_of(a, 16, 32) <= kMaxGrid;
-}
+// Whether a forward decodes the weights into the workspace first.  A call of
+// fewer rows does not unless this one does.
+bool decodes(const mlora_affine_shape& s) { return s.rows >= mlora::kAffineDecoded * s.n_experts; }
 
 mlora_status check_call(const mlora_affine_shape& s, const int32_t* offsets, const int32_t* order, void* ws,
                         size_t ws_bytes, int64_t need) {
@@ -140,7 +135,7 @@ mlora_status mlora_affine_workspace(const mlora_affine_shape* shape, int64_t* fo
   mlora_status st;
   if (const char* msg = shape_error(shape, &st)) return api_fail(st, msg);
   // the decoded weight; of a forward of fewer rows no more
-  if (forward) *forward = takes_codes(*shape) ? 0 : 2 * weights_of(*shape);
+  if (forward) *forward = decodes(*shape) ? 2 * weights_of(*shape) : 0;
   if (backward) *backward = shape->rows > 0 ? 2 * weights_of(*shape) : 0;
   return MLORA_OK;
 }
@@ -150,7 +145,7 @@ mlora_status mlora_affine_forward(const mlora_affine_shape* shape, const void* X
   mlora_status st;
   if (const char* msg = shape_error(shape, &st)) return api_fail(st, msg);
   const mlora_affine_shape& s = *shape;
-  const bool codes = takes_codes(s);
+  const bool codes = !decodes(s);
   st = check_call(s, offsets, order, workspace, ws_bytes, s.rows > 0 && !codes ? 2 * weights_of(s) : 0);
   if (st != MLORA_OK) return st;
   if (!q || (s.rows > 0 && (!X || !Y))) return api_fail(MLORA_ERR_INVALID_ARG, "affine forward: X, q and Y must be non-NULL");
@@ -166,7 +161,9 @@ mlora_status mlora_affine_forward(const mlora_affine_shape* shape, const void* X
     a.B = w;
     a.b_expert = s.d_in * s.d_out / 2;
     a.b_scale = w + mlora::affine_code_bytes(s.n_experts * s.d_out, s.d_in);
-    mlora::launch_affine_few(a, s.group, cs);
+    const mlora::AffineChoice& c = mlora::affine_choose(a, s.group);
+    if (c.few) mlora::launch_affine_few(a, s.group, c.rows, c.cols, cs);
+    else mlora::launch_affine_tile(a, s.group, c.rows, c.split, cs);
   } else {
     st = decode(s, w, workspace, cs);
     if (st != MLORA_OK) return st;

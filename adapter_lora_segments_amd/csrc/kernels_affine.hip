@@ -152,41 +152,48 @@ __global__ __launch_bounds__(256) void k_affine_decode(const uint32_t* codes, co
   out[i] = o;
 }
 
-// Few rows per group: every weight is read once.  As in the bf16 product, a
-// workgroup of eight waves owns 16 MB rows and 16 NB columns, its waves share
-// the reduction, 512 inputs a wave and pass, and their sums meet in LDS in
-// wave order.  Lane l = c + 16 g: the first matrix operand is row c of the
-// activations, the second column c of the weights, inputs 8 g .. 8 g + 7 of
-// the step's 32, and the lane holds rows 4 g .. 4 g + 3 of its column, so a
-// group's scale and zero point are the lane's own.  Rows past the tile's are
-// not loaded.  Codes come 16 bytes a lane, 32 neighbours of a column; with
-// groups under 128 the words are exchanged between the lane groups, so that a
-// step's 32 inputs lie in one group.
-template <int GROUP, int MB, int NB>
-__global__ __launch_bounds__(512) void k_affine_few(ExpertArgs a) {
-  constexpr int COLS = 16 * NB, NW = 8, BM = 16 * MB, PG = 128 / GROUP, SG = GROUP / 32;
-  __shared__ float sums[NW][BM][COLS + 4];
-  const int nN = (a.N + COLS - 1) / COLS;
-  const RowTile t = RowTiles<BM, 1>(a, nN).at(a, blockIdx.x);
-  if (t.mrows <= 0) return;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
-  const int n0 = t.tn * COLS, K = a.K;
+// Few rows per group: every weight is read once, so what counts is bytes in
+// flight.  A workgroup of eight waves owns up to RB rows and 16 NB CS columns:
+// CS waves side by side, and 8 / CS that share the reduction, neighbouring
+// pieces of 128 inputs each, whose sums meet in LDS in their order.  A wave asks
+// for activations and then for four pieces of weights (16 bytes a lane: 32
+// neighbouring codes of a column), and multiplies when both are there; the
+// activations wait in LDS, 512 inputs of every row, since the registers hold the
+// weights in flight.
+// Lane l = c + 16 g: the first matrix operand is row c of the activations, the
+// second column c of the weights, and the lane holds rows 4 g .. 4 g + 3 of its
+// column, so a group's scale and zero point are the lane's own.  With groups
+// under 128 the words of a piece are exchanged between the lane groups, so that
+// a step's 32 inputs lie in one group.
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
-  const uint8_t* xp[MB];
-  bool mine[MB];
+template <int GROUP, int RB, int NB, int CS>
+__global__ __launch_bounds__(512, RB <= 8 ? 4 : 2) void k_affine_few(ExpertArgs a) {
+  constexpr int KS = 8 / CS, COLS = 16 * NB * CS, MB = RB > 16 ? RB / 16 : 1;
+  constexpr int PG = 128 / GROUP, SG = GROUP / 32, XR = 1024 + 16;
+  constexpr int XB = KS * RB * XR, SB = KS * RB * (COLS + 4) * 4;
+  __shared__ u32x4 lds[(XB > SB ? XB : SB) / 16];
+  const int nN = (a.N + COLS - 1) / COLS;
+  const RowTile t = RowTiles<RB, 1>(a, nN).at(a, blockIdx.x);
+  if (t.mrows <= 0) return;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
+  const int ks = w / CS, cs = w % CS, n0 = t.tn * COLS, K = a.K;
+
+  // a wave's pieces
+  const int pieces = (K + 127) / 128, share = (pieces + KS - 1) / KS;
+  const int kend = min(K, (ks + 1) * share * 128);
+  // codes and parameters by 32-bit offsets from the tile's first column
+  const uint8_t* const wt = a.B + (int64_t)t.e * a.b_expert + (int64_t)n0 * (K / 2);
+  const uint8_t* const pt = a.b_scale + ((int64_t)t.e * a.N + n0) * (K / GROUP) * 4;
+  uint32_t col[NB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    mine[m] = 16 * m + c < t.mrows;
-    xp[m] = a.A + source_row(a, a.ma, t.row0 + min(16 * m + c, t.mrows - 1)) * a.lda * 2;
-  }
-  const uint8_t* wp[NB];
-  const uint32_t* pp[NB];
+  for (int j = 0; j < NB; ++j) col[j] = (uint32_t)min(16 * NB * cs + 16 * j + c, a.N - 1 - n0);
+  // activations: the waves of a part of the reduction copy its rows in turn, lane l a row's 16 bytes l
+  constexpr int XC = RB / CS;
+  const uint8_t* xp[XC];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int col = min(n0 + 16 * j + c, a.N - 1);
-    wp[j] = a.B + (int64_t)t.e * a.b_expert + (int64_t)col * (K / 2);
-    pp[j] = reinterpret_cast<const uint32_t*>(a.b_scale) + ((int64_t)t.e * a.N + col) * (K / GROUP);
-  }
+  for (int r = 0; r < XC; ++r) xp[r] = a.A + source_row(a, a.ma, t.row0 + min(CS * r + cs, t.mrows - 1)) * a.lda * 2;
+  char* const xw = reinterpret_cast<char*>(lds) + ks * RB * XR;
 
   f32x4 acc[MB][NB];
 #pragma unroll
@@ -195,46 +202,57 @@ __global__ __launch_bounds__(512) void k_affine_few(ExpertArgs a) {
     for (int j = 0; j < NB; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const u32x4 ones = {kOnes, kOnes, kOnes, kOnes};
 
-  for (int k0 = 512 * w; k0 < K; k0 += 512 * NW) {
-    u32x4 cw[NB][4];
-    uint32_t pw[NB][4][PG];
+  for (int i0 = 0; i0 < share; i0 += 4) {
+    const int k0 = (ks * share + i0) * 128;
+    u32x4 xv[XC], cw[NB][4];
+    uint32_t pw[NB][4 * PG];
+    {
+      const int k = k0 + 8 * lane, kk = k < K ? k : 0;
+#pragma unroll
+      for (int r = 0; r < XC; ++r) xv[r] = *reinterpret_cast<const u32x4*>(xp[r] + (int64_t)kk * 2);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (K is a multiple of 32: a lane's 32 codes are all in or all out; those out are read
-      // from the row's start and their steps left out)
+      // from the column's start and their steps left out)
       const int kc = k0 + 128 * i + 32 * g, kk = kc < K ? kc : 0;
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        cw[j][i] = *reinterpret_cast<const u32x4*>(wp[j] + kk / 2);
+      for (int j = 0; j < NB; ++j)
+        cw[j][i] = *reinterpret_cast<const u32x4*>(wt + (col[j] * (uint32_t)(K / 2) + (uint32_t)kk / 2));
+    }
+    if (k0 + 512 <= K) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int q = 0; q < PG; ++q) {
-          const int kp = k0 + 128 * i + GROUP * q;
-          pw[j][i][q] = pp[j][kp < K ? kp / GROUP : 0];
+          const u32x4 v = *reinterpret_cast<const u32x4_a4*>(pt + (col[j] * (uint32_t)(K / GROUP) + (uint32_t)(k0 / GROUP + 4 * q)) * 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) pw[j][4 * q + x] = v[x];
         }
-      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4 * PG; ++q) {
+          const int kp = k0 + GROUP * q, kk = kp < K ? kp : 0;
+          pw[j][q] = *reinterpret_cast<const uint32_t*>(pt + (col[j] * (uint32_t)(K / GROUP) + (uint32_t)kk / GROUP) * 4);
+        }
     }
-    u32x4 xv[MB][4][4];
+    // (CS = 1: in the wave's own LDS, and a wave's accesses run in order)
+    if (CS > 1 && i0 > 0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // GROUP 128: any order of the piece's inputs will do, so the codes stay where they are
-        const int k = k0 + 128 * i + (PG == 1 ? 32 * g + 8 * q : 32 * q + 8 * g);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-          xv[m][i][q] = zero4();
-          if (mine[m] && k < K) xv[m][i][q] = *reinterpret_cast<const u32x4*>(xp[m] + (int64_t)k * 2);
-        }
-      }
+    for (int r = 0; r < XC; ++r) *reinterpret_cast<u32x4*>(xw + (CS * r + cs) * XR + 16 * lane) = code_order(xv[r]);
+    if (CS > 1) __syncthreads();
+    else __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (k0 + 128 * i >= K) break;
+      if (k0 + 128 * i >= kend) break;
       u32x4 cc[NB];
 #pragma unroll
       for (int j = 0; j < NB; ++j) cc[j] = PG == 1 ? cw[j][i] : transpose_groups(cw[j][i]);
 #pragma unroll
       for (int p = 0; p < PG; ++p) {
-        if (k0 + 128 * i + GROUP * p >= K) break;
+        if (k0 + 128 * i + GROUP * p >= kend) break;
         f32x4 xs[MB], ps[MB][NB];
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
@@ -244,23 +262,26 @@ __global__ __launch_bounds__(512) void k_affine_few(ExpertArgs a) {
         }
 #pragma unroll
         for (int q = p * SG; q < (p + 1) * SG; ++q) {
-          u32x4 xo[MB];
+          // GROUP 128: any order of the piece's inputs will do, so the codes stay where they are
+          u32x4 x[MB];
 #pragma unroll
           for (int m = 0; m < MB; ++m) {
-            xo[m] = code_order(xv[m][i][q]);
-            xs[m] = mfma16(xo[m], ones, xs[m]);
+            x[m] = *reinterpret_cast<const u32x4*>(xw + (16 * m + min(c, RB - 1)) * XR + 256 * i +
+                                                   (PG == 1 ? 64 * g + 16 * q : 64 * q + 16 * g));
+            xs[m] = mfma16(x[m], ones, xs[m]);
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             const u32x4 wv = bf16_of_codes(cc[j][q]);
 #pragma unroll
-            for (int m = 0; m < MB; ++m) ps[m][j] = mfma16(xo[m], wv, ps[m][j]);
+            for (int m = 0; m < MB; ++m) ps[m][j] = mfma16(x[m], wv, ps[m][j]);
           }
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const float s = __uint_as_float(pw[j][i][p] & 0xffff0000u) * 128.f;
-          const float z = -1.f - __uint_as_float(pw[j][i][p] << 16) * (1.f / 128.f);
+          const uint32_t pj = pw[j][PG * i + p];
+          const float s = __uint_as_float(pj & 0xffff0000u) * 128.f;
+          const float z = -1.f - __uint_as_float(pj << 16) * (1.f / 128.f);
 #pragma unroll
           for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -268,24 +289,29 @@ __global__ __launch_bounds__(512) void k_affine_few(ExpertArgs a) {
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 
-  // acc[m][j][e]: row 16 m + 4 g + e, column 16 j + c
+  // acc[m][j][e]: row 16 m + 4 g + e, column 16 NB cs + 16 j + c
+  __syncthreads();
+  typedef float Sums[RB][COLS + 4];
+  Sums* const sums = reinterpret_cast<Sums*>(lds);
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) sums[w][16 * m + 4 * g + e][16 * j + c] = acc[m][j][e];
+      for (int j = 0; j < NB; ++j)
+        if (4 * g + e < RB) sums[ks][16 * m + 4 * g + e][16 * NB * cs + 16 * j + c] = acc[m][j][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < BM * COLS / 4; i += 512) {
+  for (int i = threadIdx.x; i < RB * COLS / 4; i += 512) {
     const int m = i / (COLS / 4), cc = 4 * (i % (COLS / 4));
     if (m >= t.mrows || n0 + cc >= a.N) continue;
     const int s = t.row0 + m, v = a.mc.by_order ? a.order[s] : s;
     if ((unsigned)v >= (unsigned)a.rows) continue;
     f32x4 sum = *reinterpret_cast<const f32x4*>(&sums[0][m][cc]);
 #pragma unroll
-    for (int q = 1; q < NW; ++q) sum += *reinterpret_cast<const f32x4*>(&sums[q][m][cc]);
+    for (int q = 1; q < KS; ++q) sum += *reinterpret_cast<const f32x4*>(&sums[q][m][cc]);
     const u32x2 o = {pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.C) + (int64_t)v * a.ldc + n0 + cc) = o;
   }
@@ -307,13 +333,13 @@ void quantize_of(const void* X, int64_t rows, int64_t cols, int64_t ld, int32_t 
   else go(k_affine_quantize<T, 128>);
 }
 
-template <int MB, int NB>
+template <int RB, int NB, int CS>
 void few_of(const ExpertArgs& a, int32_t group, hipStream_t s) {
-  const unsigned grid = (unsigned)rows_grid_of(a, 16 * MB, 16 * NB);
+  const unsigned grid = (unsigned)affine_grid(a, RB, 16 * NB * CS);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(512), 0, s, a); };
-  if (group == 32) go(k_affine_few<32, MB, NB>);
-  else if (group == 64) go(k_affine_few<64, MB, NB>);
-  else go(k_affine_few<128, MB, NB>);
+  if (group == 32) go(k_affine_few<32, RB, NB, CS>);
+  else if (group == 64) go(k_affine_few<64, RB, NB, CS>);
+  else go(k_affine_few<128, RB, NB, CS>);
 }
 
 }  // namespace
@@ -337,9 +363,14 @@ void launch_affine_decode(const uint8_t* codes, const uint32_t* params, int64_t 
   else go(k_affine_decode<128>);
 }
 
-void launch_affine_few(const ExpertArgs& a, int32_t group, hipStream_t s) {
-  if (affine_few_rows(a) <= 16) few_of<1, 2>(a, group, s);
-  else few_of<2, 2>(a, group, s);
+void launch_affine_few(const ExpertArgs& a, int32_t group, int rows, int cols, hipStream_t s) {
+  if (rows == 4) return few_of<4, 1, 1>(a, group, s);
+  if (rows == 8) return cols == 16 ? few_of<8, 1, 1>(a, group, s) : few_of<8, 2, 1>(a, group, s);
+  if (rows == 16 && cols == 16) return few_of<16, 1, 1>(a, group, s);
+  if (rows == 16) return cols == 32 ? few_of<16, 1, 2>(a, group, s) : few_of<16, 2, 2>(a, group, s);
+  if (cols == 32) return few_of<32, 1, 2>(a, group, s);
+  if (cols == 64) return few_of<32, 2, 2>(a, group, s);
+  few_of<32, 2, 4>(a, group, s);
 }
 
 }  // namespace mlora

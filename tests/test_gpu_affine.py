@@ -59,7 +59,9 @@ class Case:
         from adapter_lora_segments_amd import AffineLinear
         return AffineLinear(self.q, self.E, self.di, self.do, rows or self.rows, group=self.group, **self.kw)
 
-    def check_y(self, Y, codes, tables=True):
+    def check_y(self, Y, codes=None):
+        if codes is None:                             # at most 16 rows a group: the codes as they are
+            codes = self.rows <= 16 * min(self.E, self.rows)
         want, S, owned = ox.forward(self.Xh, self.W, self.off, self.order, self.rows, **self.kw)
         if codes:
             _, B, _ = ox.forward(self.Xh, self.M, self.off, self.order, self.rows, **self.kw)
@@ -97,7 +99,7 @@ def test_products(sizes, group, di):
         L = c.layer()
         Y = torch.full((c.rows, do), 7.5, dtype=torch.bfloat16, device="cuda")
         L.forward(c.X, c.d_off, c.d_order, Y)
-        owned = c.check_y(Y, L.shape.forward_workspace_bytes == 0)
+        owned = c.check_y(Y)
         assert (Y[torch.from_numpy(~owned).cuda()] == 7.5).all(), "rows of no group were written"
         dX = torch.full((c.rows, di), 7.5, dtype=torch.bfloat16, device="cuda")
         L.backward(c.dY, c.d_off, c.d_order, dX)
@@ -112,14 +114,14 @@ def test_one_weight(rows, group):
     say(f"affine one weight {rows} {group}")
     c = Case([rows], 512 + group, 1032, group, seed=rows)
     L = c.layer(rows=rows + 40)
-    c.check_y(L.forward(c.X), L._need_of(rows, 0) == 0)
+    c.check_y(L.forward(c.X))
     c.check_dx(L.backward(c.dY))
 
 
 def test_many_experts():
     c = Case([1, 0] * 2048, 64, 16, 64, x_order=True, top_k=2, y_order=True)
     L = c.layer()
-    c.check_y(L.forward(c.X, c.d_off, c.d_order), L.shape.forward_workspace_bytes == 0)
+    c.check_y(L.forward(c.X, c.d_off, c.d_order))
     c.check_dx(L.backward(c.dY, c.d_off, c.d_order))
 
 
@@ -129,7 +131,7 @@ def test_no_rows_and_fewer_rows():
     L = c.layer(rows=2000)
     assert L.forward(c.X[:0], c.d_off, c.d_order[:0]).shape == (0, 64)
     assert L.backward(c.dY[:0], c.d_off, c.d_order[:0]).shape == (0, 128)
-    c.check_y(L.forward(c.X, c.d_off, c.d_order), True)
+    c.check_y(L.forward(c.X, c.d_off, c.d_order))
     z = torch.zeros(3, dtype=torch.int32, device="cuda")
     Y = torch.full((70, 64), 7.5, dtype=torch.bfloat16, device="cuda")
     L.forward(c.X, z, c.d_order, Y)
