@@ -41,11 +41,11 @@ struct Piece {
   }
 };
 
-// Lanes that share a token: a power of two that covers its 16-byte pieces, up
-// to the workgroup.
-inline int token_lanes(int pieces) {
+// Lanes that share a token: a power of two that covers its 16-byte pieces, at
+// most `most`.
+inline int token_lanes(int pieces, int most) {
   int p = 1;
-  while (p < pieces && p < kThreads) p <<= 1;
+  while (p < pieces && p < most) p <<= 1;
   return p;
 }
 
@@ -82,83 +82,86 @@ __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a, int lanes, 
   sum.store(a.out, t * pieces + c);
 }
 
-// All pieces of a token by one workgroup (or a part of one): the dot products
-// meet by lane exchanges, then across the token's waves in wave order.
-template <bool F32>
+// All pieces of a token by one wave (or a part of one), KT of its slots at a
+// time: the loads of a piece of dout and of KT rows of Y are in flight together,
+// and the dot products meet by lane exchanges, the same ones whatever the number
+// of tokens.
+template <bool F32, int KT>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineArgs a, int lanes) {
-  constexpr int N = Piece<F32>::N, KB = 8;
-  __shared__ float part[kThreads / 64][KB];
-  const int pieces = a.d / N, per = kThreads / lanes, sub = threadIdx.x % lanes, wave = threadIdx.x >> 6;
+  constexpr int N = Piece<F32>::N;
+  const int pieces = a.d / N, per = kThreads / lanes, sub = threadIdx.x % lanes;
   const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
   const bool on = t < a.tokens;
-  const int64_t slot = t * a.k;
-  for (int j0 = 0; j0 < a.k; j0 += KB) {
-    float dot[KB];
+  const int64_t slot = (on ? t : 0) * a.k;
+  for (int j0 = 0; j0 < a.k; j0 += KT) {
+    float dot[KT], w[KT];
+    bool kept[KT];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) dot[j] = 0.f;
-    for (int c = sub; on && c < pieces; c += lanes) {
-      Piece<F32> g;
-      g.load(a.dout, t * pieces + c);
+    for (int j = 0; j < KT; ++j) {
+      dot[j] = 0.f;
+      const int64_t s = slot + min(j0 + j, a.k - 1);
+      kept[j] = !a.ids || (uint32_t)a.ids[s] < a.limit;
+      w[j] = a.weights ? a.weights[s] : 1.f;
+    }
+#pragma unroll 2
+    for (int c = sub; c < pieces; c += lanes) {
+      Piece<F32> g, y[KT];
+      g.load(a.dout, slot / a.k * pieces + c);
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        if (j0 + j >= a.k) break;
-        const int64_t s = slot + j0 + j;
-        const bool kept = !a.ids || (uint32_t)a.ids[s] < a.limit;
-        const float w = kept ? (a.weights ? a.weights[s] : 1.f) : 0.f;
-        if (a.dweights && kept) {
-          Piece<F32> y;
-          y.load(a.Y, s * pieces + c);
+      for (int j = 0; j < KT; ++j)
+        if (a.dweights && kept[j]) y[j].load(a.Y, (slot + min(j0 + j, a.k - 1)) * pieces + c);
 #pragma unroll
-          for (int i = 0; i < N; ++i) dot[j] += g.v[i] * y.v[i];
+      for (int j = 0; j < KT; ++j) {
+        if (a.dweights && kept[j]) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) dot[j] += g.v[i] * y[j].v[i];
         }
-        if (a.dY) {
+        if (a.dY && on && j0 + j < a.k) {
           Piece<F32> o;
 #pragma unroll
-          for (int i = 0; i < N; ++i) o.v[i] = kept ? w * g.v[i] : 0.f;
-          o.store(a.dY, s * pieces + c);
+          for (int i = 0; i < N; ++i) o.v[i] = kept[j] ? w[j] * g.v[i] : 0.f;
+          o.store(a.dY, (slot + j0 + j) * pieces + c);
         }
       }
     }
     if (!a.dweights) continue;
-    const int in_wave = lanes < 64 ? lanes : 64;
 #pragma unroll
-    for (int j = 0; j < KB; ++j)
-      for (int d = 1; d < in_wave; d <<= 1) dot[j] += __shfl_xor(dot[j], d);
-    if (lanes > 64) {
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-        for (int j = 0; j < KB; ++j) part[wave][j] = dot[j];
-      }
-      __syncthreads();
-      const int first = wave - sub / 64;
-#pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        dot[j] = part[first][j];
-        for (int w = 1; w < lanes / 64; ++w) dot[j] += part[first + w][j];
-      }
-    }
+    for (int j = 0; j < KT; ++j)
+      for (int d = 1; d < lanes; d <<= 1) dot[j] += __shfl_xor(dot[j], d);
     if (on && sub == 0) {
 #pragma unroll
-      for (int j = 0; j < KB; ++j)
+      for (int j = 0; j < KT; ++j)
         if (j0 + j < a.k) a.dweights[slot + j0 + j] = dot[j];
     }
   }
 }
 
 void launch_combine(bool f32, const CombineArgs& a, hipStream_t s) {
-  const int pieces = a.d / (f32 ? 4 : 8), lanes = token_lanes(pieces), per = kThreads / lanes;
+  const int pieces = a.d / (f32 ? 4 : 8), lanes = token_lanes(pieces, kThreads), per = kThreads / lanes;
   const int split = (pieces + kThreads - 1) / kThreads;
   const unsigned grid = (unsigned)((a.tokens + per - 1) / per * split);
   if (f32) hipLaunchKernelGGL((k_combine<true>), dim3(grid), dim3(kThreads), 0, s, a, lanes, split);
   else hipLaunchKernelGGL((k_combine<false>), dim3(grid), dim3(kThreads), 0, s, a, lanes, split);
 }
 
-void launch_combine_backward(bool f32, const CombineArgs& a, hipStream_t s) {
-  const int pieces = a.d / (f32 ? 4 : 8), lanes = token_lanes(pieces), per = kThreads / lanes;
+namespace {
+
+template <bool F32>
+void backward_of(const CombineArgs& a, hipStream_t s) {
+  const int lanes = token_lanes(a.d / (F32 ? 4 : 8), 64), per = kThreads / lanes;
   const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
-  if (f32) hipLaunchKernelGGL((k_combine_backward<true>), dim3(grid), dim3(kThreads), 0, s, a, lanes);
-  else hipLaunchKernelGGL((k_combine_backward<false>), dim3(grid), dim3(kThreads), 0, s, a, lanes);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, s, a, lanes); };
+  if (a.k == 1) go(k_combine_backward<F32, 1>);
+  else if (a.k == 2) go(k_combine_backward<F32, 2>);
+  else if (a.k <= 4) go(k_combine_backward<F32, 4>);
+  else go(k_combine_backward<F32, 8>);
+}
+
+}  // namespace
+
+void launch_combine_backward(bool f32, const CombineArgs& a, hipStream_t s) {
+  if (f32) backward_of<true>(a, s);
+  else backward_of<false>(a, s);
 }
 
 }  // namespace mlora

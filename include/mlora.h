@@ -659,8 +659,7 @@ typedef struct {
 /* logits: bf16 or fp32, row r starting at element r * ld (ld >= n_experts),
  * aligned to an element.  0 <= rows < 2^31; MLORA_ERR_UNSUPPORTED for more
  * rows than a launch takes (2^26 - 4; 2^24 - 1 over 1024 experts).  One kernel
- * on `stream`; with rows = 0 nothing is launched.  Results do not depend on
- * the other rows of a call. */
+ * on `stream`; with rows = 0 nothing is launched. */
 mlora_status mlora_route(const mlora_router *router, const void *logits, mlora_dtype dtype, int64_t rows,
                          int64_t ld, const float *bias, int32_t *ids, float *weights, void *stream);
 
