@@ -1070,9 +1070,9 @@ class AffineLinear:
     """A frozen 4-bit weight, or one per expert: ``q`` is the packed buffer of
     [n_experts * d_out][d_in] (``mlora_affine_quantize``, ``affine_pack``).
     ``forward`` and ``backward`` take up to ``max_rows`` grouped rows, as those
-    of ``ExpertLinear``.  Nothing is kept beside ``q``: workspaces (a decoded
-    weight, 2 bytes each) come from torch's allocator for the call, so calls may
-    overlap.  A call given a ``stream`` runs there, and what it makes is made
+    of ``ExpertLinear``.  Nothing is kept beside ``q``: the workspace of calls of
+    many rows (the decoded weight, 2 bytes each) comes from torch's allocator for
+    the call, so calls may overlap.  A call given a ``stream`` runs there, and what it makes is made
     there: the stream has to wait for the inputs, and a reader on another stream
     for the results."""
 
@@ -1082,15 +1082,14 @@ class AffineLinear:
         _need(q, "q", self.shape.q_shape, torch.uint8)
         self.q = q
 
-    def _workspace(self, need, stream):
-        torch = _torch()
-        return _made(stream, torch.empty, need, torch.uint8, self.q.device, returned=False) if need else None
-
-    def _need_of(self, rows, which):
-        """Workspace bytes of a call of ``rows`` rows."""
+    def _workspace(self, rows, most, which, stream):
+        """A call's workspace, for ``rows`` rows where ``most`` is that of max_rows."""
+        if not most:
+            return None
         f, b = ctypes.c_int64(), ctypes.c_int64()
         check(lib().mlora_affine_workspace(ctypes.byref(self.shape.struct(rows)), ctypes.byref(f), ctypes.byref(b)))
-        return (f, b)[which].value
+        need = (f, b)[which].value
+        return _made(stream, _torch().empty, need, _torch().uint8, self.q.device, returned=False) if need else None
 
     def forward(self, X, offsets=None, order=None, Y=None, stream=None):
         """Y [rows][d_out]; a Y made here is zero in rows of no group when an
@@ -1101,8 +1100,8 @@ class AffineLinear:
             rows = X.shape[0] * sh.top_k if sh.x_order else X.shape[0]
             make = torch.zeros if sh.y_order else torch.empty
             Y = _made(stream, make, (rows, sh.d_out), X.dtype, X.device)
-        need = self._need_of(Y.shape[0], 0) if sh.forward_workspace_bytes else 0
-        return mlora_affine_forward(sh, X, self.q, offsets, order, Y, self._workspace(need, stream), stream)
+        ws = self._workspace(Y.shape[0], sh.forward_workspace_bytes, 0, stream)
+        return mlora_affine_forward(sh, X, self.q, offsets, order, Y, ws, stream)
 
     def backward(self, dY, offsets=None, order=None, dX=None, stream=None):
         """dX [rows][d_in]; a dX made here is zero in rows of no group when an
@@ -1112,5 +1111,5 @@ class AffineLinear:
         if dX is None:
             make = torch.zeros if sh.x_order else torch.empty
             dX = _made(stream, make, (dY.shape[0], sh.d_in), dY.dtype, dY.device)
-        ws = self._workspace(sh.backward_workspace_bytes if dY.shape[0] > 0 else 0, stream)
+        ws = self._workspace(dY.shape[0], sh.backward_workspace_bytes, 1, stream)
         return mlora_affine_backward(sh, dY, self.q, offsets, order, dX, ws, stream)

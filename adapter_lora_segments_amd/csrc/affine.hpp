@@ -25,5 +25,7 @@ void launch_affine_decode(const uint8_t* codes, const uint32_t* params, int64_t 
 // parameters; one of the tiles that affine_choice.hpp chooses from.
 void launch_affine_few(const ExpertArgs& a, int32_t group, int rows, int cols, hipStream_t s);
 void launch_affine_tile(const ExpertArgs& a, int32_t group, int rows, int parts, hipStream_t s);
+// dX over the same weights (a.N = d_in, a.K = d_out).
+void launch_affine_dx(const ExpertArgs& a, int32_t group, int rows, hipStream_t s);
 
 }  // namespace mlora

@@ -28,10 +28,11 @@ constexpr double kAffineExact = 16;
 
 // From this many rows a group on, the weights are decoded to bf16 in memory
 // first and the bf16 product runs over them: 2.5 bytes a weight once more,
-// against tiles that decode on the way at three quarters of its rate.
-// Measured (us, decoded first and in tiles): 1024 rows, 4096 -> 14336 127 and
-// 139; 512 rows, 4096 -> 4096 43 and 27; 2048 rows over 8 experts, 4096 -> 4096
-// 175 and 77; 8192 rows, 4096 -> 14336 766 and 1050.
+// against tiles that decode on the way at 0.7 of its rate.  Measured (us,
+// decoded first and in tiles): 1024 rows, 4096 -> 14336 128 and 136; 512 rows,
+// 4096 -> 4096 43 and 27; 2048 rows over 8 experts, 4096 -> 4096 175 and 76;
+// 8192 rows, 4096 -> 14336 766 and 1050; dX of 1024 rows 163 and 163, of 2048
+// rows 227 and 281, of 2048 rows over 8 experts of 4096 x 4096 176 and 88.
 constexpr int64_t kAffineDecoded = 1024;
 
 // A tile of rows x cols: of the few-row kernel (split: waves side by side, the
@@ -60,6 +61,13 @@ constexpr AffineChoice kAffine[] = {
     {false, 64, 128, 1, 3.0, .00700, .00550, 3.0e6},  {false, 64, 128, 2, 3.5, .00560, .00610, 3.0e6},
     {false, 128, 128, 1, 3.0, .00990, .00920, 3.0e6}, {false, 128, 128, 2, 3.5, .00800, .00980, 3.0e6}};
 
+// The same for dX, whose tiled kernel has them all.  K = 4096, N = 4096 (us;
+// 32, 64 and 128 rows): 256 rows 29, 35, 49; 512 rows over 8 experts 46, 38, 53;
+// 2048 rows over 8 153, 107, 89; 8192 rows 596, 398, 330.
+constexpr AffineChoice kAffineDx[] = {{false, 32, 128, 2, 3.0, .00560, .00500, 3.0e6},
+                                      {false, 64, 128, 1, 3.0, .00820, .00640, 3.0e6},
+                                      {false, 128, 128, 1, 3.0, .01130, .01000, 3.0e6}};
+
 inline double affine_us(const AffineChoice& c, const ExpertArgs& a, double weight_bytes) {
   double groups = 1;
   if (a.offsets && a.n_experts > 1) groups = a.n_experts * (1 - std::pow(1.0 - 1.0 / a.n_experts, a.rows));
@@ -74,23 +82,24 @@ inline double affine_us(const AffineChoice& c, const ExpertArgs& a, double weigh
   return us > read ? us : read;
 }
 
-// The last entry's grid always fits a launch.
-inline const AffineChoice& affine_choose(const ExpertArgs& a, int32_t group) {
-  constexpr int n = sizeof(kAffine) / sizeof(kAffine[0]);
+// (The few-row kernel's last entry and the list's last one always fit a launch.)
+template <int N>
+const AffineChoice& affine_choose(const AffineChoice (&list)[N], const ExpertArgs& a, int32_t group) {
   const double bytes = (double)a.K * a.N * (0.5 + 4.0 / group);
-  const bool exact = affine_rows(a) <= kAffineExact;
+  const bool exact = list[0].few && affine_rows(a) <= kAffineExact;
   int best = -1;
   double best_us = 0;
-  for (int i = 0; i < n; ++i) {
-    const AffineChoice& c = kAffine[i];
-    if ((exact && !c.few) || (affine_grid(a, c.rows, c.cols) > kMaxGrid && (exact ? c.cols < 128 : i + 1 < n))) continue;
+  for (int i = 0; i < N; ++i) {
+    const AffineChoice& c = list[i];
+    const bool last = exact ? c.few && !list[i + 1].few : i + 1 == N;
+    if ((exact && !c.few) || (!last && affine_grid(a, c.rows, c.cols) > kMaxGrid)) continue;
     const double us = affine_us(c, a, bytes);
     if (best < 0 || us < best_us) {
       best = i;
       best_us = us;
     }
   }
-  return kAffine[best];
+  return list[best];
 }
 
 }  // namespace mlora

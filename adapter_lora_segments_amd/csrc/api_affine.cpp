@@ -67,7 +67,7 @@ mlora::ExpertArgs forward_args(const mlora_affine_shape& s, const int32_t* offse
 
 int64_t weights_of(const mlora_affine_shape& s) { return (int64_t)s.n_experts * s.d_in * s.d_out; }
 
-// Whether a forward decodes the weights into the workspace first.  A call of
+// Whether a call decodes the weights into the workspace first.  A call of
 // fewer rows does not unless this one does.
 bool decodes(const mlora_affine_shape& s) { return s.rows >= mlora::kAffineDecoded * s.n_experts; }
 
@@ -134,9 +134,8 @@ mlora_status mlora_affine_quantize(const void* X, mlora_dtype dtype, int64_t row
 mlora_status mlora_affine_workspace(const mlora_affine_shape* shape, int64_t* forward, int64_t* backward) {
   mlora_status st;
   if (const char* msg = shape_error(shape, &st)) return api_fail(st, msg);
-  // the decoded weight; of a forward of fewer rows no more
   if (forward) *forward = decodes(*shape) ? 2 * weights_of(*shape) : 0;
-  if (backward) *backward = shape->rows > 0 ? 2 * weights_of(*shape) : 0;
+  if (backward) *backward = decodes(*shape) ? 2 * weights_of(*shape) : 0;
   return MLORA_OK;
 }
 
@@ -146,7 +145,7 @@ mlora_status mlora_affine_forward(const mlora_affine_shape* shape, const void* X
   if (const char* msg = shape_error(shape, &st)) return api_fail(st, msg);
   const mlora_affine_shape& s = *shape;
   const bool codes = !decodes(s);
-  st = check_call(s, offsets, order, workspace, ws_bytes, s.rows > 0 && !codes ? 2 * weights_of(s) : 0);
+  st = check_call(s, offsets, order, workspace, ws_bytes, codes ? 0 : 2 * weights_of(s));
   if (st != MLORA_OK) return st;
   if (!q || (s.rows > 0 && (!X || !Y))) return api_fail(MLORA_ERR_INVALID_ARG, "affine forward: X, q and Y must be non-NULL");
   if (!api_aligned(X, 16) || !api_aligned(q, 16) || !api_aligned(Y, 16))
@@ -161,7 +160,7 @@ mlora_status mlora_affine_forward(const mlora_affine_shape* shape, const void* X
     a.B = w;
     a.b_expert = s.d_in * s.d_out / 2;
     a.b_scale = w + mlora::affine_code_bytes(s.n_experts * s.d_out, s.d_in);
-    const mlora::AffineChoice& c = mlora::affine_choose(a, s.group);
+    const mlora::AffineChoice& c = mlora::affine_choose(mlora::kAffine, a, s.group);
     if (c.few) mlora::launch_affine_few(a, s.group, c.rows, c.cols, cs);
     else mlora::launch_affine_tile(a, s.group, c.rows, c.split, cs);
   } else {
@@ -179,18 +178,16 @@ mlora_status mlora_affine_backward(const mlora_affine_shape* shape, const void* 
   mlora_status st;
   if (const char* msg = shape_error(shape, &st)) return api_fail(st, msg);
   const mlora_affine_shape& s = *shape;
-  st = check_call(s, offsets, order, workspace, ws_bytes, s.rows > 0 ? 2 * weights_of(s) : 0);
+  const bool codes = !decodes(s);
+  st = check_call(s, offsets, order, workspace, ws_bytes, codes ? 0 : 2 * weights_of(s));
   if (st != MLORA_OK) return st;
   if (!q || (s.rows > 0 && (!dY || !dX))) return api_fail(MLORA_ERR_INVALID_ARG, "affine backward: dY, q and dX must be non-NULL");
   if (!api_aligned(dY, 16) || !api_aligned(q, 16) || !api_aligned(dX, 16))
     return api_fail(MLORA_ERR_INVALID_ARG, "affine backward: device pointers must be 16-byte aligned");
   if (s.rows == 0) return MLORA_OK;
   hipStream_t cs = static_cast<hipStream_t>(stream);
-  st = decode(s, static_cast<const uint8_t*>(q), workspace, cs);
-  if (st != MLORA_OK) return st;
   mlora::ExpertArgs a = base_args(s, offsets, order);
   a.A = static_cast<const uint8_t*>(dY);
-  a.B = static_cast<const uint8_t*>(workspace);
   a.C = dX;
   a.lda = s.d_out;
   a.ldb = s.d_in;
@@ -199,8 +196,19 @@ mlora_status mlora_affine_backward(const mlora_affine_shape* shape, const void* 
   a.mc = {s.x_by_order, {0, 0}};
   a.N = (int32_t)s.d_in;
   a.K = (int32_t)s.d_out;
-  a.b_expert = s.d_in * s.d_out * 2;
-  mlora::launch_expert_rows(mlora::ExpertForm::kBf16, false, a, cs);
+  const uint8_t* const w = static_cast<const uint8_t*>(q);
+  if (codes) {
+    a.B = w;
+    a.b_expert = s.d_in * s.d_out / 2;
+    a.b_scale = w + mlora::affine_code_bytes(s.n_experts * s.d_out, s.d_in);
+    mlora::launch_affine_dx(a, s.group, mlora::affine_choose(mlora::kAffineDx, a, s.group).rows, cs);
+  } else {
+    st = decode(s, w, workspace, cs);
+    if (st != MLORA_OK) return st;
+    a.B = static_cast<const uint8_t*>(workspace);
+    a.b_expert = s.d_in * s.d_out * 2;
+    mlora::launch_expert_rows(mlora::ExpertForm::kBf16, false, a, cs);
+  }
   return api_launched();
 }
 

@@ -736,11 +736,12 @@ mlora_status mlora_affine_quantize(const void *X, mlora_dtype dtype, int64_t row
  *   backward:  dX[p(s)] = dY[y(s)] W_e       (the weight is frozen)
  * offsets, order, x_by_order, y_by_order and top_k as in mlora_expert_shape,
  * also in which rows are left as they were.  Sums in fp32, one rounding at the
- * end.  Over few rows a group the codes are multiplied as they are, the scales
- * in fp32: the weights are not rounded (activations whose sums over a group
- * pass fp32's range, or that are not finite, make NaN).  Over more rows and in
- * the backward the weights are rounded to bf16 first, as the matrix cores take
- * them.
+ * end.  Forwards of up to 16 rows a group (rows / min(n_experts, rows))
+ * multiply the codes as they are and scale in fp32: the weights are not
+ * rounded.  Over more rows (by predicted time) and in the backward the weights
+ * are rounded to bf16, as the matrix cores take them.  A row with values that
+ * are not finite, or whose sums pass fp32's range, makes inf or NaN in its own
+ * output row alone; magnitudes of s are below 2^100.
  */
 typedef struct {
   int64_t rows;            /* grouped rows, 0 <= rows < 2^31, a multiple of top_k */
@@ -753,7 +754,8 @@ typedef struct {
 } mlora_affine_shape;
 
 /* Workspaces of forward and backward for this shape or one with fewer rows
- * (either pointer may be NULL).  Nothing in them has to be kept between calls;
+ * (either pointer may be NULL): 0 below 1024 rows an expert, where tiles decode
+ * on the way, else the decoded weight (2 bytes each).  Nothing in them has to be kept between calls;
  * calls that may overlap (streams, host threads, replays of captured graphs)
  * need one each. */
 mlora_status mlora_affine_workspace(const mlora_affine_shape *shape, int64_t *forward, int64_t *backward);
