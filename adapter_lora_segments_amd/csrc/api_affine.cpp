@@ -18,6 +18,10 @@ constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 
 bool group_ok(int32_t group) { return group == 32 || group == 64 || group == 128; }
 
+// Whether a call decodes the weights into the workspace first.  A call of
+// fewer rows does not unless this one does.
+bool decodes(const mlora_affine_shape& s) { return s.rows >= mlora::kAffineDecoded * s.n_experts; }
+
 // Message of the first thing wrong with a shape, or NULL.
 const char* shape_error(const mlora_affine_shape* s, mlora_status* st) {
   *st = MLORA_ERR_INVALID_ARG;
@@ -34,11 +38,14 @@ const char* shape_error(const mlora_affine_shape* s, mlora_status* st) {
   if (s->top_k > 1 && !s->x_by_order) return "affine: top_k > 1 needs x_by_order";
   *st = MLORA_ERR_UNSUPPORTED;
   if (s->d_in > MLORA_MAX_EXPERT_DIM || s->d_out > MLORA_MAX_EXPERT_DIM) return "affine: d_in and d_out are at most 2^20";
+  if (s->n_experts * s->d_out > ((int64_t)1 << 40) / s->d_in) return "affine: more than 2^40 weights";
   // launch bounds: tiles of 128 x 128 (larger ones of the decoded products, smaller
-  // ones where they fit; few rows a group: 32 x 128), a lane per eight decoded weights
+  // ones where they fit; few rows a group: 32 x 128), and where the weights are decoded
+  // first, a lane per eight of them
   const int64_t d = (s->d_in > s->d_out ? s->d_in : s->d_out) + 127;
   const int64_t groups = s->n_experts < s->rows ? s->n_experts : s->rows;
-  if (s->rows / 128 + 2 * groups > kMaxGrid / (d / 128) || s->n_experts * s->d_out > kMaxGrid * 256 / (s->d_in / 8))
+  if (s->rows / 128 + 2 * groups > kMaxGrid / (d / 128) ||
+      (decodes(*s) && s->n_experts * s->d_out > kMaxGrid * 256 / (s->d_in / 8)))
     return "affine: too many tiles for one launch";
   *st = MLORA_OK;
   return nullptr;
@@ -66,10 +73,6 @@ mlora::ExpertArgs forward_args(const mlora_affine_shape& s, const int32_t* offse
 }
 
 int64_t weights_of(const mlora_affine_shape& s) { return (int64_t)s.n_experts * s.d_in * s.d_out; }
-
-// Whether a call decodes the weights into the workspace first.  A call of
-// fewer rows does not unless this one does.
-bool decodes(const mlora_affine_shape& s) { return s.rows >= mlora::kAffineDecoded * s.n_experts; }
 
 mlora_status check_call(const mlora_affine_shape& s, const int32_t* offsets, const int32_t* order, void* ws,
                         size_t ws_bytes, int64_t need) {

@@ -741,7 +741,8 @@ mlora_status mlora_affine_quantize(const void *X, mlora_dtype dtype, int64_t row
  * rounded.  Over more rows (by predicted time) and in the backward the weights
  * are rounded to bf16, as the matrix cores take them.  A row with values that
  * are not finite, or whose sums pass fp32's range, makes inf or NaN in its own
- * output row alone; magnitudes of s are below 2^100.
+ * output row alone; magnitudes of s are below 2^100.  A weight has at most 2^40
+ * elements, and 2^34 - 2048 where a call decodes it first.
  */
 typedef struct {
   int64_t rows;            /* grouped rows, 0 <= rows < 2^31, a multiple of top_k */
