@@ -6,10 +6,9 @@
 // rows take few lanes each (work per row counts), few rows many (latency does).
 // Scores are computed in 64 bits, which the vector units run at the rate of
 // 32, and rounded to fp32 once: two programs then agree on every choice but
-// for scores within 2^-45 of a rounding border.  A choice compares (score +
-// bias in fp32, expert from behind) as one whole number below 2^44, held
-// exactly in a double, so a step of the top_k is a maximum, and ties go to the
-// lowest expert.
+// for scores within 2^-45 of a rounding border.  A choice compares score + bias,
+// in fp32, with the expert's number in the 29 bits that fp32 leaves of a double,
+// so a step of the top_k is a maximum, and ties go to the lowest expert.
 #include "device_common.hpp"
 #include "route.hpp"
 
@@ -27,38 +26,46 @@ constexpr float kNone = -__builtin_inff();
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
 
-// e^x in 64 bits for x <= 0: x = n ln 2 + r, |r| <= ln 2 / 2, the Taylor series
-// of e^r to r^11 (the next term is below 2^-47).  NaN stays.
+// A constant in scalar registers, where a multiply-add takes it as it is (the
+// compiler's choice copies it into vector registers before each).
+__device__ __forceinline__ double constant(double c) {
+  asm("" : "+s"(c));
+  return c;
+}
+// e^x in 64 bits for |x| <= 1e9: x = n ln 2 + r, |r| <= ln 2 / 2 (the rounding
+// to n by the sum with 3 2^51, which leaves n in the low bits), and for e^r the
+// polynomial of degree 10 through 1 at 0 of least relative error, 2^-51.6 (by
+// Remez exchange).  NaN stays.
 __device__ __forceinline__ double exp64(double x) {
-  const double c = x < -800.0 ? -800.0 : x;          // zero, also of -infinity
-  const double n = __builtin_rint(c * 1.4426950408889634);
-  double r = __builtin_fma(n, -0.6931471805599453, c);
-  r = __builtin_fma(n, -2.3190468138462996e-17, r);
-  double p = 1.0 / 39916800.0;
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
-  p = __builtin_fma(p, r, 0.5);
+  const double big = constant(6755399441055744.0);
+  const double t = __builtin_fma(x, constant(1.4426950408889634), big), n = t - big;
+  double r = __builtin_fma(n, constant(-0.6931471805599453), x);
+  r = __builtin_fma(n, constant(-2.3190468138462996e-17), r);
+  double p = constant(0x1.2a4757db84f44p-22);
+  p = __builtin_fma(p, r, constant(0x1.730bd565ae4cdp-19));
+  p = __builtin_fma(p, r, constant(0x1.a017fb62f39a4p-16));
+  p = __builtin_fma(p, r, constant(0x1.a01967c4fae8fp-13));
+  p = __builtin_fma(p, r, constant(0x1.6c16c20da84a3p-10));
+  p = __builtin_fma(p, r, constant(0x1.111111337199ap-7));
+  p = __builtin_fma(p, r, constant(0x1.555555552f91ep-5));
+  p = __builtin_fma(p, r, constant(0x1.5555555548c99p-3));
+  p = __builtin_fma(p, r, constant(0x1.000000000004bp-1));
+  p = __builtin_fma(p, r, constant(0x1.0000000000029p+0));
   p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_ldexp(p, (int)n);
+  return __builtin_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
 }
-// 1 / x for x in [1, 2]: the hardware's approximation and two Newton steps (its
-// error is squared by each).
+// 1 / x for x in [1, 2^1011]: the hardware's approximation, off by e < 2^-20, times
+// 1 + e + e^2.
 __device__ __forceinline__ double reciprocal(double x) {
-  double r = __builtin_amdgcn_rcp(x);
-  r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-  return __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+  const double r = __builtin_amdgcn_rcp(x), e = __builtin_fma(-x, r, 1.0);
+  return __builtin_fma(__builtin_fma(e, e, e), r, r);
 }
-__device__ __forceinline__ double sigmoid64(float x) {
-  const double t = exp64(-__builtin_fabs((double)x)), r = reciprocal(1.0 + t);
-  return x < 0.f ? t * r : r;
+__device__ __forceinline__ float clamp(float x, float lo, float hi) {     // NaN stays
+  const float y = x < lo ? lo : x;
+  return y > hi ? hi : y;
 }
+// (e^700 has a reciprocal; what is below counts as zero, which it is in fp32)
+__device__ __forceinline__ double sigmoid64(float x) { return reciprocal(1.0 + exp64(-(double)clamp(x, -700.f, 700.f))); }
 
 // Exchanges within L lanes.  Each step pairs groups that already agree, so any
 // lane of the other group will do: within 16 lanes DPP moves, then swaps of
@@ -113,14 +120,45 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// The key of a choice: c as a double, its lowest 12 bits 4095 - e where c is not
+// negative and e where it is (a larger number is then a smaller key).  Not
+// numbers of that kind, which the bits would make a NaN: infinity 2^1000 and NaN
+// 2^1001, both with the bits; none, 2^1000 below zero, for an expert that may
+// not be chosen.
+constexpr uint32_t kLast = MLORA_MAX_EXPERTS - 1;      // 12 bits
+constexpr double kNoKey = -0x1p1000;
+__device__ __forceinline__ double with_low(double v, uint32_t low) {
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, v) | low);
+}
+__device__ __forceinline__ double key_of(float c, uint32_t last) {
+  const uint32_t flip = (uint32_t)((int32_t)__float_as_uint(c) >> 31) & kLast;
+  const double k = with_low((double)c, last ^ flip);
+  return c == kNone ? kNoKey : k;
+}
+__device__ __forceinline__ bool no_key(double key) { return key < -0x1p999; }
+__device__ __forceinline__ int expert_of(double key) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, key);
+  const uint32_t flip = (uint32_t)((int32_t)(b >> 32) >> 31) & kLast;
+  const int e = (int)((((uint32_t)b & kLast) ^ flip) ^ kLast);
+  return no_key(key) ? -1 : e;
+}
+__device__ __forceinline__ uint32_t image_of(double key) {
+  return no_key(key) ? 0u : key >= 0x1p1001 ? 0xffffffffu : ordered((float)key);
+}
+
 // A row's softmax terms: its maximum and the reciprocal of the sum of e^(x - max).
 struct Soft {
   double top, inv;
 };
+// x - top <= 0, where e^ of it is zero in fp32 and in every sum at most -800.
+__device__ __forceinline__ double below(float x, double top) {
+  const double d = (double)x - top;
+  return d < -800.0 ? -800.0 : d;
+}
 __device__ __forceinline__ double score_of(const RouteArgs& a, const Soft& s, float x) {
   if (x == kNone) return 0.0;
-  if (a.sigmoid) return sigmoid64(x);
-  return exp64((double)x - s.top) * s.inv;
+  if (a.sigmoid) return x < -700.f ? 0.0 : sigmoid64(x);
+  return exp64(below(x, s.top)) * s.inv;
 }
 // e[v] = e^(x - max), zero at -infinity
 template <int L, int V>
@@ -134,7 +172,7 @@ __device__ __forceinline__ Soft softmax_terms(const float (&x)[V], double (&e)[V
   double sum = 0.0;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    e[v] = x[v] == kNone ? 0.0 : exp64((double)x[v] - s.top);
+    e[v] = x[v] == kNone ? 0.0 : exp64(below(x[v], s.top));
     sum += e[v];
   }
   sum = group_sum<L>(sum);
@@ -227,11 +265,6 @@ __device__ __forceinline__ void top8(double (&key)[V], double (&k)[8]) {
   across8<L>(k);
 }
 
-__device__ __forceinline__ int expert_of(double key) {
-  const double whole = __builtin_floor(key * (1.0 / 4096.0));
-  return key >= 1.0 ? 4095 - (int)__builtin_fma(-4096.0, whole, key) : -1;
-}
-
 }  // namespace
 
 // LDS of a row: the chosen ids [top_k]; with expert groups, per run of min(V,
@@ -256,16 +289,27 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] *= sm.inv;
   }
-  float b[V];
+  float c[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) b[v] = 0.f;
-  if (a.bias) load_row<float, V>(a.bias, a.E, sub, bias_whole, b);
+  for (int v = 0; v < V; ++v) c[v] = x[v] == kNone ? kNone : (float)key[v];
+  if (a.bias) {
+    float b[V];
+    load_row<float, V>(a.bias, a.E, sub, bias_whole, b);
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] += c[v] == kNone ? 0.f : b[v];
+  }
+  // (V is a power of two: 4095 - e is what the lane's experts share and V - 1 - v)
+  const uint32_t last = kLast + 1 - (sub + 1) * V;
+  bool odd = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = sub * V + v;
-    const float c = (float)key[v] + b[v];
-    const bool may = x[v] != kNone && c != kNone;
-    key[v] = may ? __builtin_fma((double)ordered(c), 4096.0, (double)(4095 - e)) : 0.0;
+    odd = odd || !(c[v] < -kNone);
+    key[v] = key_of(c[v], last | (V - 1 - v));
+  }
+  if (__any(odd)) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (!(c[v] < -kNone)) key[v] = with_low(c[v] != c[v] ? 0x1p1001 : 0x1p1000, last | (V - 1 - v));
   }
 
   int* const sel = lds + rb * a.k;
@@ -274,21 +318,21 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
     uint32_t* const cs = gs + a.n_groups;
     const bool runs = a.per_group % V == 0;       // a lane's experts lie in one group
     if (runs) {
-      double b1 = 0.0, b2 = 0.0;
+      double b1 = kNoKey, b2 = kNoKey;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         b2 = key_max(b2, key_min(b1, key[v]));
         b1 = key_max(b1, key[v]);
       }
       if (sub * V < a.E) {
-        cs[CS * sub] = (uint32_t)(b1 * (1.0 / 4096.0));
-        if (V > 1) cs[CS * sub + 1] = (uint32_t)(b2 * (1.0 / 4096.0));
+        cs[CS * sub] = image_of(b1);
+        if (V > 1) cs[CS * sub + 1] = image_of(b2);
       }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int e = sub * V + v;
-        if (e < a.E) cs[e] = (uint32_t)(key[v] * (1.0 / 4096.0));
+        if (e < a.E) cs[e] = image_of(key[v]);
       }
     }
     __syncthreads();
@@ -319,18 +363,18 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
       for (int i = 0; i < a.n_groups; ++i) ahead += (gs[i] > mine || (gs[i] == mine && i < g)) ? 1 : 0;
       if (ahead >= a.top_groups) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = 0.0;
+        for (int v = 0; v < V; ++v) key[v] = kNoKey;
       }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int e = sub * V + v;
-        if (key[v] > 0.0) {
+        if (!no_key(key[v])) {
           const int g = e / a.per_group;
           const uint32_t mine = gs[g];
           int ahead = 0;
           for (int i = 0; i < a.n_groups; ++i) ahead += (gs[i] > mine || (gs[i] == mine && i < g)) ? 1 : 0;
-          if (ahead >= a.top_groups) key[v] = 0.0;
+          if (ahead >= a.top_groups) key[v] = kNoKey;
         }
       }
     }
@@ -355,28 +399,27 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
       for (int v = 1; v < V; ++v) m = key_max(m, key[v]);
       m = across<L>(m, [](double a, double b) { return key_max(a, b); });
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = key[v] == m ? 0.0 : key[v];
+      for (int v = 0; v < V; ++v) key[v] = key[v] == m ? kNoKey : key[v];
       if (sub == 0) sel[j] = expert_of(m);
     }
   }
   __syncthreads();
-  // weights: the chosen logits once more, a lane per slot
-  double total = 0.0;
-  if (a.renorm) {
-    for (int j = sub; j < a.k; j += L) {
-      const int id = sel[j];
-      total += id >= 0 ? score_of(a, sm, load_logit(p + id)) : 0.0;
-    }
-    total = group_sum<L>(total);
+  // weights: the chosen logits once more, a lane per slot (a lane's first slot's score is kept)
+  const int id0 = sub < a.k ? sel[sub] : -1;
+  const double u0 = id0 >= 0 ? score_of(a, sm, load_logit(p + id0)) : 0.0;
+  double total = u0;
+  for (int j = sub + L; j < a.k; j += L) {
+    const int id = sel[j];
+    total += id >= 0 ? score_of(a, sm, load_logit(p + id)) : 0.0;
   }
+  if (a.renorm) total = group_sum<L>(total);
+  if (!on) return;
   for (int j = sub; j < a.k; j += L) {
     const int id = sel[j];
-    double w = id >= 0 ? score_of(a, sm, load_logit(p + id)) : 0.0;
-    if (a.renorm && total != 0.0) w /= total;
-    if (on) {
-      a.ids[row * a.k + j] = id;
-      a.weights[row * a.k + j] = (float)(w * (double)a.scale);
-    }
+    double u = j == sub ? u0 : id >= 0 ? score_of(a, sm, load_logit(p + id)) : 0.0;
+    if (a.renorm && total != 0.0) u /= total;
+    a.ids[row * a.k + j] = id;
+    a.weights[row * a.k + j] = (float)(u * (double)a.scale);
   }
 }
 
