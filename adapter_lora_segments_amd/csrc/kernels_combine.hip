@@ -12,6 +12,7 @@ namespace mlora {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMostGroups = (1 << 24) - 1;       // workgroups of a launch: below 2^32 threads
 
 // 16 bytes of a row as fp32: eight bf16 or four fp32.
 template <bool F32>
@@ -82,57 +83,51 @@ __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a, int lanes, 
   sum.store(a.out, t * pieces + c);
 }
 
-// All pieces of a token by one wave (or a part of one), KT of its slots at a
-// time: the loads of a piece of dout and of KT rows of Y are in flight together,
-// and the dot products meet by lane exchanges, the same ones whatever the number
-// of tokens.
-template <bool F32, int KT>
+// A slot by one wave (`lanes` of one where a row has fewer pieces), with the loads
+// of U pieces of dout and of its row of Y in flight; the slots of a token read
+// dout once each, all but the first from the caches.  A lane's pieces are added
+// in order and the lanes meet by exchanges, the same ones for any number of
+// tokens and slots.
+template <bool F32, int U>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineArgs a, int lanes) {
   constexpr int N = Piece<F32>::N;
   const int pieces = a.d / N, per = kThreads / lanes, sub = threadIdx.x % lanes;
-  const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
-  const bool on = t < a.tokens;
-  const int64_t slot = (on ? t : 0) * a.k;
-  for (int j0 = 0; j0 < a.k; j0 += KT) {
-    float dot[KT], w[KT];
-    bool kept[KT];
+  const int64_t slots = a.tokens * a.k;
+  for (int64_t s0 = (int64_t)blockIdx.x * per; s0 < slots; s0 += (int64_t)gridDim.x * per) {
+    // (below 2^31; lanes past the last slot take the last one's, but store nothing)
+    const bool on = s0 + threadIdx.x / lanes < slots;
+    const uint32_t slot = (uint32_t)(on ? s0 + threadIdx.x / lanes : slots - 1), t = slot / (uint32_t)a.k;
+    const bool kept = !a.ids || (uint32_t)a.ids[slot] < a.limit;
+    const bool dots = a.dweights && kept;
+    const float w = a.weights ? a.weights[slot] : 1.f;
+    const int64_t g_at = (int64_t)t * pieces, y_at = dots ? (int64_t)slot * pieces : g_at;
+    const void* const y_of = dots ? a.Y : a.dout;       // a dropped slot's row is not read
+    float dot = 0.f;
+    for (int c0 = sub; c0 < pieces; c0 += lanes * U) {
+      Piece<F32> g[U], y[U];
 #pragma unroll
-    for (int j = 0; j < KT; ++j) {
-      dot[j] = 0.f;
-      const int64_t s = slot + min(j0 + j, a.k - 1);
-      kept[j] = !a.ids || (uint32_t)a.ids[s] < a.limit;
-      w[j] = a.weights ? a.weights[s] : 1.f;
-    }
-#pragma unroll 2
-    for (int c = sub; c < pieces; c += lanes) {
-      Piece<F32> g, y[KT];
-      g.load(a.dout, slot / a.k * pieces + c);
+      for (int u = 0; u < U; ++u) {
+        const int c = min(c0 + lanes * u, pieces - 1);
+        g[u].load(a.dout, g_at + c);
+        y[u].load(y_of, y_at + c);
+      }
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
-        if (a.dweights && kept[j]) y[j].load(a.Y, (slot + min(j0 + j, a.k - 1)) * pieces + c);
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + lanes * u;
+        if (c >= pieces) break;
 #pragma unroll
-      for (int j = 0; j < KT; ++j) {
-        if (a.dweights && kept[j]) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) dot[j] += g.v[i] * y[j].v[i];
-        }
-        if (a.dY && on && j0 + j < a.k) {
+        for (int i = 0; i < N; ++i) dot += g[u].v[i] * y[u].v[i];
+        if (a.dY && on) {
           Piece<F32> o;
 #pragma unroll
-          for (int i = 0; i < N; ++i) o.v[i] = kept[j] ? w[j] * g.v[i] : 0.f;
-          o.store(a.dY, (slot + j0 + j) * pieces + c);
+          for (int i = 0; i < N; ++i) o.v[i] = kept ? w * g[u].v[i] : 0.f;
+          o.store(a.dY, (int64_t)slot * pieces + c);
         }
       }
     }
     if (!a.dweights) continue;
-#pragma unroll
-    for (int j = 0; j < KT; ++j)
-      for (int d = 1; d < lanes; d <<= 1) dot[j] += __shfl_xor(dot[j], d);
-    if (on && sub == 0) {
-#pragma unroll
-      for (int j = 0; j < KT; ++j)
-        if (j0 + j < a.k) a.dweights[slot + j0 + j] = dot[j];
-    }
+    for (int d = 1; d < lanes; d <<= 1) dot += __shfl_xor(dot, d);
+    if (on && sub == 0) a.dweights[slot] = kept ? dot : 0.f;
   }
 }
 
@@ -148,12 +143,13 @@ namespace {
 
 template <bool F32>
 void backward_of(const CombineArgs& a, hipStream_t s) {
-  const int lanes = token_lanes(a.d / (F32 ? 4 : 8), 64), per = kThreads / lanes;
-  const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
+  const int pieces = a.d / (F32 ? 4 : 8), lanes = token_lanes(pieces, 64), per = kThreads / lanes;
+  const int64_t groups = (a.tokens * a.k + per - 1) / per;
+  const unsigned grid = (unsigned)(groups < kMostGroups ? groups : kMostGroups);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, s, a, lanes); };
-  if (a.k == 1) go(k_combine_backward<F32, 1>);
-  else if (a.k == 2) go(k_combine_backward<F32, 2>);
-  else if (a.k <= 4) go(k_combine_backward<F32, 4>);
+  if (pieces <= lanes) go(k_combine_backward<F32, 1>);
+  else if (pieces <= 2 * lanes) go(k_combine_backward<F32, 2>);
+  else if (pieces <= 4 * lanes) go(k_combine_backward<F32, 4>);
   else go(k_combine_backward<F32, 8>);
 }
 

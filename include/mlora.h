@@ -695,7 +695,8 @@ mlora_status mlora_route_backward(const mlora_router *router, const void *logits
  * mlora_combine_backward -- its gradients: dY [tokens * top_k][d] = weights_tj
  * dout_t (zero in slots that do not count) and dweights_tj = <dout_t,
  * Y[t top_k + j]> in fp32, a fixed order (0 in those slots); either may be
- * NULL.  Y may be NULL without dweights.  The gradient of add is dout itself.
+ * NULL.  Y may be NULL without dweights; dY may be Y.  The gradient of add is
+ * dout itself.
  */
 mlora_status mlora_combine(const void *Y, mlora_dtype dtype, int64_t tokens, int32_t top_k, int64_t d,
                            const int32_t *ids, int32_t n_experts, const float *weights, const void *add,

@@ -107,3 +107,31 @@ def test_logits_of_any_size(score):
         x[5] += 500
         x[6, :60] = -200
         check(x.cuda(), 6, score=score, renorm=False)
+
+
+@pytest.mark.parametrize("k,d", [(1, 64), (3, 1032), (8, 4104)])
+def test_combine_backward_in_place(k, d):
+    """dY over Y, and the same bits for any number of tokens."""
+    import torch
+    from adapter_lora_segments_amd import mlora_combine_backward
+    Y = torch.randn(300 * k, d, device="cuda").to(torch.bfloat16)
+    dout, w = torch.randn(300, d, device="cuda").to(torch.bfloat16), torch.rand(300, k, device="cuda")
+    ids = torch.randint(-1, 9, (300, k), device="cuda", dtype=torch.int32)
+    dY, dw = mlora_combine_backward(dout, Y, k, ids, w)
+    y2, w2 = mlora_combine_backward(dout[:5], Y[:5 * k], k, ids[:5], w[:5])
+    assert torch.equal(y2, dY[:5 * k]) and torch.equal(w2, dw[:5])
+    same, w3 = mlora_combine_backward(dout, Y, k, ids, w, dY=Y)
+    assert same is Y and torch.equal(Y, dY) and torch.equal(w3, dw)
+
+
+def test_combine_backward_of_more_slots_than_a_launch_has_waves():
+    import torch
+    from adapter_lora_segments_amd import mlora_combine_backward
+    T, k, d = (1 << 20) + 3, 64, 264
+    say(f"combine backward {T} x {k} x {d}")
+    dout = torch.randn(T, d, device="cuda").to(torch.bfloat16)
+    dY, none = mlora_combine_backward(dout, None, k)
+    assert none is None
+    for lo in (0, T // 2, T - 4):
+        assert torch.equal(dY.view(T, k, d)[lo:lo + 4], dout[lo:lo + 4, None].expand(4, k, d))
+    assert torch.equal(dY.view(T, k, d)[:, 63], dout)
