@@ -50,31 +50,23 @@ __device__ __forceinline__ u32x4 transpose_groups(const u32x4& w) {
   return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-template <int G>
-__device__ __forceinline__ float lanes_min(float v) {
-#pragma unroll
-  for (int d = 1; d < G; d <<= 1) v = fminf(v, __shfl_xor(v, d));
-  return v;
-}
-template <int G>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int d = 1; d < G; d <<= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-
 }  // namespace
 
-// Eight elements a lane, GROUP / 8 neighbouring lanes a group.  Bound by HBM.
+// Eight elements a lane, GROUP / 8 neighbouring lanes a group (`split` divides by
+// a row's eights).  Bound by HBM, once the arithmetic is short: an element's
+// quotient x / s rounded to fp32 comes from a product with 1 / s in 64 bits,
+// which rounds alike, since s has 8 bits and x 24: x / s is no nearer than 2^-34
+// of itself to the middle of two fp32 numbers.
 template <class T, int GROUP>
-__global__ __launch_bounds__(256) void k_affine_quantize(const T* X, int64_t rows, int cols, int64_t ld, bool symmetric,
-                                                       uint32_t* codes, uint32_t* params, T* values) {
+__global__ __launch_bounds__(256) void k_affine_quantize(const T* X, uint32_t n, DivBy split, int cols, int64_t ld,
+                                                       bool symmetric, uint32_t* codes, uint32_t* params, T* values) {
   constexpr int L = GROUP / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = rows * (cols / 8);
+  constexpr float kInf = __builtin_inff();
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
   // (cols / 8 is a multiple of L: a group's lanes are all in or all out)
   if (i >= n) return;
-  const int64_t r = i / (cols / 8);
-  const int c = (int)(i - r * (cols / 8)) * 8;
+  const uint32_t r = div_fast(i, split);
+  const int c = (int)(i - r * (uint32_t)(cols / 8)) * 8;
   float x[8];
   if constexpr (sizeof(T) == 4) {
     const u32x4* p = reinterpret_cast<const u32x4*>(X + r * ld + c);
@@ -93,33 +85,36 @@ __global__ __launch_bounds__(256) void k_affine_quantize(const T* X, int64_t row
     }
   }
   float lo = 0.f, hi = 0.f;
-  bool bad = false;
+  bool nan = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     lo = fminf(lo, x[j]);
     hi = fmaxf(hi, x[j]);
-    bad = bad || !(__builtin_fabsf(x[j]) <= 3.402823466e+38f);
+    nan = nan || x[j] != x[j];
   }
-  lo = lanes_min<L>(lo);
-  hi = lanes_max<L>(hi);
-  bad = lanes_max<L>(bad ? 1.f : 0.f) > 0.f;
+  hi = nan ? kInf : hi;
+  lo = across<L>(lo, [](float a, float b) { return fminf(a, b); });
+  hi = across<L>(hi, [](float a, float b) { return fmaxf(a, b); });
+  const bool bad = hi == kInf || lo == -kInf;
   const float s32 = symmetric ? fmaxf(hi, -lo) / 7.f : hi / 15.f - lo / 15.f;
   const uint32_t sb = pack_bf16x2(s32, s32) & 0xffffu;
   float s = __uint_as_float(sb << 16);
-  float z = symmetric ? 8.f : s > 0.f ? fminf(fmaxf(__builtin_rintf(-lo / s), 0.f), 15.f) : 0.f;
+  // (a group of zeros, or one whose scale underflows: code = zero point)
+  const double inv = s > 0.f ? 1.0 / (double)s : 0.0;
+  auto steps = [&](float v) { return __builtin_rintf((float)((double)v * inv)); };
+  float z = symmetric ? 8.f : fminf(fmaxf(steps(-lo), 0.f), 15.f);
   uint32_t word = 0;
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    // a group of zeros (or one whose scale underflows): code = zero point
-    const float t = s > 0.f ? __builtin_rintf(x[j] / s) : 0.f;
-    const float q = fminf(fmaxf(t + z, 0.f), 15.f);
-    word |= (uint32_t)(bad ? 0.f : q) << (4 * j);
+    const float q = fminf(fmaxf(steps(x[j]) + z, 0.f), 15.f);
+    word |= (uint32_t)q << (4 * j);
     v[j] = s * (q - z);
   }
   if (bad) {
     s = __uint_as_float(0x7fc00000u);
     z = 0.f;
+    word = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = s;
   }
@@ -127,12 +122,12 @@ __global__ __launch_bounds__(256) void k_affine_quantize(const T* X, int64_t row
   if ((threadIdx.x & (L - 1)) == 0) params[i / L] = (__float_as_uint(s) & 0xffff0000u) | (__float_as_uint(z) >> 16);
   if (values) {
     if constexpr (sizeof(T) == 4) {
-      u32x4* p = reinterpret_cast<u32x4*>(values + r * cols + c);
+      u32x4* p = reinterpret_cast<u32x4*>(values + (int64_t)r * cols + c);
       p[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
       p[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
     } else {
-      *reinterpret_cast<u32x4*>(values + r * cols + c) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      *reinterpret_cast<u32x4*>(values + (int64_t)r * cols + c) =
+          u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     }
   }
 }
@@ -322,11 +317,11 @@ namespace {
 template <class T>
 void quantize_of(const void* X, int64_t rows, int64_t cols, int64_t ld, int32_t group, bool symmetric, uint8_t* codes,
                  uint32_t* params, void* values, hipStream_t s) {
-  const dim3 grid((unsigned)((rows * (cols / 8) + 255) / 256));
+  const uint32_t n = (uint32_t)(rows * (cols / 8));      // (below 2^31)
   auto* c = reinterpret_cast<uint32_t*>(codes);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, static_cast<const T*>(X), rows, (int)cols, ld, symmetric, c,
-                       params, static_cast<T*>(values));
+    hipLaunchKernelGGL(kernel, dim3((n + 255) / 256), dim3(256), 0, s, static_cast<const T*>(X), n,
+                       div_by((int32_t)(cols / 8)), (int)cols, ld, symmetric, c, params, static_cast<T*>(values));
   };
   if (group == 32) go(k_affine_quantize<T, 32>);
   else if (group == 64) go(k_affine_quantize<T, 64>);

@@ -67,27 +67,6 @@ __device__ __forceinline__ float clamp(float x, float lo, float hi) {     // NaN
 // (e^700 has a reciprocal; what is below counts as zero, which it is in fp32)
 __device__ __forceinline__ double sigmoid64(float x) { return reciprocal(1.0 + exp64(-(double)clamp(x, -700.f, 700.f))); }
 
-// Exchanges within L lanes.  Each step pairs groups that already agree, so any
-// lane of the other group will do: within 16 lanes DPP moves, then swaps of
-// rows.
-template <int STEP>
-__device__ __forceinline__ uint32_t other(uint32_t v) {
-  if constexpr (STEP == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);         // quad 1 0 3 2
-  else if constexpr (STEP == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);    // quad 2 3 0 1
-  else if constexpr (STEP == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);   // mirror of 8
-  else if constexpr (STEP == 8) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);   // mirror of 16
-  else return __shfl_xor((int)v, STEP);
-}
-template <int STEP>
-__device__ __forceinline__ double other(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = other<STEP>((uint32_t)b), hi = other<STEP>((uint32_t)(b >> 32));
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-template <int STEP>
-__device__ __forceinline__ float other(float v) {
-  return __uint_as_float(other<STEP>(__float_as_uint(v)));
-}
 // max and min of keys (no NaN among them)
 __device__ __forceinline__ double key_max(double a, double b) {
   double r;
@@ -98,11 +77,6 @@ __device__ __forceinline__ double key_min(double a, double b) {
   double r;
   asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
   return r;
-}
-template <int L, int STEP = 1, class T, class OP>
-__device__ __forceinline__ T across(T v, OP op) {
-  if constexpr (STEP < L) return across<L, 2 * STEP>(op(v, other<STEP>(v)), op);
-  else return v;
 }
 template <int L>
 __device__ __forceinline__ double group_sum(double v) {
