@@ -56,7 +56,8 @@ __device__ __forceinline__ u32x4 transpose_groups(const u32x4& w) {
 // a row's eights).  Bound by HBM, once the arithmetic is short: an element's
 // quotient x / s rounded to fp32 comes from a product with 1 / s in 64 bits,
 // which rounds alike, since s has 8 bits and x 24: x / s is no nearer than 2^-34
-// of itself to the middle of two fp32 numbers.
+// of itself to the middle of two fp32 numbers.  14336 x 4096 in bf16 with values
+// 43 us (6.2 TB/s; 59 with divisions), without 36; fp32 91 and 44 us.
 template <class T, int GROUP>
 __global__ __launch_bounds__(256) void k_affine_quantize(const T* X, uint32_t n, DivBy split, int cols, int64_t ld,
                                                        bool symmetric, uint32_t* codes, uint32_t* params, T* values) {
@@ -132,7 +133,8 @@ __global__ __launch_bounds__(256) void k_affine_quantize(const T* X, uint32_t n,
   }
 }
 
-// Eight weights a lane.  Bound by HBM.
+// Eight weights a lane.  Bound by HBM, four fifths of it stores: 14336 x 4096 30 us
+// (4.9 TB/s).
 template <int GROUP>
 __global__ __launch_bounds__(256) void k_affine_decode(const uint32_t* codes, const uint32_t* params, int64_t n,
                                                      u32x4* out) {
@@ -160,6 +162,12 @@ __global__ __launch_bounds__(256) void k_affine_decode(const uint32_t* codes, co
 // column, so a group's scale and zero point are the lane's own.  With groups
 // under 128 the words of a piece are exchanged between the lane groups, so that
 // a step's 32 inputs lie in one group.
+// What bounds it: one round of loads, decoded when they come (vector instructions
+// busy 30 to 40%, matrix ones 9%, HBM half).  K = 4096: 1 row, N = 14336 10.0 us
+// (3.1 TB/s), 16 rows 12.5; 32 rows over 8 experts, N = 4096, groups of 64 21.8
+// us (3.5 TB/s).  Asking for the next four pieces before these are multiplied
+// did not gain (more registers, fewer waves), nor did weights before activations
+// (10.6 us).
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
 template <int GROUP, int RB, int NB, int CS>

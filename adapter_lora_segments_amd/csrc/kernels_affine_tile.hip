@@ -12,6 +12,15 @@
 // inputs, the step's blocks 2 u + h for u = 0, 1; word q of them and chunk
 // 8 u + 4 h + q of the activations make one matrix instruction's 16 inputs.
 // A block of 32 lies in one group, so its scale is the lane's own.
+//
+// Bound by issue: a step's matrix instructions, decoding (1.5 vector
+// instructions a weight) and LDS reads (each wave reads all activations) take
+// about as long as each other, and two or three waves a SIMD overlap them in
+// part.  A full chip does 0.9 PF in tiles of 128 rows and 0.76 PF in tiles of 64.
+// 4096 rows over 32 experts, 4096 -> 1024 66 us (640 tiles of 64 rows, a fifth
+// of them padding); 2048 rows over 8 experts, 4096 -> 4096 76 us (0.9 PF); 64
+// rows, 4096 -> 14336 25 us.  In copies of the kernel: without the stores to LDS
+// 47 -> 39 us, without decoding 55 -> 42 (64-row tiles) and no gain (128).
 #include "affine_choice.hpp"
 #include "expert_common.hpp"
 
@@ -244,6 +253,10 @@ __global__ __launch_bounds__(256 * KS, 2) void k_affine_tile(ExpertArgs a) {
 // Both in two buffers: while step s is multiplied, step s + 1's are written and
 // step s + 2's loads are in flight.  One slice of a step: 16 rows of the
 // weight; lane c + 32 h takes rows 8 h .. 8 h + 7 of column c.
+// 1501 rows over 4 experts of 4096 x 4096, groups of 32 79 us (101 with the weights
+// decoded to memory first), 512 rows over 8 36 us (133).  Bound as the kernel above: matrix
+// instructions are busy 29%, vector ones 28%, the rest waits for LDS and for the
+// tile that is twice on one CU.
 template <int GROUP, int FI, int KS>
 __global__ __launch_bounds__(256 * KS, 2) void k_affine_dx(ExpertArgs a) {
   constexpr int BM = 32 * FI, BN = 128, KD = 64, NP = BM / 32, D = 2;

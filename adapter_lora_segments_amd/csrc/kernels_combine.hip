@@ -3,7 +3,8 @@
 //   dY[t k + j] = w_tj dout_t,   dw_tj = sum_i dout_ti Y[t k + j][i]
 // over the slots j that a router filled; a dropped slot's row is not read (it
 // may hold anything) and gets a zero gradient.  Sums in fp32, one rounding.
-// One pass over the data, 16 bytes a lane and row, bound by HBM.
+// One pass over the data, 16 bytes a lane and row, bound by HBM: 16384 tokens of 8
+// rows of 4096 in bf16 224 us, 5.4 TB/s; 16 tokens of 2 2.4 us, a launch.
 #include "device_common.hpp"
 #include "route.hpp"
 
@@ -87,7 +88,10 @@ __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a, int lanes, 
 // of U pieces of dout and of its row of Y in flight; the slots of a token read
 // dout once each, all but the first from the caches.  A lane's pieces are added
 // in order and the lanes meet by exchanges, the same ones for any number of
-// tokens and slots.
+// tokens and slots.  7681 tokens of 2 rows of 4104 in bf16 55 us (5.7 TB/s), of 8
+// rows of 4096 (16384 tokens) 400 us (5.7 TB/s), 35 tokens of 8 rows of 8072 in
+// fp32 8 us; all slots of a token by one wave took 64, 490 and 64 us: fewer
+// loads in flight, since a store may be to what a later load reads.
 template <bool F32, int U>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineArgs a, int lanes) {
   constexpr int N = Piece<F32>::N;

@@ -9,6 +9,13 @@
 // for scores within 2^-45 of a rounding border.  A choice compares score + bias,
 // in fp32, with the expert's number in the 29 bits that fp32 leaves of a double,
 // so a step of the top_k is a maximum, and ties go to the lowest expert.
+//
+// Bound by instructions, not by the logits' bytes: 32768 rows of 256, sigmoid, 8
+// of 256 out of 4 of 8 groups, fp32 take 21.9 us (1.5 TB/s; 18.3 without
+// groups), of which about 24 instructions an expert are its score, 9 its key and
+// 19 sorting; 32768 rows of 64 in bf16, 2 or 8 chosen, 6.6 and 7.4 us; 16 rows of
+// 64 3.2 us, a launch.  With 32 experts a lane in place of 16 the groups' case
+// took as long (fewer exchanges, fewer waves).
 #include "device_common.hpp"
 #include "route.hpp"
 
@@ -354,7 +361,8 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
     }
   }
 
-  // The sorted eight pay from the fifth expert on.
+  // The sorted eight pay from the fifth expert on (32768 rows of 64: two chosen one by one
+  // 6.6 us, eight by sorting 7.4).
   bool done = false;
   if constexpr (V % 8 == 0) {
     if (a.k > 4 && a.k <= 8) {
@@ -404,7 +412,9 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
 // forward made; any ids are taken).  DENSE: softmax weights that are not
 // renormalised, where every expert's score enters.  Else the chosen logits are
 // all that is read: sum_j du_j u_j is zero, and the scores' common factor
-// cancels in u / S.  LDS: the row's gradient [E].
+// cancels in u / S.  LDS: the row's gradient [E].  16384 rows of 64 in bf16 6.8
+// us dense and 5.1 not (the chosen slots' serial work), of 256 in fp32, sigmoid,
+// 9.3 us (3.6 TB/s).
 template <class T, int L, int V, bool DENSE>
 __global__ __launch_bounds__(kThreads<V>) void k_route_backward(RouteArgs a, int whole) {
   extern __shared__ float grad[];
@@ -519,7 +529,8 @@ void route_of(bool back, const RouteArgs& a, hipStream_t s) {
   }
 }
 
-// Rows up to which a row takes a whole wave.
+// Rows up to which a row takes a whole wave: 1024 waves, one for each of the
+// chip's SIMDs (16 rows of 64 with eight lanes a row 7.0 us, with 64 3.9).
 constexpr int64_t kFewRows = 1024;
 
 template <class T>
