@@ -161,13 +161,18 @@ __device__ __forceinline__ Soft softmax_terms(const float (&x)[V], double (&e)[V
   return s;
 }
 
-// Lane `sub`'s experts sub V .. of a row (-infinity past the last); whole: all
-// lanes are full and 16-byte aligned.
+// Lane `sub`'s experts sub V .. of a row (-infinity past the last); whole: each
+// lane's are all there or all past it, and 16-byte aligned.
 template <class T, int V>
 __device__ __forceinline__ void load_row(const T* p, int E, int sub, bool whole, float (&x)[V]) {
   constexpr int P = 16 / sizeof(T);
   if constexpr (V % P == 0) {
     if (whole) {
+      if (sub * V >= E) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = kNone;
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < V / P; ++i) {
         const u32x4 u = reinterpret_cast<const u32x4*>(p + sub * V)[i];
@@ -513,8 +518,8 @@ template <class T, int L, int V>
 void route_of(bool back, const RouteArgs& a, hipStream_t s) {
   constexpr int R = kThreads<V> / L;
   const unsigned grid = (unsigned)((a.rows + R - 1) / R);
-  // rows that start and end on 16 bytes and fill every lane
-  const bool whole = a.E == L * V && a.E * sizeof(T) % 16 == 0 && a.ld * sizeof(T) % 16 == 0 && aligned16(a.logits) &&
+  // rows that start and end on 16 bytes and fill the lanes that they reach
+  const bool whole = a.E % V == 0 && a.E * sizeof(T) % 16 == 0 && a.ld * sizeof(T) % 16 == 0 && aligned16(a.logits) &&
                      aligned16(a.dlogits);
   if (back) {
     const size_t lds = (size_t)R * a.E * 4;
@@ -525,7 +530,7 @@ void route_of(bool back, const RouteArgs& a, hipStream_t s) {
   } else {
     const size_t lds = (size_t)R * 4 * (a.k + (a.n_groups > 1 ? a.E + a.n_groups : 0));
     hipLaunchKernelGGL((k_route<T, L, V>), dim3(grid), dim3(kThreads<V>), lds, s, a, whole,
-                       a.E == L * V && a.E % 4 == 0 && aligned16(a.bias));
+                       a.E % V == 0 && a.E % 4 == 0 && aligned16(a.bias));
   }
 }
 

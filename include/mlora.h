@@ -634,8 +634,9 @@ mlora_status mlora_microscale_quantize(const void *X, mlora_dtype dtype, int64_t
  * equal scores to the lowest group.  ids [rows][top_k]: the experts of the
  * largest c, falling, equal values to the lowest expert.  weights [rows]
  * [top_k] fp32: scale s, or with renormalize scale s / (sum of the chosen s)
- * (from the 64-bit scores; a sum of 0 divides by 1).  The bias enters the
- * choice only.
+ * (from the 64-bit scores; a sum of 0 divides by 1, and a sigmoid of less than
+ * -700 or a softmax term e^-800 below its row's largest counts as 0).  The bias
+ * enters the choice only.
  *
  * An expert whose logit or c is -infinity is never chosen (a mask, a row of
  * padding); slots with no expert left have id -1 and weight 0, which

@@ -26,7 +26,7 @@ def check(x, k, bias=None, **kw):
     return r, ids, w
 
 
-@pytest.mark.parametrize("E", [1, 5, 8, 13, 16, 31, 32, 60, 64, 97, 128, 200, 256, 500, 512])
+@pytest.mark.parametrize("E", [1, 5, 8, 13, 16, 31, 32, 40, 60, 64, 97, 128, 160, 192, 200, 256, 384, 500, 512])
 def test_many_rows(E):
     import torch
     say(f"route many rows {E}")
@@ -51,7 +51,7 @@ def test_many_rows_in_groups(E, G, tg, score):
                     torch.randn(E, device="cuda") * 0.2, score=score, groups=G, top_groups=tg, group_score=gs)
 
 
-@pytest.mark.parametrize("E", [8, 30, 64, 128, 256, 512])
+@pytest.mark.parametrize("E", [8, 30, 48, 64, 128, 192, 256, 384, 512])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_many_rows_backward(E, renorm, score):
