@@ -35,3 +35,38 @@ def test_dense_gradient_of_saturated_rows(E, k, rows, dt):
     bound = (HALF[dt] + 2.0 ** -24) * np.abs(want) + 2.0 ** -47 * terms + 2.0 ** -140
     err = np.abs(host(r.backward(x, ids, dw)) - want)
     assert (err <= bound).all(), (err / bound).max()
+
+
+# Rows of 64 logits in eighths and a scale 1 + m 2^-23 whose scores lie so near a
+# border of fp32 that a sum of the 64 terms in another order rounds to the other side.
+NEAR = [(False, 4190641, [
+    -13, 19, 10, -11, 8, -12, -17, 0, 11, -5, -9, 3, -8, 6, 28, -5, 8, 3, -2, 12, 11, 3, -3, 21, -24, -17, 15, -8, 0, 20, -8,
+    0, 3, 4, 24, 29, -20, -13, 5, -8, 8, -1, 0, -21, 20, -10, 19, 3, 6, -10, 0, 23, 1, -21, -5, -12, -5, -3, -4, 0, 11, 10,
+    15, -27]), (False, 6911962, [
+    10, 7, 14, 19, -18, 8, -6, -5, -18, -3, 9, -8, 7, 3, -2, 6, 11, -13, 0, 11, -18, -5, 12, -9, -20, -27, 9, 16, -10, -12,
+    -13, -25, 0, 6, 16, 2, -5, -4, -8, -11, 31, -11, -8, -5, 23, -1, -22, -9, -8, 10, -22, -11, 17, 10, 3, -1, 11, 16, 23, 4,
+    2, 1, 21, -4]), (True, 2010098, [
+    5, -8, 8, 23, 12, -11, 6, 7, 14, -5, -9, 5, -2, -17, 16, 1, -2, 9, 10, 11, 7, 19, 11, -17, -7, -4, 5, -13, -15, 16, 8,
+    -7, -3, 15, -23, 6, -26, -15, 5, 7, 4, -25, -4, -11, -4, -5, -5, -9, 8, -25, 13, 3, -10, 11, 2, 11, 3, 7, -8, 2, 18, 4,
+    -8, -8]), (True, 6250845, [
+    -14, 11, -4, -22, -10, 14, -5, 12, 28, 15, -21, 24, -9, -25, 3, 12, -5, -9, 3, -9, 6, -23, -5, -27, -21, -18, 3, 3, -3,
+    -7, -7, -20, -6, -4, 1, 13, 9, -3, 14, -23, -2, -7, 6, 17, -11, -2, 10, -8, -10, -19, -23, 6, 1, 6, 14, 18, 14, 12, -6,
+    10, -8, -4, -16, -16])]
+
+
+@pytest.mark.parametrize("case", range(len(NEAR)))
+def test_sums_do_not_depend_on_lanes(case):
+    """All 64 experts chosen, in a call of 3 rows (64 lanes a row) and of 1100 (8
+    lanes): the same bits."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    renorm, m, eighths = NEAR[case]
+    x = torch.tensor([eighths], dtype=torch.float32, device="cuda") / 8
+    r = Router(64, 64, renormalize=renorm, scale=1 + m * 2.0 ** -23)
+    ids, w = r.route(x.expand(3, 64).contiguous())
+    i2, w2 = r.route(x.expand(1100, 64).contiguous())
+    assert torch.equal(i2, ids[:1].expand(1100, 64)) and torch.equal(w2, w[:1].expand(1100, 64))
+    dw = torch.randn(1, 64, device="cuda")
+    d = r.backward(x.expand(3, 64).contiguous(), ids, dw.expand(3, 64).contiguous())
+    d2 = r.backward(x.expand(1100, 64).contiguous(), i2, dw.expand(1100, 64).contiguous())
+    assert torch.equal(d2, d[:1].expand(1100, 64))
