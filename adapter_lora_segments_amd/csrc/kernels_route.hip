@@ -495,7 +495,7 @@ __global__ __launch_bounds__(kThreads<V>) void k_route_backward(RouteArgs a, int
     return TwoSums{u, (double)dw[j] * u};
   });
   const double S = group_sum<L>(sums.a), dot = group_sum<L>(sums.b);
-  const double f = a.renorm ? (S == 0.0 ? 0.0 : (double)a.scale / S) : (double)a.scale;
+  const double inv = a.renorm ? (S == 0.0 ? 0.0 : 1.0 / S) : 1.0;
   const double less = a.renorm && S != 0.0 ? dot / S : 0.0;
   __syncthreads();
   // of slots that name one expert the first adds them all, in order
@@ -514,7 +514,9 @@ __global__ __launch_bounds__(kThreads<V>) void k_route_backward(RouteArgs a, int
       const float l = load_logit(p + id);
       const double s = score_of(a, sm, l);
       // (an expert at -infinity has no gradient, whatever the others hold)
-      sum = l == kNone ? 0.0 : a.sigmoid ? sum * f * s * (1.0 - s) : sum * f * s;
+      // (s / S first: S may be as little as e^-700)
+      sum *= (double)a.scale * (s * inv);
+      sum = l == kNone ? 0.0 : a.sigmoid ? sum * (1.0 - s) : sum;
     }
     du[id] = (float)sum;
   }

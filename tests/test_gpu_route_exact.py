@@ -70,3 +70,31 @@ def test_sums_do_not_depend_on_lanes(case):
     d = r.backward(x.expand(3, 64).contiguous(), ids, dw.expand(3, 64).contiguous())
     d2 = r.backward(x.expand(1100, 64).contiguous(), i2, dw.expand(1100, 64).contiguous())
     assert torch.equal(d2, d[:1].expand(1100, 64))
+
+
+@pytest.mark.parametrize("rows", [4, 1100])
+@pytest.mark.parametrize("low", [-80.0, -600.0, -699.0])
+def test_sigmoid_gradient_of_tiny_sums(low, rows):
+    """Renormalised sigmoid scores of e^-699, chosen by a bias (in fp32 they are all
+    zero): a score over their sum is of ordinary size, whatever the sum is.  As
+    before, with the terms p sum |g| that cancel."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    E, k = 12, 3
+    x = torch.full((rows, E), low)
+    x[:, 2], x[:, 7] = low + 0.5, low + 0.25
+    r = Router(E, k, score="sigmoid", scale=2.5)
+    bias = torch.zeros(E)
+    bias[2], bias[7], bias[0] = 3, 2, 1
+    ids, w = r.route(x.cuda(), bias.cuda())
+    assert (ids.cpu() == torch.tensor([2, 7, 0])).all()
+    at = [2, 7, 0]
+    s = 1 / (1 + np.exp(-host(x)[:, at]))
+    p = s / s.sum(axis=1, keepdims=True)
+    dw = torch.randn(rows, k, device="cuda") * 1e6
+    h = host(dw)
+    want, terms = np.zeros((rows, E)), np.zeros((rows, E))
+    want[:, at] = 2.5 * p * (1 - s) * (h - (h * p).sum(axis=1, keepdims=True))
+    terms[:, at] = 2.5 * p * 2 * np.abs(h).sum(axis=1, keepdims=True)
+    err = np.abs(host(r.backward(x.cuda(), ids, dw)) - want)
+    assert (err <= 2.0 ** -24 * np.abs(want) + 2.0 ** -47 * terms).all()
