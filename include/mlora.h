@@ -633,10 +633,12 @@ mlora_status mlora_microscale_quantize(const void *X, mlora_dtype dtype, int64_t
  * (MLORA_GROUP_TOP2; the largest alone if one expert only can be chosen),
  * equal scores to the lowest group.  ids [rows][top_k]: the experts of the
  * largest c, falling, equal values to the lowest expert.  weights [rows]
- * [top_k] fp32: scale s, or with renormalize scale s / (sum of the chosen s)
- * (from the 64-bit scores; a sum of 0 divides by 1, and a sigmoid of less than
- * -700 or a softmax term e^-800 below its row's largest counts as 0).  The bias
- * enters the choice only.
+ * [top_k] fp32: scale s, or with renormalize scale s / (sum of the chosen s),
+ * from the 64-bit scores.  A sigmoid of less than -700 counts as 0, and a sum of
+ * 0 divides by 1; a softmax term e^-800 below its row's largest counts as 0
+ * without renormalize, and with it the weights are the softmax of the chosen
+ * logits, however far those lie below the row's largest.  The bias enters the
+ * choice only.
  *
  * An expert whose logit or c is -infinity is never chosen (a mask, a row of
  * padding); slots with no expert left have id -1 and weight 0, which
@@ -672,7 +674,9 @@ mlora_status mlora_route(const mlora_router *router, const void *logits, mlora_d
  *   softmax: dlogit_e = s_e (du_e - sum_j du_j u_j)
  *   sigmoid: dlogit_e = s_e (1 - s_e) du_e
  * where du_e is the sum over the slots of e.  Slots whose id names no expert
- * have no part.  An expert at -infinity gets 0.  dlogits may be the logits
+ * have no part.  But for a softmax that is not renormalized the chosen logits
+ * are all that is read: a NaN or an infinity elsewhere in the row, which made
+ * the weights of a renormalized softmax NaN, does not reach this gradient.  An expert at -infinity gets 0.  dlogits may be the logits
  * themselves when ld = n_experts. */
 mlora_status mlora_route_backward(const mlora_router *router, const void *logits, mlora_dtype dtype,
                                   int64_t rows, int64_t ld, const int32_t *ids, const float *dweights,

@@ -98,3 +98,52 @@ def test_sigmoid_gradient_of_tiny_sums(low, rows):
     terms[:, at] = 2.5 * p * 2 * np.abs(h).sum(axis=1, keepdims=True)
     err = np.abs(host(r.backward(x.cuda(), ids, dw)) - want)
     assert (err <= 2.0 ** -24 * np.abs(want) + 2.0 ** -47 * terms).all()
+
+
+@pytest.mark.parametrize("rows", [4, 1100])
+@pytest.mark.parametrize("gap", [3.0, 690.0, 720.0, 744.0, 760.0, 1e30])
+def test_chosen_scores_far_below_the_largest(gap, rows):
+    """A bias that chooses experts whose scores are next to nothing beside the row's
+    largest: renormalised weights are the softmax of the chosen logits however far
+    down they lie, and the gradient is those weights'."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    E, k = 16, 3
+    x = torch.zeros(rows, E)
+    d = torch.tensor([0.0, 1.5, -2.0]) if gap < 1e3 else torch.zeros(3)
+    x[:, 4:7] = d - gap
+    bias = torch.zeros(E)
+    bias[4:7] = torch.tensor([4.0, 3.0, 2.0])
+    r = Router(E, k, scale=1.5)
+    ids, w = r.route(x.cuda(), bias.cuda())
+    assert (ids.cpu() == torch.tensor([4, 5, 6])).all()
+    p = np.exp(host(x[:, 4:7]) - host(x[:, 4:7]).max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    assert (np.abs(host(w) - 1.5 * p) <= 2.0 ** -24 * 1.5 * p * (1 + 2.0 ** -20)).all()
+    dw = torch.randn(rows, k, device="cuda")
+    h = host(dw)
+    want = np.zeros((rows, E))
+    want[:, 4:7] = 1.5 * p * (h - (h * p).sum(axis=1, keepdims=True))
+    terms = np.zeros((rows, E))
+    terms[:, 4:7] = 1.5 * p * 2 * np.abs(h).sum(axis=1, keepdims=True)
+    err = np.abs(host(r.backward(x.cuda(), ids, dw)) - want)
+    assert (err <= 2.0 ** -24 * np.abs(want) + 2.0 ** -47 * terms).all()
+
+
+@pytest.mark.parametrize("rows", [2, 1100])
+def test_renormalised_softmax_of_a_row_that_is_not_finite(rows):
+    """A NaN or an infinity among the logits makes every weight of the row NaN, chosen
+    or not; the gradient is of the chosen logits alone."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    x = torch.zeros(rows, 16)
+    x[:, 3] = torch.tensor([float("nan"), float("inf")] * (rows // 2))
+    x[rows - 1] = 0.0
+    r = Router(16, 3)
+    ids, w = r.route(x.cuda())
+    assert torch.isnan(w[:-1]).all() and (ids.cpu() == torch.tensor([0, 1, 2])).all()
+    assert torch.equal(w[-1], w.new_full((3,), 1 / 3))
+    d = r.backward(x.cuda(), ids, torch.tensor([[3.0, 0.0, 0.0]], device="cuda").expand(rows, 3).contiguous())
+    want = torch.zeros(16)
+    want[:3] = torch.tensor([2 / 3, -1 / 3, -1 / 3])
+    assert torch.allclose(d.cpu(), want.expand(rows, 16), rtol=1e-6, atol=0)
