@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/mlora.h"
+#include "api_common.hpp"
 #include "kernels.hpp"
 #include "plan.hpp"
 

@@ -4,34 +4,17 @@
 #include <hip/hip_runtime.h>
 
 #include <new>
-#include <string>
 
 #include "../../include/mlora.h"
+#include "api_common.hpp"
 #include "experts.hpp"
 #include "kernels.hpp"
 
 namespace {
 
-// No exception leaves a C entry, not even from building a message.
-mlora_status fail(mlora_status st, const char* msg) noexcept {
-  try {
-    mlora::set_last_error(msg);
-  } catch (...) {
-  }
-  return st;
-}
-
-mlora_status launched() noexcept {
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return MLORA_OK;
-  try {
-    mlora::set_last_error(std::string("kernel launch: ") + hipGetErrorName(e) + " (" + hipGetErrorString(e) + ")");
-  } catch (...) {
-  }
-  return MLORA_ERR_HIP;
-}
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+using mlora::api_aligned;
+using mlora::api_fail;
+using mlora::api_launched;
 
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 using mlora::kMaxGrid;
@@ -93,14 +76,14 @@ int64_t dw_ws(const mlora_expert_shape& s) {
 
 mlora_status check_call(const mlora_expert_shape* s, const int32_t* offsets, const int32_t* order, void* ws,
                         size_t ws_bytes, int64_t need) {
-  if (!offsets && s->n_experts != 1) return fail(MLORA_ERR_INVALID_ARG, "expert: offsets may be NULL with one expert only");
+  if (!offsets && s->n_experts != 1) return api_fail(MLORA_ERR_INVALID_ARG, "expert: offsets may be NULL with one expert only");
   if (!order && (s->x_by_order || s->y_by_order))
-    return fail(MLORA_ERR_INVALID_ARG, "expert: x_by_order and y_by_order need order");
-  if (!aligned(offsets, 4) || !aligned(order, 4))
-    return fail(MLORA_ERR_INVALID_ARG, "expert: offsets and order must be 4-byte aligned");
+    return api_fail(MLORA_ERR_INVALID_ARG, "expert: x_by_order and y_by_order need order");
+  if (!api_aligned(offsets, 4) || !api_aligned(order, 4))
+    return api_fail(MLORA_ERR_INVALID_ARG, "expert: offsets and order must be 4-byte aligned");
   if (need > 0) {
-    if (!ws || !aligned(ws, 16)) return fail(MLORA_ERR_INVALID_ARG, "expert: workspace must be non-NULL and 16-byte aligned");
-    if ((uint64_t)ws_bytes < (uint64_t)need) return fail(MLORA_ERR_WORKSPACE, "expert: workspace too small");
+    if (!ws || !api_aligned(ws, 16)) return api_fail(MLORA_ERR_INVALID_ARG, "expert: workspace must be non-NULL and 16-byte aligned");
+    if ((uint64_t)ws_bytes < (uint64_t)need) return api_fail(MLORA_ERR_WORKSPACE, "expert: workspace too small");
   }
   return MLORA_OK;
 }
@@ -119,10 +102,10 @@ mlora::ExpertArgs base_args(const mlora_expert_shape& s, const int32_t* offsets,
 extern "C" {
 
 mlora_status mlora_group_rows_workspace(int64_t rows, int32_t n_groups, int64_t* bytes) {
-  if (!bytes) return fail(MLORA_ERR_INVALID_ARG, "group_rows: bytes is NULL");
-  if (rows < 0 || rows > kMaxRows) return fail(MLORA_ERR_INVALID_ARG, "group_rows: rows must be in [0, 2^31)");
+  if (!bytes) return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: bytes is NULL");
+  if (rows < 0 || rows > kMaxRows) return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: rows must be in [0, 2^31)");
   if (n_groups < 1 || n_groups > MLORA_MAX_EXPERTS)
-    return fail(MLORA_ERR_INVALID_ARG, "group_rows: n_groups must be in [1, 4096]");
+    return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: n_groups must be in [1, 4096]");
   // the most parts any smaller number of rows takes
   const int64_t parts = (rows + mlora::kGroupMinPart - 1) / mlora::kGroupMinPart;
   *bytes = rows <= mlora::kGroupOneLaunch
@@ -137,23 +120,23 @@ mlora_status mlora_group_rows(const int32_t* ids, int64_t rows, int32_t n_groups
   const mlora_status st = mlora_group_rows_workspace(rows, n_groups, &need);
   if (st != MLORA_OK) return st;
   if (!offsets || (rows > 0 && (!ids || !order)))
-    return fail(MLORA_ERR_INVALID_ARG, "group_rows: ids, offsets and order must be non-NULL");
-  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4))
-    return fail(MLORA_ERR_INVALID_ARG, "group_rows: ids, offsets and order must be 4-byte aligned");
+    return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: ids, offsets and order must be non-NULL");
+  if (!api_aligned(ids, 4) || !api_aligned(offsets, 4) || !api_aligned(order, 4))
+    return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: ids, offsets and order must be 4-byte aligned");
   if (need > 0) {
-    if (!workspace || !aligned(workspace, 16))
-      return fail(MLORA_ERR_INVALID_ARG, "group_rows: workspace must be non-NULL and 16-byte aligned");
-    if ((uint64_t)ws_bytes < (uint64_t)need) return fail(MLORA_ERR_WORKSPACE, "group_rows: workspace too small");
+    if (!workspace || !api_aligned(workspace, 16))
+      return api_fail(MLORA_ERR_INVALID_ARG, "group_rows: workspace must be non-NULL and 16-byte aligned");
+    if ((uint64_t)ws_bytes < (uint64_t)need) return api_fail(MLORA_ERR_WORKSPACE, "group_rows: workspace too small");
   }
   mlora::launch_group_rows(ids, rows, n_groups, offsets, order, static_cast<int32_t*>(workspace),
                            static_cast<hipStream_t>(stream));
-  return launched();
+  return api_launched();
 }
 
 mlora_status mlora_expert_workspace(const mlora_expert_shape* shape, int64_t* bytes) {
-  if (!shape || !bytes) return fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
+  if (!shape || !bytes) return api_fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
   mlora_status st;
-  if (const char* msg = shape_error(*shape, &st)) return fail(st, msg);
+  if (const char* msg = shape_error(*shape, &st)) return api_fail(st, msg);
   // a weight is quantized (dX only) or has a dW
   const int64_t f = forward_ws(*shape), b = dx_ws(*shape) + dw_ws(*shape);
   *bytes = f > b ? f : b;
@@ -161,9 +144,9 @@ mlora_status mlora_expert_workspace(const mlora_expert_shape* shape, int64_t* by
 }
 
 mlora_status mlora_expert_forward_workspace(const mlora_expert_shape* shape, int64_t* bytes) {
-  if (!shape || !bytes) return fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
+  if (!shape || !bytes) return api_fail(MLORA_ERR_INVALID_ARG, "expert: shape and bytes must be non-NULL");
   mlora_status st;
-  if (const char* msg = shape_error(*shape, &st)) return fail(st, msg);
+  if (const char* msg = shape_error(*shape, &st)) return api_fail(st, msg);
   *bytes = forward_ws(*shape);
   return MLORA_OK;
 }
@@ -171,15 +154,15 @@ mlora_status mlora_expert_forward_workspace(const mlora_expert_shape* shape, int
 mlora_status mlora_expert_forward(const mlora_expert_shape* shape, const void* X, const void* W,
                                   const int32_t* offsets, const int32_t* order, void* Y, void* workspace,
                                   size_t ws_bytes, void* stream) {
-  if (!shape) return fail(MLORA_ERR_INVALID_ARG, "expert: shape is NULL");
+  if (!shape) return api_fail(MLORA_ERR_INVALID_ARG, "expert: shape is NULL");
   const mlora_expert_shape& s = *shape;
   mlora_status st;
-  if (const char* msg = shape_error(s, &st)) return fail(st, msg);
+  if (const char* msg = shape_error(s, &st)) return api_fail(st, msg);
   st = check_call(shape, offsets, order, workspace, ws_bytes, s.rows > 0 ? forward_ws(s) : 0);
   if (st != MLORA_OK) return st;
-  if (!W || (s.rows > 0 && (!X || !Y))) return fail(MLORA_ERR_INVALID_ARG, "expert forward: X, W and Y must be non-NULL");
+  if (!W || (s.rows > 0 && (!X || !Y))) return api_fail(MLORA_ERR_INVALID_ARG, "expert forward: X, W and Y must be non-NULL");
   for (const void* p : {X, W, (const void*)Y})
-    if (!aligned(p, 16)) return fail(MLORA_ERR_INVALID_ARG, "expert forward: device pointers must be 16-byte aligned");
+    if (!api_aligned(p, 16)) return api_fail(MLORA_ERR_INVALID_ARG, "expert forward: device pointers must be 16-byte aligned");
   if (s.rows == 0) return MLORA_OK;
 
   hipStream_t cs = static_cast<hipStream_t>(stream);
@@ -208,7 +191,7 @@ mlora_status mlora_expert_forward(const mlora_expert_shape* shape, const void* X
       uint8_t* codes = static_cast<uint8_t*>(workspace);
       uint8_t* scales = codes + round16(t * s.d_in / 2);
       mlora::launch_quant_mx4(false, false, X, t, s.d_in, s.d_in, codes, scales, nullptr, cs);
-      st = launched();
+      st = api_launched();
       if (st != MLORA_OK) return st;
       a.A = codes;
       a.a_scale = scales;
@@ -216,25 +199,25 @@ mlora_status mlora_expert_forward(const mlora_expert_shape* shape, const void* X
     }
   }
   mlora::launch_expert_rows(form, nk, a, cs);
-  return launched();
+  return api_launched();
 }
 
 mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* dY, const void* X, const void* W,
                                    const int32_t* offsets, const int32_t* order, void* dX, float* dW,
                                    void* workspace, size_t ws_bytes, void* stream) {
-  if (!shape) return fail(MLORA_ERR_INVALID_ARG, "expert: shape is NULL");
+  if (!shape) return api_fail(MLORA_ERR_INVALID_ARG, "expert: shape is NULL");
   const mlora_expert_shape& s = *shape;
   mlora_status st;
-  if (const char* msg = shape_error(s, &st)) return fail(st, msg);
+  if (const char* msg = shape_error(s, &st)) return api_fail(st, msg);
   const bool w4 = s.w_format == MLORA_W0_MXFP4;
   const bool want_dx = dX != nullptr && s.rows > 0;
   st = check_call(shape, offsets, order, workspace, ws_bytes, (want_dx ? dx_ws(s) : 0) + (dW ? dw_ws(s) : 0));
   if (st != MLORA_OK) return st;
-  if (w4 && dW) return fail(MLORA_ERR_UNSUPPORTED, "expert backward: an MXFP4 weight is frozen, dW must be NULL");
+  if (w4 && dW) return api_fail(MLORA_ERR_UNSUPPORTED, "expert backward: an MXFP4 weight is frozen, dW must be NULL");
   if ((s.rows > 0 && !dY) || (want_dx && !W) || (dW && s.rows > 0 && !X))
-    return fail(MLORA_ERR_INVALID_ARG, "expert backward: dY, W (for dX) and X (for dW) must be non-NULL");
+    return api_fail(MLORA_ERR_INVALID_ARG, "expert backward: dY, W (for dX) and X (for dW) must be non-NULL");
   for (const void* p : {dY, X, W, (const void*)dX, (const void*)dW})
-    if (!aligned(p, 16)) return fail(MLORA_ERR_INVALID_ARG, "expert backward: device pointers must be 16-byte aligned");
+    if (!api_aligned(p, 16)) return api_fail(MLORA_ERR_INVALID_ARG, "expert backward: device pointers must be 16-byte aligned");
 
   hipStream_t cs = static_cast<hipStream_t>(stream);
   const bool f32 = s.dtype == MLORA_FP32, nk = s.w_layout == MLORA_W0_NK;
@@ -249,7 +232,7 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
       const uint8_t* codes = static_cast<const uint8_t*>(W);
       mlora::launch_dequant_mx4(true, codes, codes + s.n_experts * (wn / 2), s.d_in, s.n_experts * s.d_out,
                                 static_cast<uint16_t*>(workspace), cs);
-      st = launched();
+      st = api_launched();
       if (st != MLORA_OK) return st;
       a.B = static_cast<const uint8_t*>(workspace);
     }
@@ -263,7 +246,7 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
     a.ldb = nk ? s.d_in : s.d_out;
     a.b_expert = wn * esz;
     mlora::launch_expert_rows(f32 ? mlora::ExpertForm::kF32 : mlora::ExpertForm::kBf16, !nk, a, cs);
-    st = launched();
+    st = api_launched();
     if (st != MLORA_OK) return st;
   }
   if (dW && !(s.rows == 0 && s.grad_accumulate)) {
@@ -284,7 +267,7 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
     a.chunk = (int32_t)mlora::dw_chunk(f32, s.rows, s.n_experts, s.d_in, s.d_out);
     a.part = static_cast<float*>(workspace);
     mlora::launch_expert_dw(f32, a, cs);
-    st = launched();
+    st = api_launched();
     if (st != MLORA_OK) return st;
   }
   return MLORA_OK;
@@ -292,24 +275,24 @@ mlora_status mlora_expert_backward(const mlora_expert_shape* shape, const void* 
 
 mlora_status mlora_microscale_quantize(const void* X, mlora_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
                                        int32_t down, void* q, void* values, void* stream) {
-  if (dtype != MLORA_BF16 && dtype != MLORA_FP32) return fail(MLORA_ERR_INVALID_ARG, "quantize: unknown dtype");
-  if (down != 0 && down != 1) return fail(MLORA_ERR_INVALID_ARG, "quantize: down must be 0 or 1");
+  if (dtype != MLORA_BF16 && dtype != MLORA_FP32) return api_fail(MLORA_ERR_INVALID_ARG, "quantize: unknown dtype");
+  if (down != 0 && down != 1) return api_fail(MLORA_ERR_INVALID_ARG, "quantize: down must be 0 or 1");
   const int64_t unit = dtype == MLORA_BF16 ? 8 : 4;
   if (rows < 0 || cols <= 0 || ld < cols || ld % unit)
-    return fail(MLORA_ERR_INVALID_ARG, "quantize: rows >= 0, cols > 0, ld >= cols and a multiple of 8 (bf16) or 4 (fp32)");
+    return api_fail(MLORA_ERR_INVALID_ARG, "quantize: rows >= 0, cols > 0, ld >= cols and a multiple of 8 (bf16) or 4 (fp32)");
   if (down ? (rows % 32 || cols % 8) : cols % 32 != 0)
-    return fail(MLORA_ERR_INVALID_ARG,
+    return api_fail(MLORA_ERR_INVALID_ARG,
                 "quantize: cols must be a multiple of 32, or with down rows of 32 and cols of 8");
   if (cols > MLORA_MAX_EXPERT_DIM || rows > (kMaxGrid * 256) / (cols / 8))
-    return fail(MLORA_ERR_UNSUPPORTED, "quantize: matrix too large for one launch");
+    return api_fail(MLORA_ERR_UNSUPPORTED, "quantize: matrix too large for one launch");
   if (rows == 0) return MLORA_OK;
-  if (!X || !q) return fail(MLORA_ERR_INVALID_ARG, "quantize: X and q must be non-NULL");
-  if (!aligned(X, 16) || !aligned(q, 16) || !aligned(values, 16))
-    return fail(MLORA_ERR_INVALID_ARG, "quantize: device pointers must be 16-byte aligned");
+  if (!X || !q) return api_fail(MLORA_ERR_INVALID_ARG, "quantize: X and q must be non-NULL");
+  if (!api_aligned(X, 16) || !api_aligned(q, 16) || !api_aligned(values, 16))
+    return api_fail(MLORA_ERR_INVALID_ARG, "quantize: device pointers must be 16-byte aligned");
   uint8_t* codes = static_cast<uint8_t*>(q);
   mlora::launch_quant_mx4(dtype == MLORA_FP32, down != 0, X, rows, cols, ld, codes, codes + rows * (cols / 2), values,
                           static_cast<hipStream_t>(stream));
-  return launched();
+  return api_launched();
 }
 
 }  // extern "C"

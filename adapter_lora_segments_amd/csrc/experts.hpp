@@ -5,14 +5,10 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <string>
 
 #include "../../include/mlora.h"
 
 namespace mlora {
-
-// The message mlora_last_error() returns on this thread (api.cpp).
-void set_last_error(const std::string& msg);
 
 // ---------------- row grouping ----------------
 

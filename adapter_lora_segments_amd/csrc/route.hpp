@@ -22,9 +22,6 @@ struct RouteArgs {
   float scale;
 };
 
-// Experts a row's lanes hold at most.
-constexpr int kRouteMaxExperts = MLORA_MAX_EXPERTS;
-
 void launch_route(bool f32, const RouteArgs& a, hipStream_t s);
 void launch_route_backward(bool f32, const RouteArgs& a, hipStream_t s);
 
