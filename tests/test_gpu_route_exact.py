@@ -147,3 +147,35 @@ def test_renormalised_softmax_of_a_row_that_is_not_finite(rows):
     want = torch.zeros(16)
     want[:3] = torch.tensor([2 / 3, -1 / 3, -1 / 3])
     assert torch.allclose(d.cpu(), want.expand(rows, 16), rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("E,k", [(16, 13), (30, 30), (64, 33), (100, 17), (128, 64), (200, 40), (256, 64), (400, 33), (512, 64)])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_more_slots_than_lanes(E, k, renorm, score):
+    """Many rows with more chosen experts than a row has lanes, against the oracle and
+    against calls of few rows, which have a lane for every slot."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    say(f"more slots than lanes {E} {k} {score} {renorm}")
+    rows = 1030
+    r = Router(E, k, score=score, renormalize=renorm, scale=1.3)
+    for dt in ("bf16", "fp32"):
+        g = torch.Generator().manual_seed(E)
+        x = torch.randn(rows, E, generator=g)
+        x[5, k // 2:] = -np.inf                          # fewer experts than slots
+        x = x.to(_t(dt)).cuda()
+        ids, w = r.route(x)
+        some = [0, 5, 17, 700, rows - 1]
+        want, ww = orc.route(host(x)[some], k, score=score, renorm=renorm, scale=1.3)
+        assert np.array_equal(ids.cpu().numpy()[some], want)
+        assert (np.abs(host(w)[some] - ww) <= 2.0 ** -24 * np.abs(ww) * (1 + 2.0 ** -20) + 2.0 ** -150).all()
+        i2, w2 = r.route(x[:1024])
+        assert torch.equal(i2, ids[:1024]) and torch.equal(w2, w[:1024])
+        dw = torch.randn(rows, k, generator=g).cuda()
+        d = r.backward(x, ids, dw)
+        want, _, terms = orc.route_backward(host(x)[some], ids.cpu().numpy()[some], host(dw)[some], score, renorm, 1.3)
+        # (up to k + 9 = 73 operations of 2^-53 on either side: 2^-45)
+        bound = (HALF[dt] + 2.0 ** -24) * np.abs(want) + 2.0 ** -45 * terms + 2.0 ** -140
+        assert (np.abs(host(d)[some] - want) <= bound).all()
+        assert torch.equal(r.backward(x[:1024], ids[:1024], dw[:1024]), d[:1024])
