@@ -11,7 +11,8 @@
 // saves the shift of a word's first codes, loses five and takes as long but for 1%).
 // A product has 13 bits, so the sums are exact, and weights that are zero (c = z)
 // give zeros, where a group's activations differ by no more than 2^(11 - log2 group)
-// in size; over 4096 normal ones a column of zeros is off by 6e-5 s at most (5e-4).
+// in size; over 4096 normal ones a column of zeros is off by 6e-5 s at most (5e-4
+// with 1 + c / 128).
 #include "expert_common.hpp"
 #include "affine_choice.hpp"
 
@@ -167,12 +168,15 @@ __global__ __launch_bounds__(256) void k_affine_decode(const uint32_t* codes, co
 // column, so a group's scale and zero point are the lane's own.  With groups
 // under 128 the words of a piece are exchanged between the lane groups, so that
 // a step's 32 inputs lie in one group.
-// What bounds it: one round of loads, decoded when they come (vector instructions
-// busy 30 to 40%, matrix ones 9%, HBM half).  K = 4096: 1 row, N = 14336 10.0 us
-// (3.1 TB/s), 16 rows 12.5; 32 rows over 8 experts, N = 4096, groups of 64 21.8
-// us (3.5 TB/s).  Asking for the next four pieces before these are multiplied
-// did not gain (more registers, fewer waves), nor did weights before activations
-// (10.6 us).
+// What bounds it: up to K = 4096 one round of loads, decoded when they come (vector
+// instructions busy 30 to 40%, matrix ones 8%, HBM half): 1 row, N = 14336 9.6 us
+// (3.3 TB/s), 16 rows 12.2; 32 rows over 8 experts, N = 4096, groups of 64 22 us
+// (3.4 TB/s; 512 workgroups, two a CU, at once).  Weights before activations were
+// slower (10.6 us for the row).  Over longer inputs a wave takes one round after
+// the other, and where N is short as well few workgroups do (K = 14336, N = 4096: 1
+// row 10.4 us, 16 rows 17, 64 rows 32, the weights' bytes 6).  Asking for the
+// next four pieces before these are multiplied was measured at K = 4096 only, where
+// there are none: there it costs registers and gains nothing.
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
 template <int GROUP, int RB, int NB, int CS>

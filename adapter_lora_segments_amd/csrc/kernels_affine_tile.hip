@@ -13,16 +13,17 @@
 // 8 u + 4 h + q of the activations make one matrix instruction's 16 inputs.
 // A block of 32 lies in one group, so its scale is the lane's own.
 //
-// Bound by issue: over a full chip (1024 tiles of 128 rows) matrix instructions
-// are busy 45% of the cycles and vector ones, mostly decoding at 2.5 a weight,
-// another 44%, and the two waves of a SIMD hardly overlap them.  0.9 PF in tiles
-// of 128 rows and 0.76 PF in tiles of 64.  Tiles of 128 x 256, with half the LDS
-// reads a product, and of 96 x 128 were no faster where they fit (2048 rows over 8
-// experts 74 and 95 us, 4096 over 32 64 and 63).
+// What bounds it, from copies of the kernel that leave a part out: at 128 rows the
+// stores of the activations to LDS (47 -> 39 us without them; without decoding no
+// gain), at 64 rows decoding (55 -> 42 us without), which takes 2.5 vector
+// instructions a weight whatever the rows.  Over a full chip (1024 tiles of 128 rows)
+// matrix instructions are busy 45% of the cycles and vector ones 44%.  0.9 PF in
+// tiles of 128 rows and 0.76 PF in tiles of 64.  Tiles of 128 x 256, with half the
+// LDS reads a product, and of 96 x 128 were no faster where they fit (2048 rows over
+// 8 experts 74 and 95 us, 4096 over 32 64 and 63).
 // 4096 rows over 32 experts, 4096 -> 1024 66 us (640 tiles of 64 rows, a fifth
-// of them padding); 2048 rows over 8 experts, 4096 -> 4096 76 us (0.9 PF); 64
-// rows, 4096 -> 14336 25 us.  In copies of the kernel: without the stores to LDS
-// 47 -> 39 us, without decoding 55 -> 42 (64-row tiles) and no gain (128).
+// of them padding); 2048 rows over 8 experts, 4096 -> 4096 76 to 84 us (0.8 to 0.9
+// PF); 128 rows, 4096 -> 14336 26 us, 200 rows 39.
 #include "affine_choice.hpp"
 #include "expert_common.hpp"
 

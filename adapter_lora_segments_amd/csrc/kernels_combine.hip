@@ -91,7 +91,9 @@ __global__ __launch_bounds__(kThreads) void k_combine(CombineArgs a, int lanes, 
 // tokens and slots.  7681 tokens of 2 rows of 4104 in bf16 55 us (5.7 TB/s), of 8
 // rows of 4096 (16384 tokens) 400 us (5.7 TB/s), 35 tokens of 8 rows of 8072 in
 // fp32 8 us; all slots of a token by one wave took 64, 490 and 64 us: fewer
-// loads in flight, since a store may be to what a later load reads.
+// loads in flight, since a store may be to what a later load reads.  Where no dot
+// product is wanted (dweights NULL, a dropped slot) dout stands in for Y and is read
+// twice, the second time from the caches.
 template <bool F32, int U>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(CombineArgs a, int lanes) {
   constexpr int N = Piece<F32>::N;

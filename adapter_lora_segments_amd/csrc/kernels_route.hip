@@ -13,9 +13,12 @@
 // Bound by instructions, not by the logits' bytes: 32768 rows of 256, sigmoid, 8
 // of 256 out of 4 of 8 groups, fp32 take 21.9 us (1.5 TB/s; 18.3 without
 // groups), of which about 24 instructions an expert are its score, 9 its key and
-// 19 sorting; 32768 rows of 64 in bf16, 2 or 8 chosen, 6.6 and 7.4 us; 16 rows of
-// 64 3.2 us, a launch.  With 32 experts a lane in place of 16 the groups' case
-// took as long (fewer exchanges, fewer waves).
+// 19 sorting; 32768 rows of 256 softmax 20.2 us, in bf16 19.7 (half the bytes: they
+// do not count); of 64 in bf16, 2 or 8 chosen, 6.6 and 7.4 us; 16 rows of 64 3.2 us,
+// a launch.  With 32 experts a lane in place of 16 the groups' case took as long
+// (fewer exchanges, fewer waves).  Over 2048 experts a lane's 64 keys and scores
+// pass its registers (256 in use, spilling to accumulation registers; one wave a
+// SIMD): 4096 rows of 4096 63 us, 0.5 TB/s.
 #include "device_common.hpp"
 #include "route.hpp"
 
@@ -470,9 +473,10 @@ __global__ __launch_bounds__(kThreads<V>) void k_route(RouteArgs a, int whole, i
 // cancels in u / S.  LDS: the row's gradient [E]; dense, the sums of dw until the
 // scores are there, without the scale: of an expert named once that is dw itself, so
 // that dw - sum_j dw_j u_j, which cancels where one score is nearly 1, starts from no
-// rounded number.  16384 rows of 64 in bf16 6.8
-// us dense and 5.1 not (the chosen slots' serial work), of 256 in fp32, sigmoid,
-// 9.3 us (3.6 TB/s).
+// rounded number.  Dense, 16384 rows of 64 in bf16 6.3 us, of 256 16.2 (1 TB/s: the
+// 64-bit exponentials of every expert), in fp32 18.0; not dense 4.8, 8.2 and 9.6 (the
+// chosen slots' serial work and stores, 16.8 MB at 1.8 TB/s in the last), sigmoid of
+// 256 in fp32 8.5 to 9.4 us.
 template <class T, int L, int V, bool DENSE, bool ONE>
 __global__ __launch_bounds__(kThreads<V>) void k_route_backward(RouteArgs a, int whole) {
   extern __shared__ float grad[];
