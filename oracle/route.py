@@ -9,7 +9,8 @@ float32 plus the float32 bias; experts at -infinity (logit or c) are never
 chosen; with top_groups < groups, the groups of the largest group score (largest
 c, or the sum of the two largest in float32) are kept, equal scores to the
 lowest; ids = the k largest c, falling, equal ones to the lowest, NaN first, -1
-where none is left; weights = scale s (/ the sum of the chosen s).
+where none is left; weights = scale s (/ the sum of the chosen s).  (In float64:
+softmax scores below e^-700, which only a bias chooses, are not this oracle's.)
 """
 from __future__ import annotations
 
