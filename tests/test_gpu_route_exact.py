@@ -179,3 +179,32 @@ def test_more_slots_than_lanes(E, k, renorm, score):
         bound = (HALF[dt] + 2.0 ** -24) * np.abs(want) + 2.0 ** -45 * terms + 2.0 ** -140
         assert (np.abs(host(d)[some] - want) <= bound).all()
         assert torch.equal(r.backward(x[:1024], ids[:1024], dw[:1024]), d[:1024])
+
+
+@pytest.mark.parametrize("rows", [9, 1100])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_sigmoid_gradient_of_saturated_scores(dt, renorm, rows):
+    """Logits from 5 to 80, where 1 - s is e^-logit, which a rounded s no longer holds:
+    s (1 - s) du with 1 - s = 1 / (1 + e^logit).  Tolerances as above, the terms that
+    cancel times 1 - s."""
+    import torch
+    from adapter_lora_segments_amd import Router
+    E, k = 16, 4
+    g = torch.Generator().manual_seed(rows)
+    x = (torch.rand(rows, E, generator=g) * 75 + 5).to(_t(dt)).cuda()
+    r = Router(E, k, score="sigmoid", renormalize=renorm, scale=1.3)
+    ids, _ = r.route(x)
+    dw = torch.randn(rows, k, generator=g).cuda()
+    at, h = ids.cpu().numpy().astype(np.int64), host(dw)
+    l = np.take_along_axis(host(x), at, axis=1)
+    s, rest = 1 / (1 + np.exp(-l)), 1 / (1 + np.exp(l))
+    scale = float(np.float32(1.3))
+    p = s / s.sum(axis=1, keepdims=True) if renorm else s
+    du = h - (h * p).sum(axis=1, keepdims=True) if renorm else h
+    want, terms = np.zeros((rows, E)), np.zeros((rows, E))
+    np.put_along_axis(want, at, scale * p * rest * du, axis=1)
+    np.put_along_axis(terms, at, scale * p * rest * 2 * np.abs(h).sum(axis=1, keepdims=True), axis=1)
+    bound = (HALF[dt] + 2.0 ** -24) * np.abs(want) + 2.0 ** -47 * terms + 2.0 ** -140
+    err = np.abs(host(r.backward(x, ids, dw)) - want)
+    assert (err <= bound).all(), (err / bound).max()
